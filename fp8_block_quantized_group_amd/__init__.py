@@ -43,6 +43,24 @@ class _Problem(ctypes.Structure):
         ("act_limit", ctypes.c_float)]
 
 
+class _Router(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_tokens", "num_experts", "top_k", "dtype", "score", "num_groups", "topk_groups",
+        "group_top", "renormalize")] + [("scale", ctypes.c_float)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_tokens", "hidden", "num_experts", "top_k", "dtype")]
+
+
+class _BlockNorm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_tokens", "hidden", "dtype", "weight_dtype", "post_norm", "gate",
+        "gate_sigmoid")] + [(n, ctypes.c_float) for n in (
+            "eps", "residual_scale", "weight_offset")]
+
+
 class _Eplb(ctypes.Structure):
     _fields_ = [("logical_to_physical", ctypes.c_void_p), ("map_stride", ctypes.c_int32),
                 ("replica_count", ctypes.c_void_p), ("num_logical", ctypes.c_int32),
@@ -71,7 +89,10 @@ EXPORTS = ("moe_routing_sizes", "moe_stage_workspace_size", "moe_workspace_size"
            "moe_grouped_gemm_w2", "moe_topk_reduce", "moe_align_capacity",
            "moe_align_block_size", "moe_grouped_gemm_w13_act_indexed",
            "moe_grouped_gemm_w2_indexed", "moe_fused_mul_sum", "moe_forward",
-           "moe_forward_static", "moe_last_error")
+           "moe_forward_static", "moe_last_error",
+           "moe_router_topk", "moe_router_topk_backward", "moe_permute_workspace_size",
+           "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
+           "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward")
 
 _lib = None
 
@@ -108,6 +129,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_fused_mul_sum.argtypes = [P(_Problem), V, V, V, V, V]
     lib.moe_forward.argtypes = [P(_Problem), V, V, V, V, V, P(_Eplb), V, V, V, V, V, V, S, V]
     lib.moe_forward_static.argtypes = [P(_Problem), V, V, V, V, V, P(_Eplb), V, V, V, V, V, V]
+    lib.moe_router_topk.argtypes = [P(_Router)] + [V] * 6
+    lib.moe_router_topk_backward.argtypes = [P(_Router)] + [V] * 5
+    lib.moe_permute_workspace_size.argtypes = [P(_Rows), P(S)]
+    lib.moe_permute.argtypes = [P(_Rows)] + [V] * 8 + [S, V]
+    lib.moe_permute_backward.argtypes = [P(_Rows)] + [V] * 4
+    lib.moe_unpermute.argtypes = [P(_Rows)] + [V] * 5
+    lib.moe_unpermute_backward.argtypes = [P(_Rows)] + [V] * 7
+    lib.moe_block_norm.argtypes = [P(_BlockNorm)] + [V] * 8
+    lib.moe_block_norm_workspace_size.argtypes = [P(_BlockNorm), P(S)]
+    lib.moe_block_norm_backward.argtypes = [P(_BlockNorm)] + [V] * 13 + [S, V]
     lib.moe_last_error.argtypes = []
     for name in EXPORTS:
         fn = getattr(lib, name)
@@ -394,3 +425,280 @@ class MoeLayer:
         forward(self.p, hidden, topk_ids, topk_weights, self.w13, self.w13_sf, self.w2,
                 self.w2_sf, out, self.ws, is_padding, expert_num_tokens, eplb)
         return out
+
+
+# ---- around the layer: router, sorted rows, block norms ----------------------
+# Unlike the layer's calls these check shapes, types and devices here, and run
+# on the tensors' device, on its current stream, whatever device is current.
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}     # moe_dtype_t
+SCORES = ("softmax", "sigmoid")                                        # moe_score_t
+GATES = ("none", "token", "channel", "full")                           # moe_gate_t
+
+
+def _choice(value, names, what: str) -> int:
+    if value not in names:
+        raise ValueError(f"{what} must be one of {tuple(names)}, got {value!r}")
+    return names[value] if isinstance(names, dict) else names.index(value)
+
+
+class _Descriptor:
+    """A frozen dataclass whose C struct is made once."""
+
+    def __post_init__(self):
+        object.__setattr__(self, "_c", self._struct())
+        object.__setattr__(self, "_ref", ctypes.byref(self._c))
+
+
+@dataclass(frozen=True)
+class Router(_Descriptor):
+    """moe_router_t: how a token's experts are chosen from its logits."""
+    num_tokens: int
+    num_experts: int
+    top_k: int
+    score: str = "softmax"                  # "softmax" | "sigmoid"
+    num_groups: int = 1
+    topk_groups: int = 1
+    group_top: int = 1
+    renormalize: bool = True
+    scale: float = 1.0
+    dtype: torch.dtype = torch.float32      # of the logits
+
+    def _struct(self):
+        return _Router(self.num_tokens, self.num_experts, self.top_k,
+                       _choice(self.dtype, _DTYPES, "dtype"),
+                       _choice(self.score, SCORES, "score"), self.num_groups,
+                       self.topk_groups, self.group_top, int(self.renormalize), self.scale)
+
+
+@dataclass(frozen=True)
+class ExpertRows(_Descriptor):
+    """moe_rows_t: token rows sorted by expert."""
+    num_tokens: int
+    hidden: int
+    num_experts: int
+    top_k: int
+    dtype: torch.dtype = torch.bfloat16
+
+    def _struct(self):
+        return _Rows(self.num_tokens, self.hidden, self.num_experts, self.top_k,
+                     _choice(self.dtype, _DTYPES, "dtype"))
+
+
+@dataclass(frozen=True)
+class BlockNorm(_Descriptor):
+    """moe_block_norm_t: the norms before and after a block with its gate and
+    residual scale."""
+    num_tokens: int
+    hidden: int
+    dtype: torch.dtype = torch.bfloat16
+    weight_dtype: Optional[torch.dtype] = None      # None: dtype
+    post_norm: bool = False
+    gate: str = "none"                              # "none" | "token" | "channel" | "full"
+    gate_sigmoid: bool = False
+    eps: float = 1e-6
+    residual_scale: float = 1.0
+    weight_offset: float = 0.0
+
+    def _struct(self):
+        return _BlockNorm(self.num_tokens, self.hidden, _choice(self.dtype, _DTYPES, "dtype"),
+                          _choice(self.weight_dtype or self.dtype, _DTYPES, "weight_dtype"),
+                          int(self.post_norm), _choice(self.gate, GATES, "gate"),
+                          int(self.gate_sigmoid), self.eps, self.residual_scale,
+                          self.weight_offset)
+
+    @property
+    def gate_shape(self):
+        return {"none": None, "token": (self.num_tokens,), "channel": (self.hidden,),
+                "full": (self.num_tokens, self.hidden)}[self.gate]
+
+
+def _arg(t, name: str, dtype, shape, device):
+    """The address of an argument, checked; None for one that is not given."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device(t: torch.Tensor, name: str) -> torch.device:
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU, got {t.device}")
+    return t.device
+
+
+def _scratch(ws: Optional[torch.Tensor], device):
+    if ws is None:
+        return None, 0
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _run(fn, device: torch.device, *args):
+    """fn(*args, stream) on the device and its current stream."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def router_topk(r: Router, logits, topk_ids, topk_weights, bias=None, is_padding=None):
+    """moe_router_topk: fills topk_ids int32 and topk_weights fp32 [T, top_k]
+    from logits [T, E]."""
+    d = _device(logits, "logits")
+    T, E, k = r.num_tokens, r.num_experts, r.top_k
+    _run(load_library().moe_router_topk, d, r._ref,
+         _arg(logits, "logits", r.dtype, (T, E), d),
+         _arg(bias, "bias", torch.float32, (E,), d),
+         _arg(is_padding, "is_padding", torch.uint8, (T,), d),
+         _arg(topk_ids, "topk_ids", torch.int32, (T, k), d),
+         _arg(topk_weights, "topk_weights", torch.float32, (T, k), d))
+
+
+def router_topk_backward(r: Router, logits, topk_ids, grad_topk_weights, grad_logits):
+    """moe_router_topk_backward: fills grad_logits [T, E]."""
+    d = _device(logits, "logits")
+    T, E, k = r.num_tokens, r.num_experts, r.top_k
+    _run(load_library().moe_router_topk_backward, d, r._ref,
+         _arg(logits, "logits", r.dtype, (T, E), d),
+         _arg(topk_ids, "topk_ids", torch.int32, (T, k), d),
+         _arg(grad_topk_weights, "grad_topk_weights", torch.float32, (T, k), d),
+         _arg(grad_logits, "grad_logits", r.dtype, (T, E), d))
+
+
+def permute_workspace_size(p: ExpertRows) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().moe_permute_workspace_size(p._ref, ctypes.byref(n)))
+    return n.value
+
+
+def alloc_permute_workspace(p: ExpertRows, device="cuda") -> torch.Tensor:
+    return torch.empty(permute_workspace_size(p), dtype=torch.uint8, device=device)
+
+
+def alloc_permute_outputs(p: ExpertRows, device="cuda") -> dict:
+    """The outputs and the workspace of permute, by its parameters' names."""
+    n = p.num_tokens * p.top_k
+    i32 = dict(dtype=torch.int32, device=device)
+    return {"rows": torch.empty((n, p.hidden), dtype=p.dtype, device=device),
+            "expert_offsets": torch.empty(p.num_experts + 1, **i32),
+            "slot_row": torch.empty((p.num_tokens, p.top_k), **i32),
+            "row_slot": torch.empty(n, **i32), "ws": alloc_permute_workspace(p, device)}
+
+
+def permute(p: ExpertRows, x, topk_ids, rows, expert_offsets, slot_row, row_slot, ws,
+            is_padding=None):
+    """moe_permute: the tokens' rows sorted by expert."""
+    d = _device(x, "x")
+    T, k = p.num_tokens, p.top_k
+    wp, wn = _scratch(ws, d)
+    _run(load_library().moe_permute, d, p._ref, _arg(x, "x", p.dtype, (T, p.hidden), d),
+         _arg(topk_ids, "topk_ids", torch.int32, (T, k), d),
+         _arg(is_padding, "is_padding", torch.uint8, (T,), d),
+         _arg(rows, "rows", p.dtype, (T * k, p.hidden), d),
+         _arg(expert_offsets, "expert_offsets", torch.int32, (p.num_experts + 1,), d),
+         _arg(slot_row, "slot_row", torch.int32, (T, k), d),
+         _arg(row_slot, "row_slot", torch.int32, (T * k,), d), wp, wn)
+
+
+def permute_backward(p: ExpertRows, grad_rows, slot_row, grad_x):
+    """moe_permute_backward: the sum of every token's rows."""
+    d = _device(grad_rows, "grad_rows")
+    T, k = p.num_tokens, p.top_k
+    _run(load_library().moe_permute_backward, d, p._ref,
+         _arg(grad_rows, "grad_rows", p.dtype, (T * k, p.hidden), d),
+         _arg(slot_row, "slot_row", torch.int32, (T, k), d),
+         _arg(grad_x, "grad_x", p.dtype, (T, p.hidden), d))
+
+
+def unpermute(p: ExpertRows, rows, slot_row, topk_weights, out):
+    """moe_unpermute: the weighted sum of every token's rows (weights None: 1)."""
+    d = _device(rows, "rows")
+    T, k = p.num_tokens, p.top_k
+    _run(load_library().moe_unpermute, d, p._ref,
+         _arg(rows, "rows", p.dtype, (T * k, p.hidden), d),
+         _arg(slot_row, "slot_row", torch.int32, (T, k), d),
+         _arg(topk_weights, "topk_weights", torch.float32, (T, k), d),
+         _arg(out, "out", p.dtype, (T, p.hidden), d))
+
+
+def unpermute_backward(p: ExpertRows, grad_out, rows, slot_row, topk_weights, grad_rows,
+                       grad_topk_weights):
+    """moe_unpermute_backward: the gradients of the rows and of the weights."""
+    d = _device(grad_out, "grad_out")
+    T, k = p.num_tokens, p.top_k
+    _run(load_library().moe_unpermute_backward, d, p._ref,
+         _arg(grad_out, "grad_out", p.dtype, (T, p.hidden), d),
+         _arg(rows, "rows", p.dtype, (T * k, p.hidden), d),
+         _arg(slot_row, "slot_row", torch.int32, (T, k), d),
+         _arg(topk_weights, "topk_weights", torch.float32, (T, k), d),
+         _arg(grad_rows, "grad_rows", p.dtype, (T * k, p.hidden), d),
+         _arg(grad_topk_weights, "grad_topk_weights", torch.float32, (T, k), d))
+
+
+def block_norm_workspace_size(p: BlockNorm) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().moe_block_norm_workspace_size(p._ref, ctypes.byref(n)))
+    return n.value
+
+
+def alloc_block_norm_workspace(p: BlockNorm, device="cuda") -> torch.Tensor:
+    """Scratch of block_norm_backward when it returns a weight's or a
+    per-channel gate's gradient."""
+    return torch.empty(block_norm_workspace_size(p), dtype=torch.uint8, device=device)
+
+
+def _block_args(p: BlockNorm, y, post_weight, gate, pre_weight, d):
+    wt = p.weight_dtype or p.dtype
+    H = p.hidden
+    return (_arg(y, "y", p.dtype, (p.num_tokens, H), d),
+            _arg(post_weight, "post_weight", wt, (H,), d),
+            _arg(gate, "gate", p.dtype, p.gate_shape or (), d),
+            _arg(pre_weight, "pre_weight", wt, (H,), d))
+
+
+def block_norm(p: BlockNorm, residual, normed=None, y=None, residual_out=None,
+               pre_weight=None, post_weight=None, gate=None):
+    """moe_block_norm: fills residual_out = residual + scale * gate * n(y) and
+    normed, its norm; y None: normed is the norm of residual."""
+    d = _device(residual, "residual")
+    shape = (p.num_tokens, p.hidden)
+    _run(load_library().moe_block_norm, d, p._ref,
+         _arg(residual, "residual", p.dtype, shape, d),
+         *_block_args(p, y, post_weight, gate, pre_weight, d),
+         _arg(residual_out, "residual_out", p.dtype, shape, d),
+         _arg(normed, "normed", p.dtype, shape, d))
+
+
+def block_norm_backward(p: BlockNorm, residual_out, grad_normed, grad_residual, y=None,
+                        grad_residual_out=None, pre_weight=None, post_weight=None, gate=None,
+                        grad_y=None, grad_pre_weight=None, grad_post_weight=None,
+                        grad_gate=None, ws="auto"):
+    """moe_block_norm_backward at the stored stream residual_out (y None: the
+    forward call's residual); ws: "auto" allocates it where it is needed."""
+    d = _device(residual_out, "residual_out")
+    shape, H = (p.num_tokens, p.hidden), p.hidden
+    if isinstance(ws, str):
+        sums = (grad_pre_weight is not None or grad_post_weight is not None
+                or (grad_gate is not None and p.gate == "channel"))
+        ws = alloc_block_norm_workspace(p, d) if sums else None
+    wp, wn = _scratch(ws, d)
+    _run(load_library().moe_block_norm_backward, d, p._ref,
+         _arg(residual_out, "residual_out", p.dtype, shape, d),
+         *_block_args(p, y, post_weight, gate, pre_weight, d),
+         _arg(grad_normed, "grad_normed", p.dtype, shape, d),
+         _arg(grad_residual_out, "grad_residual_out", p.dtype, shape, d),
+         _arg(grad_residual, "grad_residual", p.dtype, shape, d),
+         _arg(grad_y, "grad_y", p.dtype, shape, d),
+         _arg(grad_pre_weight, "grad_pre_weight", torch.float32, (H,), d),
+         _arg(grad_post_weight, "grad_post_weight", torch.float32, (H,), d),
+         _arg(grad_gate, "grad_gate", p.dtype if p.gate == "full" else torch.float32,
+              p.gate_shape or (), d), wp, wn)

@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoe_fp8.so")
 OBJ_DIR = os.path.join(ROOT, "_build")
-SOURCES = ["moe_api.hip", "quant_kernels.hip", "route_kernels.hip", "reduce_kernels.hip"]
+SOURCES = ["moe_api.hip", "quant_kernels.hip", "route_kernels.hip", "reduce_kernels.hip",
+           "block_api.hip", "router_kernels.hip", "permute_kernels.hip", "norm_kernels.hip"]
 # the grouped GEMM's scale schemes (kQuantUe8m0, kQuantF32, kQuantBf16,
 # kQuantMxfp8, kSchemeMxfp8W4)
 GEMM_SCHEMES = [0, 1, 2, 3, 4]

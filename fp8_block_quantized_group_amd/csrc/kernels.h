@@ -212,4 +212,92 @@ hipError_t launch_align(const int64_t* idx, const int32_t* slot_row, const int32
                         int32_t* sorted_ids, int32_t* expert_ids, int32_t* num_padded,
                         hipStream_t stream);
 
+// ---- the operators around the layer ------------------------------------------
+// Element types are kBf16, kF16, kF32 (row_vec.h; values match moe_dtype_t).
+
+struct RouterArgs {
+  const void* logits;          // [T, E]
+  const float* bias;           // [E] or nullptr: added for the choice only
+  const uint8_t* is_padding;   // [T] or nullptr
+  int32_t* ids;                // [T, k]
+  float* weights;              // [T, k]
+  int64_t T;
+  int E, k;
+  int groups, topk_groups, group_top;
+  bool sigmoid, renormalize;
+  float scale;
+};
+hipError_t launch_router_topk(const RouterArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_router_grad(const RouterArgs& a, const int32_t* ids, const float* grad_w,
+                              void* grad_logits, int dtype, hipStream_t stream);
+
+// slots per block of the sort's counting and ranking kernels
+constexpr int kSortChunk = 1024;
+struct SortArgs {
+  const int32_t* ids;          // [slots]
+  const uint8_t* is_padding;   // [slots / k] or nullptr
+  int64_t slots;
+  int k, E;
+  int32_t* hist;               // [chunks, E] scratch
+  int32_t* expert_offsets;     // [E + 1]
+  int32_t* slot_row;           // [slots], -1 unrouted
+  int32_t* row_slot;           // [slots], entries past the routed rows not written
+};
+hipError_t launch_sort(const SortArgs& a, hipStream_t stream);
+
+struct RowsArgs {
+  const uint8_t* in;           // tokens [T, H] or expert rows [slots, H]
+  uint8_t* out;                // the other of the two
+  const int32_t* slot_row;     // [T, k]; entries outside [0, slots) are unrouted
+  const float* weights;        // [T, k] or nullptr (all 1)
+  int64_t T, slots;
+  int k, H;
+};
+hipError_t launch_permute_rows(const RowsArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_combine_rows(const RowsArgs& a, int dtype, hipStream_t stream);
+// a.in: the gradient of the tokens; a.out: of the rows
+hipError_t launch_combine_grad(const RowsArgs& a, const void* rows, float* grad_w, int dtype,
+                               hipStream_t stream);
+
+// values match moe_gate_t
+constexpr int kGateNone = 0, kGateToken = 1, kGateChannel = 2, kGateFull = 3;
+struct NormArgs {
+  const uint8_t* r;            // [T, H] residual stream
+  const uint8_t* y;            // [T, H] the block's output or nullptr
+  uint8_t* r_out;              // [T, H], with y
+  uint8_t* h;                  // [T, H] or nullptr
+  const void* w_post;          // [H] or nullptr (ones)
+  const void* w_pre;           // [H] or nullptr (ones)
+  const uint8_t* gate;
+  int64_t T;
+  int H, gate_kind;
+  bool post, gate_sigmoid;
+  float eps, alpha, offset;
+};
+hipError_t launch_norm(const NormArgs& a, int dtype, bool w32, hipStream_t stream);
+
+// blocks of the norm gradient at most, each walking its rows
+constexpr int kNormGradBlocks = 512;
+struct NormGradArgs {
+  const uint8_t* x;            // [T, H] the stored residual stream
+  const uint8_t* y;            // [T, H] or nullptr
+  const uint8_t* dh;           // [T, H] or nullptr (0)
+  const uint8_t* dr_in;        // [T, H] or nullptr (0)
+  uint8_t* dr;                 // [T, H]
+  uint8_t* dy;                 // [T, H], with y
+  const void* w_post;
+  const void* w_pre;
+  const uint8_t* gate;
+  void* d_gate;                // token: fp32 [T]; full: [T, H]; else unused
+  float* part;                 // [3][parts][H] column sums
+  int want;                    // which of them: 1 w_pre, 2 w_post, 4 channel gate
+  int64_t T;
+  int H, gate_kind;
+  bool post, gate_sigmoid;
+  float eps, alpha, offset;
+};
+int norm_grad_parts(int64_t T, int H, int dtype);
+hipError_t launch_norm_grad(const NormGradArgs& a, int dtype, bool w32, float* g_pre,
+                            float* g_post, float* g_gate, hipStream_t stream);
+
 }  // namespace moe

@@ -21,6 +21,7 @@
 #include <string>
 
 #include "../../include/moe_fp8.h"
+#include "api_common.h"
 #include "kernels.h"
 
 // Workspace of moe_forward_static: one copy per GPU, in the library's code
@@ -30,11 +31,10 @@
 // (static_scratch_for_current_device below).
 static __device__ __align__(256) uint8_t scratch[MOE_STATIC_SCRATCH_BYTES];
 
-namespace {
+namespace moe {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
-moe_status_t fail(moe_status_t code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 moe_status_t fail(moe_status_t code, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -55,10 +55,25 @@ moe_status_t launch_status(hipError_t err, const char* what) {
   return fail(MOE_ERR_LAUNCH, "%s: kernel launch failed: %s", what, hipGetErrorString(err));
 }
 
-bool aligned(const void* ptr, size_t a) { return ((uintptr_t)ptr % a) == 0; }
+static bool aligned(const void* ptr, size_t a) { return ((uintptr_t)ptr % a) == 0; }
 
-constexpr size_t kAlign = 256;
-size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+moe_status_t check_ptr(const void* ptr, const char* name, size_t align) {
+  if (ptr == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned(ptr, align))
+    return fail(MOE_ERR_INVALID_ARG, "%s must be %zu-byte aligned", name, align);
+  return MOE_OK;
+}
+
+}  // namespace moe
+
+namespace {
+
+using moe::check_ptr;
+using moe::fail;
+using moe::kAlign;
+using moe::launch_status;
+using moe::ok;
+using moe::round_up;
 
 bool batched(const moe_problem_t* p) { return p->layout == MOE_LAYOUT_BATCHED_MASKED; }
 bool indexed(const moe_problem_t* p) { return p->layout == MOE_LAYOUT_INDEXED; }
@@ -363,19 +378,6 @@ Workspace carve(const Plan& pl, const moe_problem_t* p, uint8_t* base) {
   w.total = off;
   return w;
 }
-
-moe_status_t check_ptr(const void* ptr, const char* name, size_t align) {
-  if (ptr == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
-  if (!aligned(ptr, align))
-    return fail(MOE_ERR_INVALID_ARG, "%s must be %zu-byte aligned", name, align);
-  return MOE_OK;
-}
-
-#define CHECK(expr)                         \
-  do {                                      \
-    const moe_status_t _s = (expr);         \
-    if (_s != MOE_OK) return _s;            \
-  } while (0)
 
 // Activation-scale pointer: required for quantized activations, NULL for bf16.
 moe_status_t check_sf(const moe_problem_t* p, const void* sf, const char* name) {
@@ -768,7 +770,7 @@ moe_status_t check_indexed(const moe_problem_t* p, const int32_t* sorted_ids,
 
 extern "C" {
 
-const char* moe_last_error(void) { return g_last_error.c_str(); }
+const char* moe_last_error(void) { return moe::g_last_error.c_str(); }
 
 moe_status_t moe_routing_sizes(const moe_problem_t* p, moe_sizes_t* out) {
   CHECK(validate_problem(p));

@@ -1,0 +1,593 @@
+// The norms before and after a block, fused with the block's gate, its
+// residual scale and the residual add, and their gradients.
+//
+//   n  = y * rsqrt(mean(y^2) + eps) * (o + w_post)      (or n = y)
+//   r' = r + alpha * gate * n
+//   h  = r' * rsqrt(mean(r'^2) + eps) * (o + w_pre)
+//
+// A row stays in registers from its first load to its last store: BT lanes
+// hold VPT vectors each, the row sums cross the lanes of a wave by shuffles
+// and, for BT over 64, the waves through LDS.  Everything is fp32; h is made
+// from r' before r' is rounded.
+#include "kernels.h"
+#include "row_vec.h"
+
+namespace moe {
+
+namespace {
+
+// sums of M values over the BT lanes that share a row; buf: theirs, one per call
+template <int BT, int M>
+__device__ __forceinline__ void row_sums(float (&v)[M], float (*buf)[16]) {
+#pragma unroll
+  for (int m = 0; m < M; ++m) v[m] = wave_sum(v[m]);
+  if (BT == 64) return;
+  const int lane = threadIdx.x & 63, wave = (threadIdx.x % BT) >> 6;
+  if (lane == 0) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) buf[m][wave] = v[m];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < BT / 64; ++w) s += buf[m][w];
+    v[m] = s;
+  }
+}
+
+// Squares of values over about 1e19 pass fp32's range.  A row whose sum of
+// squares is above kBig is summed again with its values scaled by kShrink.
+constexpr float kBig = 1e38f;
+constexpr float kShrink = 0x1p-96f;
+
+// 1 / sqrt(mean + eps) from the sum of the squares of values scaled by f
+__device__ __forceinline__ float inv_rms(float sum, int H, float eps, float f) {
+  return f / sqrtf(sum / (float)H + eps * f * f);
+}
+
+// weights of columns [col, col + N): of the rows' type or fp32; o + w
+template <int DT, bool W32, int N>
+__device__ __forceinline__ void load_weights(const void* w, int col, int H, float o,
+                                             float (&f)[N]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = 1.0f;
+    return;
+  }
+  if (W32 && DT != kF32) {
+    float a[4], b[4];
+    const uint8_t* p = (const uint8_t*)w;
+    RowVec<kF32>::unpack(RowVec<kF32>::template load<false>(p, col, H), a);
+    RowVec<kF32>::unpack(RowVec<kF32>::template load<false>(p, col + 4, H), b);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = o + (i < 4 ? a[i & 3] : b[i & 3]);
+  } else {
+    RowVec<DT>::unpack(RowVec<DT>::template load<false>((const uint8_t*)w, col, H), f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] += o;
+  }
+}
+
+__device__ __forceinline__ float gate_value(float g, bool sigmoid) {
+  return sigmoid ? 1.0f / (1.0f + expf(-g)) : g;
+}
+
+// the row's inverse root mean square, its N * VPT values per lane given by f
+template <int BT, int VPT, int N, class F>
+__device__ __forceinline__ float row_inv_rms(F&& value, int H, float eps, float (*buf)[1][16]) {
+  float s[1] = {0.0f}, f = 1.0f, v[N];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    value(i, v);
+#pragma unroll
+    for (int c = 0; c < N; ++c) s[0] = fmaf(v[c], v[c], s[0]);
+  }
+  row_sums<BT, 1>(s, buf[0]);
+  if (s[0] > kBig) {                          // the same for every lane of the row
+    f = kShrink;
+    s[0] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      value(i, v);
+#pragma unroll
+      for (int c = 0; c < N; ++c) s[0] = fmaf(v[c] * f, v[c] * f, s[0]);
+    }
+    row_sums<BT, 1>(s, buf[1]);
+  }
+  return inv_rms(s[0], H, eps, f);
+}
+
+template <int DT, bool W32, int BT, int VPT>
+__global__ __launch_bounds__(BT == 64 ? 256 : BT) void norm_kernel(const NormArgs a) {
+  constexpr int N = RowVec<DT>::N;
+  __shared__ float buf[4][1][16];
+  const int64_t row = BT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (row >= a.T) return;                       // whole waves (BT 64) or never
+  const int first = BT == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const int H = a.H;
+  const int64_t at = row * H * RowVec<DT>::kSize;
+  u32x4_t rv[VPT], yv[VPT];
+  float x[VPT][N];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int col = (first + i * BT) * N;
+    rv[i] = RowVec<DT>::template load<true>(a.r + at, col, H);
+    if (a.y != nullptr) yv[i] = RowVec<DT>::template load<true>(a.y + at, col, H);
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) RowVec<DT>::unpack(rv[i], x[i]);
+  if (a.y != nullptr) {
+    float ys = 1.0f;
+    if (a.post)
+      ys = row_inv_rms<BT, VPT, N>([&](int i, float* v) { RowVec<DT>::unpack(yv[i], v); }, H,
+                                   a.eps, buf);
+    float gt = 1.0f;
+    if (a.gate_kind == kGateToken)
+      gt = gate_value(RowVec<DT>::load_one(a.gate, row), a.gate_sigmoid);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int col = (first + i * BT) * N;
+      if (col >= H) continue;
+      float y[N], w[N], g[N];
+      RowVec<DT>::unpack(yv[i], y);
+      load_weights<DT, W32>(a.post ? a.w_post : nullptr, col, H, a.offset, w);
+#pragma unroll
+      for (int c = 0; c < N; ++c) g[c] = gt;
+      if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull) {
+        RowVec<DT>::unpack(RowVec<DT>::template load<false>(
+                               a.gate + (a.gate_kind == kGateFull ? at : 0), col, H), g);
+#pragma unroll
+        for (int c = 0; c < N; ++c) g[c] = gate_value(g[c], a.gate_sigmoid);
+      }
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+        x[i][c] = col + c < H ? fmaf(a.alpha * g[c], y[c] * ys * w[c], x[i][c]) : 0.0f;
+      RowVec<DT>::template store<true>(a.r_out + at, col, H, RowVec<DT>::pack(x[i]));
+    }
+  }
+  if (a.h == nullptr) return;
+  const float xs = row_inv_rms<BT, VPT, N>(
+      [&](int i, float* v) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) v[c] = x[i][c];
+      },
+      H, a.eps, buf + 2);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int col = (first + i * BT) * N;
+    if (col >= H) continue;
+    float w[N], h[N];
+    load_weights<DT, W32>(a.w_pre, col, H, a.offset, w);
+#pragma unroll
+    for (int c = 0; c < N; ++c) h[c] = x[i][c] * xs * w[c];
+    RowVec<DT>::template store<true>(a.h + at, col, H, RowVec<DT>::pack(h));
+  }
+}
+
+// Gradients at the stored r' (x below).  With xs, ys the inverse root means,
+// xh = x xs and yh = y ys:
+//   D  = dr'_in + xs (dh w_pre - xh mean(dh w_pre xh))       -> grad r
+//   dn = alpha gate D,  e = dn w_post
+//   dy = ys (e - yh mean(e yh))
+//   grad w_pre += dh xh,  grad w_post += dn yh,  grad gate += alpha D n gate'
+// Each block walks rows with a stride of the grid and keeps the column sums
+// of its rows; they go to part[output][block][H] and are added up in block
+// order by grad_sum_kernel, so the result does not depend on timing.
+
+// what a column vector needs of the row's first sums
+struct GradRow {
+  float xs, xm;       // inverse root mean of x; mean(dh w_pre xh)
+  float ys;           // inverse root mean of y (1 without a post norm)
+  float gt;           // the token's gate
+};
+
+// D, e and the gate's gradient of one column vector
+template <int DT, bool W32>
+__device__ __forceinline__ void grad_columns(const NormGradArgs& a, const GradRow& r,
+                                             int64_t at, int col, const float* x,
+                                             const float* dh, const float* y, float* D,
+                                             float* dpre, float* e, float* dpost, float* dg) {
+  constexpr int N = RowVec<DT>::N;
+  float w[N];
+  load_weights<DT, W32>(a.w_pre, col, a.H, a.offset, w);
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const float xh = x[c] * r.xs;
+    dpre[c] = dh[c] * xh;
+    if (a.dh != nullptr) D[c] = fmaf(r.xs, fmaf(dh[c], w[c], -xh * r.xm), D[c]);
+  }
+  if (a.y == nullptr) return;
+  float g[N];
+#pragma unroll
+  for (int c = 0; c < N; ++c) g[c] = r.gt;
+  if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull) {
+    RowVec<DT>::unpack(RowVec<DT>::template load<false>(
+                           a.gate + (a.gate_kind == kGateFull ? at : 0), col, a.H), g);
+#pragma unroll
+    for (int c = 0; c < N; ++c) g[c] = gate_value(g[c], a.gate_sigmoid);
+  }
+  load_weights<DT, W32>(a.post ? a.w_post : nullptr, col, a.H, a.offset, w);
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const float yh = y[c] * r.ys, ad = a.alpha * D[c];
+    dg[c] = ad * (yh * w[c]);
+    if (a.gate_sigmoid) dg[c] *= g[c] * (1.0f - g[c]);
+    dpost[c] = ad * g[c] * yh;
+    e[c] = ad * g[c] * w[c];
+  }
+}
+
+// s: sums of x^2, dh w_pre x and y^2, of values scaled by fx and fy
+__device__ __forceinline__ GradRow grad_row(const NormGradArgs& a, const float (&s)[3], float fx,
+                                            float fy, float gt) {
+  GradRow r;
+  r.xs = inv_rms(s[0], a.H, a.eps, fx);
+  r.xm = r.xs / fx * (s[1] / (float)a.H);
+  r.ys = a.post ? inv_rms(s[2], a.H, a.eps, fy) : 1.0f;
+  r.gt = gt;
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ float token_gate(const NormGradArgs& a, int64_t row) {
+  return a.y != nullptr && a.gate_kind == kGateToken
+             ? gate_value(RowVec<DT>::load_one(a.gate, row), a.gate_sigmoid) : 1.0f;
+}
+
+// Rows in registers: BT lanes per row, kGradThreads / BT rows side by side
+// (one for BT above), each lane with the column sums of its VPT vectors.
+constexpr int kGradThreads = 512;
+constexpr int grad_groups(int bt) { return bt < kGradThreads ? kGradThreads / bt : 1; }
+
+template <int DT, bool W32, int BT, int VPT>
+__global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_grad_kernel(
+    const NormGradArgs a) {
+  constexpr int N = RowVec<DT>::N, G = grad_groups(BT);
+  __shared__ float buf1[2][G][3][16], buf2[2][G][2][16], buf3[2][G][3][16];
+  __shared__ float sums[G][BT * N];
+  const int sub = threadIdx.x / BT, first = threadIdx.x % BT;
+  const int64_t stride = (int64_t)gridDim.x * G;
+  const int H = a.H;
+  const bool has_y = a.y != nullptr;
+  float apre[VPT][N], apost[VPT][N], agate[VPT][N];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int c = 0; c < N; ++c) apre[i][c] = apost[i][c] = agate[i][c] = 0.0f;
+  int turn = 0;
+  // every group makes the same number of turns (the sums meet at barriers);
+  // one past the last row computes on zeros and stores nothing
+  for (int64_t row0 = (int64_t)blockIdx.x * G; row0 < a.T; row0 += stride, turn ^= 1) {
+    const int64_t row = row0 + sub;
+    const bool live = row < a.T;
+    const int h = live ? H : 0;               // columns of the row
+    const int64_t at = row * H * RowVec<DT>::kSize;
+    u32x4_t xv[VPT], hv[VPT], dv[VPT], yv[VPT];
+    const u32x4_t zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int col = (first + i * BT) * N;
+      xv[i] = RowVec<DT>::template load<true>(a.x + at, col, h);
+      hv[i] = a.dh != nullptr ? RowVec<DT>::template load<true>(a.dh + at, col, h) : zero;
+      dv[i] = a.dr_in != nullptr ? RowVec<DT>::template load<true>(a.dr_in + at, col, h) : zero;
+      yv[i] = has_y ? RowVec<DT>::template load<true>(a.y + at, col, h) : zero;
+    }
+    float s[3] = {0.0f, 0.0f, 0.0f}, fx = 1.0f, fy = 1.0f;
+    auto add_up = [&]() {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int col = (first + i * BT) * N;
+        if (col >= h) continue;
+        float x[N], dh[N], y[N], w[N];
+        RowVec<DT>::unpack(xv[i], x);
+        RowVec<DT>::unpack(hv[i], dh);
+        RowVec<DT>::unpack(yv[i], y);
+        load_weights<DT, W32>(a.w_pre, col, H, a.offset, w);
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          const float xc = x[c] * fx, yc = y[c] * fy;
+          s[0] = fmaf(xc, xc, s[0]);
+          s[1] = fmaf(dh[c] * w[c], xc, s[1]);
+          s[2] = fmaf(yc, yc, s[2]);
+        }
+      }
+    };
+    add_up();
+    row_sums<BT, 3>(s, buf1[turn][sub]);
+    bool again = s[0] > kBig || s[2] > kBig;
+    if (G > 1 && BT > 64) again = __syncthreads_or(again);   // the groups meet in row_sums
+    if (again) {
+      fx = s[0] > kBig ? kShrink : 1.0f;
+      fy = s[2] > kBig ? kShrink : 1.0f;
+      s[0] = s[1] = s[2] = 0.0f;
+      add_up();
+      row_sums<BT, 3>(s, buf3[turn][sub]);
+    }
+    const GradRow r = grad_row(a, s, fx, fy, live ? token_gate<DT>(a, row) : 0.0f);
+    float e[VPT][N], q[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int col = (first + i * BT) * N;
+#pragma unroll
+      for (int c = 0; c < N; ++c) e[i][c] = 0.0f;
+      if (col >= h) continue;
+      float x[N], dh[N], D[N], y[N], dpre[N], dpost[N], dg[N];
+      RowVec<DT>::unpack(xv[i], x);
+      RowVec<DT>::unpack(hv[i], dh);
+      RowVec<DT>::unpack(dv[i], D);
+      RowVec<DT>::unpack(yv[i], y);
+      grad_columns<DT, W32>(a, r, at, col, x, dh, y, D, dpre, e[i], dpost, dg);
+      RowVec<DT>::template store<true>(a.dr + at, col, H, RowVec<DT>::pack(D));
+#pragma unroll
+      for (int c = 0; c < N; ++c) apre[i][c] += dpre[c];
+      if (!has_y) continue;
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        apost[i][c] += dpost[c];
+        agate[i][c] += dg[c];
+        q[0] = fmaf(e[i][c], y[c] * r.ys, q[0]);
+        q[1] += dg[c];
+      }
+      if (a.gate_kind == kGateFull && a.d_gate != nullptr)
+        RowVec<DT>::template store<true>((uint8_t*)a.d_gate + at, col, H, RowVec<DT>::pack(dg));
+    }
+    if (!has_y) continue;
+    row_sums<BT, 2>(q, buf2[turn][sub]);
+    if (live && a.gate_kind == kGateToken && a.d_gate != nullptr && first == 0)
+      ((float*)a.d_gate)[row] = q[1];
+    const float ym = a.post ? q[0] / (float)H : 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int col = (first + i * BT) * N;
+      if (col >= h) continue;
+      float y[N], d[N];
+      RowVec<DT>::unpack(yv[i], y);
+#pragma unroll
+      for (int c = 0; c < N; ++c) d[c] = r.ys * fmaf(-y[c] * r.ys, ym, e[i][c]);
+      RowVec<DT>::template store<true>(a.dy + at, col, H, RowVec<DT>::pack(d));
+    }
+  }
+  // the groups' column sums, in group order, as the block's part
+#pragma unroll
+  for (int o = 0; o < 3; ++o) {
+    if (!(a.want & (1 << o))) continue;
+    float* part = a.part + ((int64_t)o * gridDim.x + blockIdx.x) * H;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float* mine = o == 0 ? apre[i] : o == 1 ? apost[i] : agate[i];
+      if (G > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < N; ++c) sums[sub][first * N + c] = mine[c];
+        __syncthreads();
+        if (sub != 0) continue;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          float v = 0.0f;
+#pragma unroll
+          for (int g = 0; g < G; ++g) v += sums[g][first * N + c];
+          mine[c] = v;
+        }
+      }
+      const int col = (first + i * BT) * N;
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+        if (col + c < H) part[col + c] = mine[c];
+    }
+  }
+}
+
+// Rows too wide for registers: one block per row, which is read three times
+// (from the caches after the first): for its first sums, for its second, and
+// to write.  The block's column sums are kept in its part itself.
+constexpr int kWideThreads = 1024;
+
+template <int DT, bool W32>
+__global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(const NormGradArgs a) {
+  constexpr int N = RowVec<DT>::N;
+  __shared__ float buf1[2][3][16], buf2[2][2][16], buf3[2][3][16];
+  const int H = a.H;
+  const bool has_y = a.y != nullptr;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
+    const int64_t at = row * H * RowVec<DT>::kSize;
+    float x[N], dh[N], D[N], y[N];
+    auto load = [&](int col) {
+      const u32x4_t zero = {0u, 0u, 0u, 0u};
+      RowVec<DT>::unpack(RowVec<DT>::template load<false>(a.x + at, col, H), x);
+      RowVec<DT>::unpack(
+          a.dh != nullptr ? RowVec<DT>::template load<false>(a.dh + at, col, H) : zero, dh);
+      RowVec<DT>::unpack(
+          a.dr_in != nullptr ? RowVec<DT>::template load<false>(a.dr_in + at, col, H) : zero, D);
+      RowVec<DT>::unpack(has_y ? RowVec<DT>::template load<false>(a.y + at, col, H) : zero, y);
+    };
+    float s[3] = {0.0f, 0.0f, 0.0f}, fx = 1.0f, fy = 1.0f;
+    auto add_up = [&]() {
+      for (int col = threadIdx.x * N; col < H; col += kWideThreads * N) {
+        float w[N];
+        load(col);
+        load_weights<DT, W32>(a.w_pre, col, H, a.offset, w);
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          const float xc = x[c] * fx, yc = y[c] * fy;
+          s[0] = fmaf(xc, xc, s[0]);
+          s[1] = fmaf(dh[c] * w[c], xc, s[1]);
+          s[2] = fmaf(yc, yc, s[2]);
+        }
+      }
+    };
+    add_up();
+    row_sums<kWideThreads, 3>(s, buf1[turn]);
+    if (s[0] > kBig || s[2] > kBig) {
+      fx = s[0] > kBig ? kShrink : 1.0f;
+      fy = s[2] > kBig ? kShrink : 1.0f;
+      s[0] = s[1] = s[2] = 0.0f;
+      add_up();
+      row_sums<kWideThreads, 3>(s, buf3[turn]);
+    }
+    const GradRow r = grad_row(a, s, fx, fy, token_gate<DT>(a, row));
+    float e[N], dpre[N], dpost[N], dg[N], q[2] = {0.0f, 0.0f};
+    if (has_y) {
+      for (int col = threadIdx.x * N; col < H; col += kWideThreads * N) {
+        load(col);
+        grad_columns<DT, W32>(a, r, at, col, x, dh, y, D, dpre, e, dpost, dg);
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          q[0] = fmaf(e[c], y[c] * r.ys, q[0]);
+          q[1] += dg[c];
+        }
+      }
+      row_sums<kWideThreads, 2>(q, buf2[turn]);
+      if (a.gate_kind == kGateToken && a.d_gate != nullptr && threadIdx.x == 0)
+        ((float*)a.d_gate)[row] = q[1];
+    }
+    const float ym = a.post ? q[0] / (float)H : 0.0f;
+    const bool begin = row == blockIdx.x;
+    for (int col = threadIdx.x * N; col < H; col += kWideThreads * N) {
+      load(col);
+      grad_columns<DT, W32>(a, r, at, col, x, dh, y, D, dpre, e, dpost, dg);
+      RowVec<DT>::template store<true>(a.dr + at, col, H, RowVec<DT>::pack(D));
+      if (has_y) {
+        if (a.gate_kind == kGateFull && a.d_gate != nullptr)
+          RowVec<DT>::template store<true>((uint8_t*)a.d_gate + at, col, H,
+                                           RowVec<DT>::pack(dg));
+#pragma unroll
+        for (int c = 0; c < N; ++c) e[c] = r.ys * fmaf(-y[c] * r.ys, ym, e[c]);
+        RowVec<DT>::template store<true>(a.dy + at, col, H, RowVec<DT>::pack(e));
+      }
+#pragma unroll
+      for (int o = 0; o < 3; ++o) {
+        if (!(a.want & (1 << o))) continue;
+        float* part = a.part + ((int64_t)o * gridDim.x + blockIdx.x) * H;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          if (col + c >= H) continue;
+          const float v = o == 0 ? dpre[c] : o == 1 ? dpost[c] : dg[c];
+          part[col + c] = begin ? v : part[col + c] + v;
+        }
+      }
+    }
+  }
+}
+
+constexpr int kSumCols = 64, kSumWays = 16;
+
+// column c of output o: the parts of every block in order, 16 interleaved
+// runs of them side by side
+__global__ __launch_bounds__(kSumCols* kSumWays) void grad_sum_kernel(const float* part,
+                                                                     int parts, int H, float* g0,
+                                                                     float* g1, float* g2) {
+  __shared__ float run[kSumWays][kSumCols];
+  float* out = blockIdx.y == 0 ? g0 : blockIdx.y == 1 ? g1 : g2;
+  if (out == nullptr) return;
+  part += (int64_t)blockIdx.y * parts * H;
+  const int x = threadIdx.x % kSumCols, w = threadIdx.x / kSumCols;
+  const int c = blockIdx.x * kSumCols + x;
+  float s = 0.0f;
+  if (c < H)
+    for (int p = w; p < parts; p += kSumWays) s += part[(int64_t)p * H + c];
+  run[w][x] = s;
+  __syncthreads();
+  if (w != 0 || c >= H) return;
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kSumWays; ++i) s += run[i][x];
+  out[c] = s;
+}
+
+template <int B, int V>
+struct Shape {
+  static constexpr int BT = B, VPT = V;       // lanes per row, vectors per lane
+};
+
+template <int DT, bool W32>
+hipError_t norm_dt(const NormArgs& a, hipStream_t stream) {
+  const int nv = (a.H + RowVec<DT>::N - 1) / RowVec<DT>::N;
+  auto go = [&](auto shape) {
+    constexpr int BT = decltype(shape)::BT, VPT = decltype(shape)::VPT;
+    const int64_t grid = BT == 64 ? (a.T + 3) / 4 : a.T;
+    norm_kernel<DT, W32, BT, VPT><<<(unsigned)grid, BT == 64 ? 256 : BT, 0, stream>>>(a);
+    return hipGetLastError();
+  };
+  if (nv <= 64) return go(Shape<64, 1>());
+  if (nv <= 128) return go(Shape<64, 2>());
+  if (nv <= 256) return go(Shape<64, 4>());
+  if (nv <= 512) return go(Shape<256, 2>());
+  if (nv <= 1024) return go(Shape<256, 4>());
+  if (nv <= 2048) return go(Shape<512, 4>());
+  if (nv <= 4096) return go(Shape<1024, 4>());
+  if constexpr (DT == kF32) return go(Shape<1024, 8>());
+  return hipErrorInvalidValue;                // 2-byte rows end at 4096 vectors
+}
+
+// vectors per row above which a row does not fit the registers of a block
+constexpr int kWideVectors = 1024;
+
+template <int DT, bool W32>
+hipError_t norm_grad_dt(const NormGradArgs& a, int blocks, hipStream_t stream) {
+  const int nv = (a.H + RowVec<DT>::N - 1) / RowVec<DT>::N;
+  auto go = [&](auto shape) {
+    constexpr int BT = decltype(shape)::BT, VPT = decltype(shape)::VPT;
+    norm_grad_kernel<DT, W32, BT, VPT>
+        <<<blocks, BT < kGradThreads ? kGradThreads : BT, 0, stream>>>(a);
+    return hipGetLastError();
+  };
+  if (nv <= 64) return go(Shape<64, 1>());
+  if (nv <= 128) return go(Shape<64, 2>());
+  if (nv <= 256) return go(Shape<256, 1>());
+  if (nv <= 512) return go(Shape<512, 1>());
+  if (nv <= kWideVectors) return go(Shape<512, 2>());
+  norm_grad_wide_kernel<DT, W32><<<blocks, kWideThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+int rows_per_block(int H, int dtype) {
+  const int n = 16 / dtype_size(dtype), nv = (H + n - 1) / n;
+  return nv <= 128 ? grad_groups(64) : nv <= 256 ? grad_groups(256) : 1;
+}
+
+}  // namespace
+
+// blocks of the gradient kernel, each with a part of the column sums
+int norm_grad_parts(int64_t T, int H, int dtype) {
+  const int per = rows_per_block(H, dtype);
+  const int64_t need = (T + per - 1) / per;
+  return (int)(need < kNormGradBlocks ? need : kNormGradBlocks);
+}
+
+hipError_t launch_norm(const NormArgs& a, int dtype, bool w32, hipStream_t stream) {
+  if (a.T == 0) return hipSuccess;
+  switch (dtype) {
+    case kBf16: return w32 ? norm_dt<kBf16, true>(a, stream) : norm_dt<kBf16, false>(a, stream);
+    case kF16: return w32 ? norm_dt<kF16, true>(a, stream) : norm_dt<kF16, false>(a, stream);
+    default: return norm_dt<kF32, true>(a, stream);
+  }
+}
+
+hipError_t launch_norm_grad(const NormGradArgs& a, int dtype, bool w32, float* g_pre,
+                            float* g_post, float* g_gate, hipStream_t stream) {
+  const int blocks = norm_grad_parts(a.T, a.H, dtype);
+  hipError_t err = hipSuccess;
+  if (blocks > 0) {
+    switch (dtype) {
+      case kBf16:
+        err = w32 ? norm_grad_dt<kBf16, true>(a, blocks, stream)
+                  : norm_grad_dt<kBf16, false>(a, blocks, stream);
+        break;
+      case kF16:
+        err = w32 ? norm_grad_dt<kF16, true>(a, blocks, stream)
+                  : norm_grad_dt<kF16, false>(a, blocks, stream);
+        break;
+      default: err = norm_grad_dt<kF32, true>(a, blocks, stream);
+    }
+  }
+  if (err != hipSuccess || (g_pre == nullptr && g_post == nullptr && g_gate == nullptr))
+    return err;
+  grad_sum_kernel<<<dim3((a.H + kSumCols - 1) / kSumCols, 3), kSumCols * kSumWays, 0, stream>>>(
+      a.part, blocks, a.H, g_pre, g_post, g_gate);
+  return hipGetLastError();
+}
+
+}  // namespace moe

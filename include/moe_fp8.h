@@ -470,6 +470,184 @@ moe_status_t moe_forward_static(const moe_problem_t* p, const void* hidden,
                                 const moe_eplb_t* eplb, const void* w13, const void* w13_sf,
                                 const void* w2, const void* w2_sf, void* out, void* stream);
 
+/* ---- Around the layer: router, sorted rows, block norms -------------------
+ * The steps on both sides of moe_forward, for serving and, with their
+ * gradients, for training.  They take bf16, fp16 or fp32 data of any width
+ * (moe_dtype_t); data pointers need their element's alignment only, index
+ * arrays 4 bytes.  Sums, softmax statistics and norms are held in fp32 and
+ * rounded once on the way out.  Results do not depend on timing: no sum's
+ * order does.  An empty batch (num_tokens 0) is a no-op except where a call
+ * below says what it still writes. */
+
+/* Element types of the calls below. */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1, MOE_DT_F32 = 2 } moe_dtype_t;
+
+/* Score of an expert from its logit x. */
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0, /* softmax over the token's unmasked experts        */
+  MOE_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-x))                                */
+} moe_score_t;
+
+/* Router (host struct).  Requirements: 1 <= num_experts <= 1024; 1 <= top_k
+ * <= min(num_experts, 64); num_groups in [1, 64] divides num_experts;
+ * 1 <= topk_groups <= num_groups with topk_groups * num_experts / num_groups
+ * >= top_k; group_top 1 or 2; scale finite. */
+typedef struct {
+  int32_t num_tokens;
+  int32_t num_experts;
+  int32_t top_k;
+  int32_t dtype;       /* moe_dtype_t of the logits and of their gradient    */
+  int32_t score;       /* moe_score_t                                        */
+  int32_t num_groups;  /* groups of consecutive experts; 1: no groups        */
+  int32_t topk_groups; /* groups kept per token                              */
+  int32_t group_top;   /* experts whose keys add up to a group's value       */
+  int32_t renormalize; /* weights of a token sum to scale                    */
+  float scale;
+} moe_router_t;
+
+/* The top_k experts of every token and their weights, as moe_stage and
+ * moe_forward take them: topk_ids int32 [T, top_k], topk_weights fp32
+ * [T, top_k], from logits [T, E].
+ *  - A logit of -inf or NaN masks its expert for that token; +inf counts as
+ *    the largest finite fp32.  Padding tokens (is_padding uint8 [T] or NULL)
+ *    have every expert masked, whatever their logits hold.
+ *  - Experts are ordered by a key, largest first, ties by the lower index:
+ *    the logit, or, with a bias or group_top 2, score + bias[e] evaluated in
+ *    64 bits (bias fp32 [E] or NULL; for the choice alone, it does not enter
+ *    the weights).
+ *  - With groups, a group's value is the sum of its group_top largest
+ *    unmasked keys; only experts of the topk_groups largest groups (ties by
+ *    the lower index) are chosen from.
+ *  - Weights: scale * score, or renormalized scale * s / sum of the chosen
+ *    scores (sigmoid: plus 1e-20).
+ *  - A token with fewer than top_k unmasked experts gets id -1 and weight 0
+ *    in the places left over. */
+moe_status_t moe_router_topk(const moe_router_t* p, const void* logits, const float* bias,
+                             const uint8_t* is_padding, int32_t* topk_ids, float* topk_weights,
+                             void* stream);
+
+/* The gradient of the logits (dense [T, E], every element written) from the
+ * weights' gradient fp32 [T, top_k], at the ids moe_router_topk chose (the
+ * choice itself has no gradient, nor has the bias).  Slots with an id
+ * outside [0, E) or a masked logit contribute nothing; a token without any
+ * other gets zeros. */
+moe_status_t moe_router_topk_backward(const moe_router_t* p, const void* logits,
+                                      const int32_t* topk_ids, const float* grad_topk_weights,
+                                      void* grad_logits, void* stream);
+
+/* Rows sorted by expert (host struct).  Requirements: 1 <= hidden <= 32768;
+ * 1 <= num_experts <= 1024; top_k >= 1; num_tokens * top_k < 2^31. */
+typedef struct {
+  int32_t num_tokens;
+  int32_t hidden;
+  int32_t num_experts;
+  int32_t top_k;
+  int32_t dtype; /* moe_dtype_t of tokens and rows */
+} moe_rows_t;
+
+/* Device scratch bytes of moe_permute (host only). */
+moe_status_t moe_permute_workspace_size(const moe_rows_t* p, size_t* bytes);
+
+/* Sorts the routed (token, slot) pairs by expert, in ascending slot order
+ * t * top_k + j within an expert (moe_stage's contiguous order), and copies
+ * the tokens' rows: rows[slot_row[t, j]] = x[t].  topk_ids int32 [T, top_k]:
+ * ids outside [0, E) and the slots of padding tokens (is_padding uint8 [T]
+ * or NULL) are unrouted.  Outputs: rows [T*top_k, hidden], expert_offsets
+ * int32 [E+1], slot_row int32 [T, top_k] (-1 when unrouted), row_slot int32
+ * [T*top_k] (the flat slot of each row).  rows and row_slot entries behind
+ * the last routed row (expert_offsets[E]) stay as they were.  T = 0 still
+ * writes expert_offsets (zeros).  ws: device scratch of
+ * moe_permute_workspace_size bytes, 4-byte aligned; calls sharing one must
+ * not overlap. */
+moe_status_t moe_permute(const moe_rows_t* p, const void* x, const int32_t* topk_ids,
+                         const uint8_t* is_padding, void* rows, int32_t* expert_offsets,
+                         int32_t* slot_row, int32_t* row_slot, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* grad_x[t] = sum over j ascending of grad_rows[slot_row[t, j]]; tokens with
+ * no routed slot get 0.  Here and below, slot_row entries outside
+ * [0, T*top_k) are unrouted. */
+moe_status_t moe_permute_backward(const moe_rows_t* p, const void* grad_rows,
+                                  const int32_t* slot_row, void* grad_x, void* stream);
+
+/* out[t] = sum over j ascending of topk_weights[t, j] * rows[slot_row[t, j]]
+ * (topk_weights fp32 [T, top_k], or NULL for weights of 1); tokens with no
+ * routed slot get 0.  The form of moe_topk_reduce for any type and width. */
+moe_status_t moe_unpermute(const moe_rows_t* p, const void* rows, const int32_t* slot_row,
+                           const float* topk_weights, void* out, void* stream);
+
+/* The gradients of moe_unpermute: grad_rows[slot_row[t, j]] =
+ * topk_weights[t, j] * grad_out[t] (rows without a slot stay as they were)
+ * and grad_topk_weights[t, j] = <grad_out[t], rows[slot_row[t, j]]>, fp32
+ * [T, top_k], 0 for unrouted slots.  slot_row's routed entries must differ
+ * from each other.  grad_rows may be rows. */
+moe_status_t moe_unpermute_backward(const moe_rows_t* p, const void* grad_out, const void* rows,
+                                    const int32_t* slot_row, const float* topk_weights,
+                                    void* grad_rows, float* grad_topk_weights, void* stream);
+
+/* What multiplies the block's output in moe_block_norm. */
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_TOKEN = 1,   /* [T]: one value per token                          */
+  MOE_GATE_CHANNEL = 2, /* [hidden]: one value per column                    */
+  MOE_GATE_FULL = 3     /* [T, hidden]                                       */
+} moe_gate_t;
+
+/* Norms before and after a block (host struct).  Requirements: 1 <= hidden
+ * <= 32768; 1e-20 <= eps <= 1e20; residual_scale and weight_offset finite. */
+typedef struct {
+  int32_t num_tokens;
+  int32_t hidden;
+  int32_t dtype;        /* moe_dtype_t of the streams and the gate           */
+  int32_t weight_dtype; /* moe_dtype_t of both weights: dtype or MOE_DT_F32  */
+  int32_t post_norm;    /* the block's output is normed                      */
+  int32_t gate;         /* moe_gate_t                                        */
+  int32_t gate_sigmoid; /* the gate enters as 1 / (1 + exp(-gate))           */
+  float eps;
+  float residual_scale;
+  float weight_offset;  /* a norm multiplies by weight_offset + weight       */
+} moe_block_norm_t;
+
+/* With norm(v) = v / sqrt(mean(v^2) + eps) per row:
+ *   n            = post_norm ? norm(y) * (weight_offset + post_weight) : y
+ *   residual_out = residual + residual_scale * gate * n
+ *   normed       = norm(residual_out) * (weight_offset + pre_weight)
+ * normed is made from residual_out before that is rounded.  A NULL weight
+ * multiplies by 1.  y NULL: no block before this norm; then residual_out,
+ * gate and post_weight must be NULL and normed is the norm of residual.
+ * normed NULL: only the residual update.  The gate must be NULL exactly when
+ * its kind is NONE (or y is NULL).  residual_out may be residual and normed
+ * may be y (the same pointer). */
+moe_status_t moe_block_norm(const moe_block_norm_t* p, const void* residual, const void* y,
+                            const void* post_weight, const void* gate, const void* pre_weight,
+                            void* residual_out, void* normed, void* stream);
+
+/* Device scratch bytes of moe_block_norm_backward when it returns a weight's
+ * or a per-channel gate's gradient (host only). */
+moe_status_t moe_block_norm_workspace_size(const moe_block_norm_t* p, size_t* bytes);
+
+/* Gradients of moe_block_norm.  residual_out: the stream as the forward call
+ * stored it (with y NULL: its residual); y, weights and gate as in the
+ * forward call.  Incoming: grad_normed and grad_residual_out [T, hidden]
+ * (either may be NULL: 0).  Outgoing:
+ *   grad_residual    [T, hidden]
+ *   grad_y           [T, hidden] (NULL exactly when y is)
+ *   grad_pre_weight, grad_post_weight  fp32 [hidden] or NULL
+ *   grad_gate        fp32 [T] (token), fp32 [hidden] (channel) or dtype
+ *                    [T, hidden] (full), or NULL
+ * T = 0 writes zeros to the gradients that are sums over the tokens.
+ * grad_residual may be grad_residual_out, grad_y may be grad_normed.
+ * ws: device scratch of moe_block_norm_workspace_size bytes, 4-byte aligned,
+ * needed when grad_pre_weight, grad_post_weight or a channel gate's grad_gate
+ * is given (else it may be NULL); calls sharing one must not overlap. */
+moe_status_t moe_block_norm_backward(const moe_block_norm_t* p, const void* residual_out,
+                                     const void* y, const void* post_weight, const void* gate,
+                                     const void* pre_weight, const void* grad_normed,
+                                     const void* grad_residual_out, void* grad_residual,
+                                     void* grad_y, float* grad_pre_weight,
+                                     float* grad_post_weight, void* grad_gate, void* ws,
+                                     size_t ws_bytes, void* stream);
+
 /* Message of the last failed call on this thread ("" if none).  The
  * argument errors it describes follow the ValueError conditions of
  * prepare_megamoe_inputs and _resolve_hidden_quant
