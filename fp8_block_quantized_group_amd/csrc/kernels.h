@@ -224,6 +224,8 @@ struct RouterArgs {
   int64_t T;
   int E, k;
   int groups, topk_groups, group_top;
+  int group_size;              // set by the launcher: E / groups, and the log of the
+  int group_lanes_log;         // lanes that hold a group, -1 when they are not 2^0..2^4
   bool sigmoid, renormalize;
   float scale;
 };

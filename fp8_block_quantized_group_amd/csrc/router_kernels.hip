@@ -9,8 +9,16 @@
 // must not depend on which exp an implementation uses).  Groups of
 // consecutive experts may limit the choice first.  Ties go to the lowest
 // index.
+//
+// One wave per token; lane l holds the VPL consecutive experts from l * VPL.
+// The choice runs on 32-bit keys as ordered integers, k rounds of a wave
+// maximum; 64-bit keys are computed only for a token where two keys that
+// decide something lie within the 32-bit keys' error (kNear*: some tokens in
+// a thousand).
 #include <float.h>
 #include <limits.h>
+
+#include <type_traits>
 
 #include "kernels.h"
 #include "row_vec.h"
@@ -26,130 +34,394 @@ __device__ __forceinline__ float clean_logit(float x) {
   return x == x ? fminf(x, FLT_MAX) : -INFINITY;
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
-}
-
 // 1 / (1 + e^-x) without overflow on either side
 __device__ __forceinline__ float sigmoid_f32(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// The best (key, index) of the wave: the largest key, the lowest index among
-// equal ones.
-__device__ __forceinline__ void wave_best(double& key, int& idx) {
+// Errors of the 32-bit keys.  A sigmoid from v_exp and v_rcp is off by less
+// than 2^-22: its argument's rounding moves it by s (1 - s) |x| 2^-24 at most,
+// exp and reciprocal add a step of s each.  A softmax adds the rounding of
+// its sum, below 2^-19 of s for 1024 terms.  Adding the bias rounds once more.
+// Two keys further apart than kNear * (1 + |key|), and two groups' values
+// further apart than twice that, are in the order of their 64-bit values.
+constexpr float kNearSigmoid = 0x1p-20f;
+constexpr float kNearSoftmax = 0x1p-18f;
+
+// whether the larger key `b` and the smaller `c` (0: none) may change places
+__device__ __forceinline__ bool near_keys(uint32_t b, uint32_t c, float near) {
+  const float fb = from_ordered(b);
+  return fb - from_ordered(c) <= near * (1.0f + fabsf(fb));
+}
+
+// the VPL logits of a lane as the definition counts them; past E: masked
+template <int DT, int VPL>
+__device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E, int e0,
+                                            float (&x)[VPL]) {
+  const uint8_t* row = (const uint8_t*)logits + t * E * RowVec<DT>::kSize;
+  constexpr int N = RowVec<DT>::N;
+  if constexpr (VPL % N == 0) {
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double k2 = __shfl_xor(key, d);
-    const int i2 = __shfl_xor(idx, d);
-    if (k2 > key || (k2 == key && i2 < idx)) {
-      key = k2;
-      idx = i2;
-    }
+    for (int i = 0; i < VPL; i += N)
+      RowVec<DT>::unpack(RowVec<DT>::template load<true>(row, e0 + i, E), x + i);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) x[i] = e0 + i < E ? clean_logit(x[i]) : -INFINITY;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      x[i] = e0 + i < E ? clean_logit(RowVec<DT>::load_one(row, e0 + i)) : -INFINITY;
   }
 }
 
-// lane l holds experts l, l + 64, ... (VPL of them)
-template <int DT, int VPL>
-__global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(const RouterArgs a) {
-  extern __shared__ double lds[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kRouterWaves + wave;
-  if (t >= a.T) return;
-  double* wkeys = lds + (int64_t)wave * a.E;
-  const int E = a.E, k = a.k;
-  const bool pad = a.is_padding != nullptr && a.is_padding[t] != 0;
-  float x[VPL];
-  double key[VPL];
-  float m = -INFINITY;
+// larger and second of two pairs, each in order
+__device__ __forceinline__ void merge_top2(uint32_t& b, uint32_t& s, uint32_t b2, uint32_t s2) {
+  s = max(min(b, b2), max(s, s2));
+  b = max(b, b2);
+}
+template <int CTRL>
+__device__ __forceinline__ void merge_lanes(uint32_t& b, uint32_t& s) {
+  merge_top2(b, s, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, CTRL, 0xF, 0xF, true),
+             (uint32_t)__builtin_amdgcn_update_dpp(0, (int)s, CTRL, 0xF, 0xF, true));
+}
+
+// the value of a group from its two best ordered keys, ordered again
+__device__ __forceinline__ uint32_t group_value(uint32_t b, uint32_t s, int group_top) {
+  if (b == 0u || s == 0u || group_top == 1) return b;
+  return ordered_bits(from_ordered(b) + from_ordered(s));
+}
+
+// Drops the keys (sets them to 0) of all but the topk_groups best groups.
+// Returns whether two groups' values lie too close to tell.
+template <int VPL>
+__device__ __forceinline__ bool keep_groups(const RouterArgs& a, uint32_t (&key)[VPL],
+                                            uint32_t* wkeys, float near) {
+  const int lane = threadIdx.x & 63;
+  const int size = a.group_size;
+  // groups of 1, 2, 4, 8 or 16 whole lanes meet by lane exchanges; others
+  // through LDS, lane g walking group g
+  const bool by_lanes = a.group_lanes_log >= 0;
+  uint32_t b = 0, s = 0;
+  int group = lane, pitch = 1;
+  if (by_lanes) {
+    const int lanes = 1 << a.group_lanes_log;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 64 * i;
-    x[i] = e < E && !pad
-               ? clean_logit(RowVec<DT>::load_one((const uint8_t*)a.logits, t * E + e))
-               : -INFINITY;
-    m = fmaxf(m, x[i]);
-  }
-  m = wave_max(m);
-  const bool scored = a.bias != nullptr || a.group_top > 1;
-  double total = 0.0;
-  if (scored && !a.sigmoid) {
+    for (int i = 0; i < VPL; ++i) merge_top2(b, s, key[i], 0);
+    if (lanes > 1) merge_lanes<0xB1>(b, s);       // quad_perm [1,0,3,2]
+    if (lanes > 2) merge_lanes<0x4E>(b, s);       // quad_perm [2,3,0,1]
+    if (lanes > 4) merge_lanes<0x141>(b, s);      // row_half_mirror
+    if (lanes > 8) merge_lanes<0x140>(b, s);      // row_mirror
+    group = lane >> a.group_lanes_log;
+    pitch = lanes;
+  } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (x[i] > -INFINITY) total += exp((double)x[i] - (double)m);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+      if (lane * VPL + i < a.E) wkeys[lane * VPL + i] = key[i];
+    __builtin_amdgcn_wave_barrier();
+    if (lane < a.groups)
+      for (int j = 0; j < size; ++j) merge_top2(b, s, wkeys[lane * size + j], 0);
   }
+  const uint32_t v = group < a.groups ? group_value(b, s, a.group_top) : 0u;
+  int better = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)v, g * pitch);
+    better += (o > v || (o == v && g < group)) ? 1 : 0;
+  }
+  const bool keep = better < a.topk_groups && group < a.groups;
+  bool unclear = false;
+  if (near > 0.0f) {                      // the last group kept, the best one dropped
+    const float best_dropped = from_ordered(wave_max(keep ? 0u : v));
+    const float last_kept = from_ordered(~wave_max(keep && v != 0u ? ~v : 0u));
+    unclear = last_kept - best_dropped <= 2.0f * near * (1.0f + fabsf(last_kept));
+  }
+  if (by_lanes) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = keep ? key[i] : 0u;
+  } else {
+    const uint64_t kept = __ballot(keep);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (!((kept >> ((lane * VPL + i) / size & 63)) & 1)) key[i] = 0u;
+  }
+  return unclear;
+}
+
+// fp64 values as integers of the same order; 0 is below every one of them
+__device__ __forceinline__ uint64_t ordered_bits64(double f) {
+  const uint64_t b = (uint64_t)__double_as_longlong(f + 0.0);
+  return (b >> 63) ? ~b : b | (1ull << 63);
+}
+__device__ __forceinline__ double from_ordered64(uint64_t u) {
+  return __longlong_as_double((long long)((u >> 63) ? u & ~(1ull << 63) : ~u));
+}
+__device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
+  const uint32_t hi = wave_max((uint32_t)(v >> 32));
+  return (uint64_t)hi << 32 | wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+}
+__device__ __forceinline__ uint64_t read_lane(uint64_t v, int l) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), l) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)v, l);
+}
+
+// the softmax's sum in 64 bits (1 for a sigmoid)
+template <int VPL>
+__device__ double exact_total(const RouterArgs& a, const float (&x)[VPL], float m) {
+  if (a.sigmoid) return 1.0;
+  double total = 0.0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (x[i] > -INFINITY) total += exp((double)x[i] - (double)m);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+  return total;
+}
+__device__ double exact_key(const RouterArgs& a, float x, float m, double total, float bias) {
+  const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x))
+                             : exp((double)x - (double)m) / total;
+  return s + (double)bias;
+}
+
+// The n candidates, one per lane, ordered by their 64-bit keys.  Every
+// expert outside is clearly below the first k.
+template <int VPL>
+__device__ int rank_exactly(const RouterArgs& a, const float (&x)[VPL], float m, float my_x,
+                            float bias, int my_id, int n) {
+  const int lane = threadIdx.x & 63;
+  const double total = exact_total<VPL>(a, x, m);
+  const uint64_t key =
+      my_id >= 0 ? ordered_bits64(exact_key(a, my_x, m, total, bias)) : 0;
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const uint64_t o = read_lane(key, j);
+    const int oid = __builtin_amdgcn_readlane(my_id, j);
+    rank += (o > key || (o == key && oid < my_id)) ? 1 : 0;
+  }
+  // a permutation: the lanes past the candidates stay where they are
+  return __builtin_amdgcn_ds_permute((my_id >= 0 ? rank : lane) * 4, my_id);
+}
+
+// The choice from 64-bit keys: lane j gets the j-th expert (-1: none left).
+// Few tokens come here (two groups too close to tell), but a kernel ends with
+// its slowest wave: the same steps as for 32-bit keys, on integers.
+template <int VPL>
+__device__ int choose_exactly(const RouterArgs& a, const float (&x)[VPL], float m,
+                              uint64_t* wkeys) {
+  const int lane = threadIdx.x & 63;
+  const double total = exact_total<VPL>(a, x, m);
+  uint64_t key[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 64 * i;
-    key[i] = x[i];
-    if (scored && x[i] > -INFINITY) {
-      key[i] = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x[i]))
-                         : exp((double)x[i] - (double)m) / total;
-      if (a.bias != nullptr) key[i] += (double)a.bias[e];
+    key[i] = 0;
+    if (x[i] > -INFINITY) {
+      const double f = exact_key(a, x[i], m, total,
+                                 a.bias != nullptr ? a.bias[lane * VPL + i] : 0.0f);
+      if (f > -INFINITY) key[i] = ordered_bits64(f);           // NaN masks
     }
   }
   if (a.groups > 1) {
-    const int size = E / a.groups;
+    const int size = a.group_size;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (lane + 64 * i < E) wkeys[lane + 64 * i] = key[i];
+      if (lane * VPL + i < a.E) wkeys[lane * VPL + i] = key[i];
     __builtin_amdgcn_wave_barrier();
-    // lane g: the value of group g
-    double value = -INFINITY;
+    uint64_t best = 0, second = 0;          // lane g: of group g
     if (lane < a.groups) {
-      double best = -INFINITY, second = -INFINITY;
+#pragma unroll 8
       for (int j = 0; j < size; ++j) {
-        const double v = wkeys[lane * size + j];
-        if (v > best) {
-          second = best;
-          best = v;
-        } else if (v > second) {
-          second = v;
-        }
+        const uint64_t v = wkeys[lane * size + j];
+        second = max(second, min(best, v));
+        best = max(best, v);
       }
-      value = best + (a.group_top > 1 && second > -INFINITY ? second : 0.0);
+      if (a.group_top > 1 && second != 0)
+        best = ordered_bits64(from_ordered64(best) + from_ordered64(second));
     }
-    uint64_t kept = 0;
-    for (int r = 0; r < a.topk_groups; ++r) {
-      double b = value;
-      int g = lane;
-      wave_best(b, g);
-      if (b == -INFINITY) break;
-      kept |= 1ull << g;
-      if (lane == g) value = -INFINITY;
+    int better = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const uint64_t o = read_lane(best, g);
+      better += (o > best || (o == best && g < lane)) ? 1 : 0;
     }
+    const uint64_t kept = __ballot(lane < a.groups && better < a.topk_groups);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (!((kept >> ((lane * VPL + i) / size & 63)) & 1)) key[i] = 0;
+  }
+  int my_id = -1;
+  for (int j = 0; j < a.k; ++j) {
+    uint64_t b = key[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) b = max(b, key[i]);
+    const uint64_t top = wave_max64(b);
+    if (top == 0) break;
+    const int l = __builtin_ctzll(__ballot(b == top));
+    int at = 0;
+#pragma unroll
+    for (int i = VPL - 1; i >= 0; --i) at = key[i] == top ? i : at;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = lane == l && at == i ? 0 : key[i];
+    const int e = __builtin_amdgcn_readlane(lane * VPL + at, l);
+    my_id = lane == j ? e : my_id;
+  }
+  return my_id;
+}
+
+// The keys of a lane's experts that are still to choose from.  Up to four are
+// kept in order (equal ones by index: neighbours swap only when the second is
+// larger), so that a round looks at one key and shifts the others up; more
+// are searched when one of them has won.
+template <int VPL>
+struct LaneKeys {
+  static constexpr bool kSorted = VPL <= 4;
+  uint32_t key[VPL];
+  int id[VPL];
+
+  __device__ __forceinline__ void init(const uint32_t (&k)[VPL], int e0) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 64 * i;
-      if (e < E && !((kept >> (e / size)) & 1)) key[i] = -INFINITY;
+      key[i] = k[i];
+      id[i] = e0 + i;
+    }
+    if (!kSorted) return;
+#pragma unroll
+    for (int n = VPL - 1; n > 0; --n) {
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const bool swap = key[i + 1] > key[i];
+        const uint32_t a = key[i], b = key[i + 1];
+        const int ia = id[i], ib = id[i + 1];
+        key[i] = swap ? b : a;
+        key[i + 1] = swap ? a : b;
+        id[i] = swap ? ib : ia;
+        id[i + 1] = swap ? ia : ib;
+      }
     }
   }
-  // the top k, one after the other; lane j keeps the j-th
-  int my_id = -1;
-  float my_x = -INFINITY;
-  for (int j = 0; j < k; ++j) {
-    double b = -INFINITY;
-    int at = INT_MAX;
-    float bx = 0.0f;
+  __device__ __forceinline__ uint32_t head() const {
+    uint32_t b = key[0];
+    if (!kSorted) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (key[i] > b) {
-        b = key[i];
-        at = lane + 64 * i;
-        bx = x[i];
+      for (int i = 1; i < VPL; ++i) b = max(b, key[i]);
+    }
+    return b;
+  }
+  // takes lane l's key b, its head, away; returns its expert
+  __device__ __forceinline__ int pop(uint32_t b, int l) {
+    const bool win = (int)(threadIdx.x & 63) == l;
+    if (kSorted) {
+      const int e = __builtin_amdgcn_readlane(id[0], l);
+#pragma unroll
+      for (int i = 0; i + 1 < VPL; ++i) {
+        key[i] = win ? key[i + 1] : key[i];
+        id[i] = win ? id[i + 1] : id[i];
       }
-    const int mine = at;
-    wave_best(b, at);
-    if (b == -INFINITY) break;
-    bx = __shfl(bx, at & 63);
+      key[VPL - 1] = win ? 0u : key[VPL - 1];
+      return e;
+    }
+    int at = 0;
+#pragma unroll
+    for (int i = VPL - 1; i >= 0; --i) at = key[i] == b ? i : at;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = win && at == i ? 0u : key[i];
+    return __builtin_amdgcn_readlane(id[0] + at, l);
+  }
+};
+
+template <int DT, int VPL>
+__global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(const RouterArgs a) {
+  extern __shared__ uint64_t lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = (int64_t)blockIdx.x * kRouterWaves + wave;
+  if (t >= a.T) return;
+  uint64_t* wkeys = lds + (int64_t)wave * a.E;
+  const int E = a.E, k = a.k, e0 = lane * VPL;
+  const bool pad = a.is_padding != nullptr && a.is_padding[t] != 0;
+  if (pad) {
+    if (lane < k) {
+      a.ids[t * k + lane] = -1;
+      a.weights[t * k + lane] = 0.0f;
+    }
+    return;
+  }
+  float x[VPL];
+  load_logits<DT, VPL>(a.logits, t, E, e0, x);
+  const bool scored = a.bias != nullptr || a.group_top > 1;
+  float m = 0.0f, total = 1.0f;             // of the softmax over all experts
+  const bool over_all = !a.sigmoid && (scored || !a.renormalize);
+  if (over_all) {
+    m = x[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, x[i]);
+    m = wave_max(m);
+    total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) total += x[i] > -INFINITY ? expf(x[i] - m) : 0.0f;
+    total = wave_sum(total);
+  }
+  const float near = !scored ? 0.0f : a.sigmoid ? kNearSigmoid : kNearSoftmax;
+  float f[VPL];
+  if (scored) {
+    float bias[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (mine == at && lane + 64 * i == at) key[i] = -INFINITY;
-    if (lane == j) {
-      my_id = at;
-      my_x = bx;
+      bias[i] = a.bias != nullptr && e0 + i < E ? a.bias[e0 + i] : 0.0f;
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        f[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[i])) + bias[i];
+    } else {
+      const float inv_total = 1.0f / total;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) f[i] = fmaf(expf(x[i] - m), inv_total, bias[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) f[i] = x[i];
+  }
+  uint32_t key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)           // a bias of NaN or -inf masks its expert too
+    key[i] = x[i] > -INFINITY && f[i] > -INFINITY ? ordered_bits(f[i]) : 0u;
+  bool near_groups = false;
+  if (a.groups > 1) near_groups = keep_groups<VPL>(a, key, (uint32_t*)wkeys, near);
+  // lane j keeps the j-th largest key and its expert
+  int my_id = -1;
+  uint32_t my_key = 0;
+  LaneKeys<VPL> mine;
+  mine.init(key, e0);
+  uint32_t last = 0;
+  int n = 0;
+  while (n < 64) {
+    const uint32_t head = mine.head();
+    const uint32_t b = wave_max(head);
+    if (b == 0u) break;
+    // k of them; where keys have an error, as many more as the last may have
+    // to be told from
+    if (n >= k && (!scored || !near_keys(last, b, near))) break;
+    const int l = __builtin_ctzll(__ballot(head == b));       // lowest lane first
+    const int e = mine.pop(b, l);
+    my_id = lane == n ? e : my_id;
+    my_key = lane == n ? b : my_key;
+    last = b;
+    ++n;
+  }
+  const uint8_t* logits = (const uint8_t*)a.logits;
+  float my_x = -INFINITY;
+  if (my_id >= 0) my_x = clean_logit(RowVec<DT>::load_one(logits, t * E + my_id));
+  if (scored) {
+    // neighbours too close to tell, unless equal logits and biases say which
+    const float bias = a.bias != nullptr && my_id >= 0 ? a.bias[my_id] : 0.0f;
+    const uint32_t prev = __shfl_up((int)my_key, 1);
+    const float prev_x = __shfl_up(my_x, 1), prev_bias = __shfl_up(bias, 1);
+    const bool unclear = lane > 0 && my_id >= 0 && near_keys(prev, my_key, near) &&
+                         !(prev_x == my_x && prev_bias == bias);
+    if (near_groups || __ballot(unclear) != 0) {
+      // (a lane is left for every expert that may be among the chosen unless
+      // 64 keys in a row are close)
+      if (near_groups || n == 64) my_id = choose_exactly<VPL>(a, x, m, wkeys);
+      else my_id = rank_exactly<VPL>(a, x, m, my_x, bias, my_id, n);
+      my_x = -INFINITY;
+      if (my_id >= 0) my_x = clean_logit(RowVec<DT>::load_one(logits, t * E + my_id));
+    }
+    if (lane >= k) {
+      my_id = -1;
+      my_x = -INFINITY;
     }
   }
   // the weights of the chosen, in 32 bits
@@ -163,11 +435,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(const Ro
     const float sum = wave_sum(w);
     w = my_id >= 0 ? w / sum : 0.0f;
   } else {
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) sum += x[i] > -INFINITY ? expf(x[i] - m) : 0.0f;
-    sum = wave_sum(sum);
-    w = my_id >= 0 ? expf(my_x - m) / sum : 0.0f;
+    w = my_id >= 0 ? expf(my_x - m) / total : 0.0f;
   }
   if (lane < k) {
     a.ids[t * k + lane] = my_id;
@@ -180,92 +448,116 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(const Ro
 // renormalized softmax the same over the chosen alone; sigmoid dx_j = c g_j
 // p_j (1 - p_j), renormalized with g_j replaced by (g_j - sum g p / D) / D.
 // A repeated id adds its terms in slot order.
-template <int DT>
-__global__ __launch_bounds__(64 * kRouterWaves) void router_grad_kernel(const RouterArgs a,
-                                                                        const int32_t* ids,
-                                                                        const float* grad_w,
-                                                                        uint8_t* grad_logits) {
-  extern __shared__ float ldsf[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+template <int DT, int VPL>
+__global__ __launch_bounds__(64 * kRouterWaves) void router_grad_kernel(
+    const RouterArgs a, const int32_t* __restrict__ ids, const float* __restrict__ grad_w,
+    uint8_t* __restrict__ grad_logits) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = (int64_t)blockIdx.x * kRouterWaves + wave;
   if (t >= a.T) return;
-  float* out = ldsf + (int64_t)wave * a.E;
-  const int E = a.E, k = a.k;
-  const uint8_t* logits = (const uint8_t*)a.logits;
+  const int E = a.E, k = a.k, e0 = lane * VPL;
+  const bool dense = !a.sigmoid && !a.renormalize;
+  float xs[VPL];
+  if (dense) load_logits<DT, VPL>(a.logits, t, E, e0, xs);
   int id = lane < k ? ids[t * k + lane] : -1;
   if (id < 0 || id >= E) id = -1;
-  float x = id >= 0 ? clean_logit(RowVec<DT>::load_one(logits, t * E + id)) : -INFINITY;
+  float x = id >= 0 ? clean_logit(RowVec<DT>::load_one((const uint8_t*)a.logits, t * E + id))
+                    : -INFINITY;
   if (x == -INFINITY) id = -1;
   const float g = id >= 0 ? grad_w[t * k + lane] : 0.0f;
-  const bool any = __ballot(id >= 0) != 0;
-  const bool dense = !a.sigmoid && !a.renormalize && any;
-  float d = 0.0f;                         // the chosen experts' gradients
-  float m = 0.0f, total = 1.0f, dot = 0.0f;
-  if (a.sigmoid) {
-    const float s = id >= 0 ? sigmoid_f32(x) : 0.0f;
-    // 1 - s as sigmoid(-x): no cancellation for large x
-    const float ds = id >= 0 ? s * sigmoid_f32(-x) : 0.0f;
-    if (a.renormalize) {
-      const float D = wave_sum(s) + 1e-20f;
-      d = (g - wave_sum(g * (s / D))) / D * ds;
+  float out[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) out[i] = 0.0f;
+  float d = 0.0f;                           // the chosen experts' gradients
+  if (__ballot(id >= 0) != 0) {
+    if (a.sigmoid) {
+      const float s = id >= 0 ? sigmoid_f32(x) : 0.0f;
+      // 1 - s as sigmoid(-x): no cancellation for large x
+      const float ds = id >= 0 ? s * sigmoid_f32(-x) : 0.0f;
+      if (a.renormalize) {
+        const float D = wave_sum(s) + 1e-20f;
+        d = (g - wave_sum(g * (s / D))) / D * ds;
+      } else {
+        d = g * ds;
+      }
+    } else if (a.renormalize) {
+      const float mx = wave_max(x);         // every lane takes part
+      const float p0 = id >= 0 ? expf(x - mx) : 0.0f;
+      const float p = p0 / wave_sum(p0);
+      d = p * (g - wave_sum(g * p));
     } else {
-      d = g * ds;
+      float m = xs[0], total = 0.0f;
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) m = fmaxf(m, xs[i]);
+      m = wave_max(m);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        xs[i] = xs[i] > -INFINITY ? expf(xs[i] - m) : 0.0f;
+        total += xs[i];
+      }
+      total = wave_sum(total);
+      const float p = id >= 0 ? expf(x - m) / total : 0.0f;
+      const float dot = wave_sum(g * p) * a.scale;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) out[i] = -dot * (xs[i] / total);
+      d = p * g;
     }
-  } else if (a.renormalize) {
-    const float mx = wave_max(x);          // every lane takes part
-    const float p0 = id >= 0 ? expf(x - mx) : 0.0f;
-    const float sum = wave_sum(p0);
-    const float p = id >= 0 ? p0 / sum : 0.0f;
-    d = p * (g - wave_sum(g * p));
-  } else if (any) {
-    m = -INFINITY;
-    for (int e = lane; e < E; e += 64)
-      m = fmaxf(m, clean_logit(RowVec<DT>::load_one(logits, t * E + e)));
-    m = wave_max(m);
-    total = 0.0f;
-    for (int e = lane; e < E; e += 64)
-      total += expf(clean_logit(RowVec<DT>::load_one(logits, t * E + e)) - m);
-    total = wave_sum(total);
-    const float p = id >= 0 ? expf(x - m) / total : 0.0f;
-    dot = wave_sum(g * p);
-    d = p * g;
+    d = id >= 0 ? d * a.scale : 0.0f;
+    for (int j = 0; j < k; ++j) {           // slot order: a repeated id adds up
+      const int ej = __builtin_amdgcn_readlane(id, j) - e0;
+      const float dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(d), j));
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) out[i] += ej == i ? dj : 0.0f;
+    }
   }
-  d = id >= 0 ? d * a.scale : 0.0f;
-  for (int e = lane; e < E; e += 64) {
-    float v = 0.0f;
-    if (dense)
-      v = -dot * a.scale *
-          (expf(clean_logit(RowVec<DT>::load_one(logits, t * E + e)) - m) / total);
-    out[e] = v;
+  uint8_t* row = grad_logits + t * E * RowVec<DT>::kSize;
+  constexpr int N = RowVec<DT>::N;
+  if constexpr (VPL % N == 0) {
+#pragma unroll
+    for (int i = 0; i < VPL; i += N)
+      if (e0 + i < E) RowVec<DT>::template store<true>(row, e0 + i, E, RowVec<DT>::pack(out + i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (e0 + i < E) RowVec<DT>::store_one(row, e0 + i, out[i]);
   }
-  __builtin_amdgcn_wave_barrier();
-  for (int j = 0; j < k; ++j) {
-    if (lane == j && id >= 0) out[id] += d;
-    __builtin_amdgcn_wave_barrier();
-  }
-  for (int e = lane; e < E; e += 64) RowVec<DT>::store_one(grad_logits, t * E + e, out[e]);
+}
+
+// VPL, the experts per lane: the smallest power of two that covers E
+template <class F>
+hipError_t per_lane(int E, F&& go) {
+  if (E <= 64) return go(std::integral_constant<int, 1>());
+  if (E <= 128) return go(std::integral_constant<int, 2>());
+  if (E <= 256) return go(std::integral_constant<int, 4>());
+  if (E <= 512) return go(std::integral_constant<int, 8>());
+  return go(std::integral_constant<int, 16>());
 }
 
 template <int DT>
-hipError_t topk_dt(const RouterArgs& a, hipStream_t stream) {
+hipError_t topk_dt(RouterArgs a, hipStream_t stream) {
   const unsigned grid = (unsigned)((a.T + kRouterWaves - 1) / kRouterWaves);
-  const size_t lds = a.groups > 1 ? (size_t)kRouterWaves * a.E * sizeof(double) : 0;
-  const int threads = 64 * kRouterWaves;
-  if (a.E <= 64) router_topk_kernel<DT, 1><<<grid, threads, lds, stream>>>(a);
-  else if (a.E <= 128) router_topk_kernel<DT, 2><<<grid, threads, lds, stream>>>(a);
-  else if (a.E <= 256) router_topk_kernel<DT, 4><<<grid, threads, lds, stream>>>(a);
-  else if (a.E <= 512) router_topk_kernel<DT, 8><<<grid, threads, lds, stream>>>(a);
-  else router_topk_kernel<DT, 16><<<grid, threads, lds, stream>>>(a);
-  return hipGetLastError();
+  const size_t lds = a.groups > 1 ? (size_t)kRouterWaves * a.E * sizeof(uint64_t) : 0;
+  return per_lane(a.E, [&](auto vpl) {
+    constexpr int VPL = decltype(vpl)::value;
+    a.group_size = a.E / a.groups;
+    a.group_lanes_log = -1;
+    for (int l = 0; l <= 4; ++l)
+      if (a.group_size == VPL << l) a.group_lanes_log = l;
+    router_topk_kernel<DT, VPL><<<grid, 64 * kRouterWaves, lds, stream>>>(a);
+    return hipGetLastError();
+  });
 }
 
 template <int DT>
 hipError_t grad_dt(const RouterArgs& a, const int32_t* ids, const float* grad_w, void* grad_logits,
                    hipStream_t stream) {
   const unsigned grid = (unsigned)((a.T + kRouterWaves - 1) / kRouterWaves);
-  router_grad_kernel<DT><<<grid, 64 * kRouterWaves, (size_t)kRouterWaves * a.E * sizeof(float),
-                           stream>>>(a, ids, grad_w, (uint8_t*)grad_logits);
-  return hipGetLastError();
+  return per_lane(a.E, [&](auto vpl) {
+    router_grad_kernel<DT, decltype(vpl)::value>
+        <<<grid, 64 * kRouterWaves, 0, stream>>>(a, ids, grad_w, (uint8_t*)grad_logits);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace

@@ -98,11 +98,50 @@ struct RowVec {
   }
 };
 
-// sum over the 64 lanes of a wave, in every lane; the order is fixed
+// Reductions over the 64 lanes of a wave, the same in every lane, in a fixed
+// order: four steps shift inside the rows of 16 lanes, two carry a row's
+// result to the next ones (DPP operands of the adds themselves, where a
+// shuffle would go through LDS), and lane 63's value is read back.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or(float old, float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL,
+                                                    ROWS, 0xF, false));
+}
+__device__ __forceinline__ float last_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+  v += dpp_or<0x111, 0xF>(0.0f, v);      // row_shr:1, 2, 4, 8
+  v += dpp_or<0x112, 0xF>(0.0f, v);
+  v += dpp_or<0x114, 0xF>(0.0f, v);
+  v += dpp_or<0x118, 0xF>(0.0f, v);
+  v += dpp_or<0x142, 0xA>(0.0f, v);      // row_bcast:15 into rows 1 and 3
+  v += dpp_or<0x143, 0xC>(0.0f, v);      // row_bcast:31 into rows 2 and 3
+  return last_lane(v);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define MOE_STEP(ctrl, rows) \
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xF, false))
+  MOE_STEP(0x111, 0xF);
+  MOE_STEP(0x112, 0xF);
+  MOE_STEP(0x114, 0xF);
+  MOE_STEP(0x118, 0xF);
+  MOE_STEP(0x142, 0xA);
+  MOE_STEP(0x143, 0xC);
+#undef MOE_STEP
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// fp32 values as integers of the same order; 0 is below every one of them
+__device__ __forceinline__ uint32_t ordered_bits(float f) {
+  const uint32_t b = __float_as_uint(f + 0.0f);          // -0 and +0 are equal
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u);
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return from_ordered(wave_max(ordered_bits(v)));
 }
 
 }  // namespace moe
