@@ -9,6 +9,8 @@
 // hold VPT vectors each, the row sums cross the lanes of a wave by shuffles
 // and, for BT over 64, the waves through LDS.  Everything is fp32; h is made
 // from r' before r' is rounded.
+#include <type_traits>
+
 #include "kernels.h"
 #include "row_vec.h"
 
@@ -180,53 +182,41 @@ __global__ __launch_bounds__(BT == 64 ? 256 : BT) void norm_kernel(const NormArg
 struct GradRow {
   float xs, xm;       // inverse root mean of x; mean(dh w_pre xh)
   float ys;           // inverse root mean of y (1 without a post norm)
-  float gt;           // the token's gate
 };
 
-// D, e and the gate's gradient of one column vector
-template <int DT, bool W32>
+// D, e and the addends of the column sums of one column vector, from its
+// weights (o + w, or 1) and its gate as it enters the product
+template <int N>
 __device__ __forceinline__ void grad_columns(const NormGradArgs& a, const GradRow& r,
-                                             int64_t at, int col, const float* x,
-                                             const float* dh, const float* y, float* D,
-                                             float* dpre, float* e, float* dpost, float* dg) {
-  constexpr int N = RowVec<DT>::N;
-  float w[N];
-  load_weights<DT, W32>(a.w_pre, col, a.H, a.offset, w);
+                                             const float (&x)[N], const float (&dh)[N],
+                                             const float (&y)[N], const float (&wpre)[N],
+                                             const float (&wpost)[N], const float (&g)[N],
+                                             float (&D)[N], float (&dpre)[N], float (&e)[N],
+                                             float (&dpost)[N], float (&dg)[N]) {
 #pragma unroll
   for (int c = 0; c < N; ++c) {
     const float xh = x[c] * r.xs;
     dpre[c] = dh[c] * xh;
-    if (a.dh != nullptr) D[c] = fmaf(r.xs, fmaf(dh[c], w[c], -xh * r.xm), D[c]);
+    if (a.dh != nullptr) D[c] = fmaf(r.xs, fmaf(dh[c], wpre[c], -xh * r.xm), D[c]);
   }
   if (a.y == nullptr) return;
-  float g[N];
-#pragma unroll
-  for (int c = 0; c < N; ++c) g[c] = r.gt;
-  if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull) {
-    RowVec<DT>::unpack(RowVec<DT>::template load<false>(
-                           a.gate + (a.gate_kind == kGateFull ? at : 0), col, a.H), g);
-#pragma unroll
-    for (int c = 0; c < N; ++c) g[c] = gate_value(g[c], a.gate_sigmoid);
-  }
-  load_weights<DT, W32>(a.post ? a.w_post : nullptr, col, a.H, a.offset, w);
 #pragma unroll
   for (int c = 0; c < N; ++c) {
-    const float yh = y[c] * r.ys, ad = a.alpha * D[c];
-    dg[c] = ad * (yh * w[c]);
+    const float yh = y[c] * r.ys, ad = a.alpha * D[c], adg = ad * g[c];
+    dg[c] = ad * (yh * wpost[c]);
     if (a.gate_sigmoid) dg[c] *= g[c] * (1.0f - g[c]);
-    dpost[c] = ad * g[c] * yh;
-    e[c] = ad * g[c] * w[c];
+    dpost[c] = adg * yh;
+    e[c] = adg * wpost[c];
   }
 }
 
 // s: sums of x^2, dh w_pre x and y^2, of values scaled by fx and fy
 __device__ __forceinline__ GradRow grad_row(const NormGradArgs& a, const float (&s)[3], float fx,
-                                            float fy, float gt) {
+                                            float fy) {
   GradRow r;
   r.xs = inv_rms(s[0], a.H, a.eps, fx);
   r.xm = r.xs / fx * (s[1] / (float)a.H);
   r.ys = a.post ? inv_rms(s[2], a.H, a.eps, fy) : 1.0f;
-  r.gt = gt;
   return r;
 }
 
@@ -238,24 +228,86 @@ __device__ __forceinline__ float token_gate(const NormGradArgs& a, int64_t row) 
 
 // Rows in registers: BT lanes per row, kGradThreads / BT rows side by side
 // (one for BT above), each lane with the column sums of its VPT vectors.
+//
+// One block per CU: the column sums and the next row, which is loaded while
+// this one is worked on, take the registers (FULL, a gate of the rows' own
+// shape, takes the place of the gate's column sums).  The weights and a
+// per-channel gate lie in LDS as fp32, so that nothing but rows goes through
+// the counter of loads in flight; a plane of four columns of every vector
+// after the other, 16 bytes from lane to lane.
 constexpr int kGradThreads = 512;
 constexpr int grad_groups(int bt) { return bt < kGradThreads ? kGradThreads / bt : 1; }
 
-template <int DT, bool W32, int BT, int VPT>
+template <int DT, int VPT>
+struct GradVectors {
+  u32x4_t x[VPT], dh[VPT], dr[VPT], y[VPT], gate[VPT];
+  float gt;
+
+  // the row's vectors of this lane, zeros for a row that is not there
+  template <int BT, bool FULL>
+  __device__ __forceinline__ void load(const NormGradArgs& a, int64_t row, int first) {
+    const u32x4_t zero = {0u, 0u, 0u, 0u};
+    const bool live = row < a.T;
+    const int h = live ? a.H : 0;
+    const int64_t at = row * a.H * RowVec<DT>::kSize;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int col = (first + i * BT) * RowVec<DT>::N;
+      x[i] = RowVec<DT>::template load<true>(a.x + at, col, h);
+      dh[i] = a.dh != nullptr ? RowVec<DT>::template load<true>(a.dh + at, col, h) : zero;
+      dr[i] = a.dr_in != nullptr ? RowVec<DT>::template load<true>(a.dr_in + at, col, h) : zero;
+      y[i] = a.y != nullptr ? RowVec<DT>::template load<true>(a.y + at, col, h) : zero;
+      if (FULL) gate[i] = RowVec<DT>::template load<true>(a.gate + at, col, h);
+    }
+    gt = live ? token_gate<DT>(a, row) : 0.0f;
+  }
+};
+
+template <int DT, bool W32, int BT, int VPT, bool FULL>
 __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_grad_kernel(
     const NormGradArgs a) {
-  constexpr int N = RowVec<DT>::N, G = grad_groups(BT);
+  constexpr int N = RowVec<DT>::N, G = grad_groups(BT), NV = BT * VPT;
   __shared__ float buf1[2][G][3][16], buf2[2][G][2][16], buf3[2][G][3][16];
   __shared__ float sums[G][BT * N];
+  __shared__ __align__(16) float wlds[FULL ? 2 : 3][N / 4][NV][4];   // pre, post, gate
   const int sub = threadIdx.x / BT, first = threadIdx.x % BT;
   const int64_t stride = (int64_t)gridDim.x * G;
   const int H = a.H;
   const bool has_y = a.y != nullptr;
-  float apre[VPT][N], apost[VPT][N], agate[VPT][N];
+  auto read = [&](int o, int i, float (&f)[N]) {
+#pragma unroll
+    for (int p = 0; p < N / 4; ++p) {
+      const float4 v = *reinterpret_cast<const float4*>(wlds[o][p][first + i * BT]);
+      f[4 * p] = v.x;
+      f[4 * p + 1] = v.y;
+      f[4 * p + 2] = v.z;
+      f[4 * p + 3] = v.w;
+    }
+  };
+  GradVectors<DT, VPT> cur;
+  cur.template load<BT, FULL>(a, (int64_t)blockIdx.x * G + sub, first);
+  for (int v = threadIdx.x; v < NV; v += blockDim.x) {
+    float f[3][N];
+    load_weights<DT, W32>(a.w_pre, v * N, H, a.offset, f[0]);
+    load_weights<DT, W32>(a.post ? a.w_post : nullptr, v * N, H, a.offset, f[1]);
+#pragma unroll
+    for (int c = 0; c < N; ++c) f[2][c] = 1.0f;
+    if (!FULL && has_y && a.gate_kind == kGateChannel) {
+      RowVec<DT>::unpack(RowVec<DT>::template load<false>(a.gate, v * N, H), f[2]);
+#pragma unroll
+      for (int c = 0; c < N; ++c) f[2][c] = gate_value(f[2][c], a.gate_sigmoid);
+    }
+#pragma unroll
+    for (int o = 0; o < (FULL ? 2 : 3); ++o)
+#pragma unroll
+      for (int c = 0; c < N; ++c) wlds[o][c / 4][v][c % 4] = f[o][c];
+  }
+  __syncthreads();
+  float apre[VPT][N], apost[VPT][N], agate[FULL ? 1 : VPT][N];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int c = 0; c < N; ++c) apre[i][c] = apost[i][c] = agate[i][c] = 0.0f;
+    for (int c = 0; c < N; ++c) apre[i][c] = apost[i][c] = agate[FULL ? 0 : i][c] = 0.0f;
   int turn = 0;
   // every group makes the same number of turns (the sums meet at barriers);
   // one past the last row computes on zeros and stores nothing
@@ -264,37 +316,27 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
     const bool live = row < a.T;
     const int h = live ? H : 0;               // columns of the row
     const int64_t at = row * H * RowVec<DT>::kSize;
-    u32x4_t xv[VPT], hv[VPT], dv[VPT], yv[VPT];
-    const u32x4_t zero = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int col = (first + i * BT) * N;
-      xv[i] = RowVec<DT>::template load<true>(a.x + at, col, h);
-      hv[i] = a.dh != nullptr ? RowVec<DT>::template load<true>(a.dh + at, col, h) : zero;
-      dv[i] = a.dr_in != nullptr ? RowVec<DT>::template load<true>(a.dr_in + at, col, h) : zero;
-      yv[i] = has_y ? RowVec<DT>::template load<true>(a.y + at, col, h) : zero;
-    }
+    GradVectors<DT, VPT> next;
+    next.template load<BT, FULL>(a, row + stride, first);
     float s[3] = {0.0f, 0.0f, 0.0f}, fx = 1.0f, fy = 1.0f;
-    auto add_up = [&]() {
+    auto add_up = [&](auto scaled) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int col = (first + i * BT) * N;
-        if (col >= h) continue;
         float x[N], dh[N], y[N], w[N];
-        RowVec<DT>::unpack(xv[i], x);
-        RowVec<DT>::unpack(hv[i], dh);
-        RowVec<DT>::unpack(yv[i], y);
-        load_weights<DT, W32>(a.w_pre, col, H, a.offset, w);
+        RowVec<DT>::unpack(cur.x[i], x);
+        RowVec<DT>::unpack(cur.dh[i], dh);
+        RowVec<DT>::unpack(cur.y[i], y);
+        read(0, i, w);
 #pragma unroll
         for (int c = 0; c < N; ++c) {
-          const float xc = x[c] * fx, yc = y[c] * fy;
+          const float xc = scaled ? x[c] * fx : x[c], yc = scaled ? y[c] * fy : y[c];
           s[0] = fmaf(xc, xc, s[0]);
           s[1] = fmaf(dh[c] * w[c], xc, s[1]);
           s[2] = fmaf(yc, yc, s[2]);
         }
       }
     };
-    add_up();
+    add_up(std::false_type());
     row_sums<BT, 3>(s, buf1[turn][sub]);
     bool again = s[0] > kBig || s[2] > kBig;
     if (G > 1 && BT > 64) again = __syncthreads_or(again);   // the groups meet in row_sums
@@ -302,61 +344,72 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
       fx = s[0] > kBig ? kShrink : 1.0f;
       fy = s[2] > kBig ? kShrink : 1.0f;
       s[0] = s[1] = s[2] = 0.0f;
-      add_up();
+      add_up(std::true_type());
       row_sums<BT, 3>(s, buf3[turn][sub]);
     }
-    const GradRow r = grad_row(a, s, fx, fy, live ? token_gate<DT>(a, row) : 0.0f);
+    const GradRow r = grad_row(a, s, fx, fy);
     float e[VPT][N], q[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+      __builtin_amdgcn_sched_barrier(0);      // one vector after the other: registers
       const int col = (first + i * BT) * N;
+      float x[N], dh[N], D[N], y[N], wpre[N], wpost[N], g[N], dpre[N], dpost[N], dg[N];
+      RowVec<DT>::unpack(cur.x[i], x);
+      RowVec<DT>::unpack(cur.dh[i], dh);
+      RowVec<DT>::unpack(cur.dr[i], D);
+      RowVec<DT>::unpack(cur.y[i], y);
+      read(0, i, wpre);
+      read(1, i, wpost);
+      if constexpr (FULL) {
+        RowVec<DT>::unpack(cur.gate[i], g);
 #pragma unroll
-      for (int c = 0; c < N; ++c) e[i][c] = 0.0f;
-      if (col >= h) continue;
-      float x[N], dh[N], D[N], y[N], dpre[N], dpost[N], dg[N];
-      RowVec<DT>::unpack(xv[i], x);
-      RowVec<DT>::unpack(hv[i], dh);
-      RowVec<DT>::unpack(dv[i], D);
-      RowVec<DT>::unpack(yv[i], y);
-      grad_columns<DT, W32>(a, r, at, col, x, dh, y, D, dpre, e[i], dpost, dg);
-      RowVec<DT>::template store<true>(a.dr + at, col, H, RowVec<DT>::pack(D));
+        for (int c = 0; c < N; ++c) g[c] = gate_value(g[c], a.gate_sigmoid);
+      } else {
+        read(2, i, g);
+#pragma unroll
+        for (int c = 0; c < N; ++c) g[c] *= cur.gt;
+      }
+      grad_columns<N>(a, r, x, dh, y, wpre, wpost, g, D, dpre, e[i], dpost, dg);
+      if (col < h) RowVec<DT>::template store<true>(a.dr + at, col, H, RowVec<DT>::pack(D));
 #pragma unroll
       for (int c = 0; c < N; ++c) apre[i][c] += dpre[c];
       if (!has_y) continue;
 #pragma unroll
       for (int c = 0; c < N; ++c) {
         apost[i][c] += dpost[c];
-        agate[i][c] += dg[c];
+        if constexpr (!FULL) agate[i][c] += dg[c];
         q[0] = fmaf(e[i][c], y[c] * r.ys, q[0]);
         q[1] += dg[c];
       }
-      if (a.gate_kind == kGateFull && a.d_gate != nullptr)
+      if (FULL && a.d_gate != nullptr && col < h)
         RowVec<DT>::template store<true>((uint8_t*)a.d_gate + at, col, H, RowVec<DT>::pack(dg));
     }
-    if (!has_y) continue;
-    row_sums<BT, 2>(q, buf2[turn][sub]);
-    if (live && a.gate_kind == kGateToken && a.d_gate != nullptr && first == 0)
-      ((float*)a.d_gate)[row] = q[1];
-    const float ym = a.post ? q[0] / (float)H : 0.0f;
+    if (has_y) {
+      row_sums<BT, 2>(q, buf2[turn][sub]);
+      if (live && a.gate_kind == kGateToken && a.d_gate != nullptr && first == 0)
+        ((float*)a.d_gate)[row] = q[1];
+      const float ym = a.post ? q[0] / (float)H : 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int col = (first + i * BT) * N;
-      if (col >= h) continue;
-      float y[N], d[N];
-      RowVec<DT>::unpack(yv[i], y);
+      for (int i = 0; i < VPT; ++i) {
+        const int col = (first + i * BT) * N;
+        if (col >= h) continue;
+        float y[N], d[N];
+        RowVec<DT>::unpack(cur.y[i], y);
 #pragma unroll
-      for (int c = 0; c < N; ++c) d[c] = r.ys * fmaf(-y[c] * r.ys, ym, e[i][c]);
-      RowVec<DT>::template store<true>(a.dy + at, col, H, RowVec<DT>::pack(d));
+        for (int c = 0; c < N; ++c) d[c] = r.ys * fmaf(-y[c] * r.ys, ym, e[i][c]);
+        RowVec<DT>::template store<true>(a.dy + at, col, H, RowVec<DT>::pack(d));
+      }
     }
+    cur = next;
   }
   // the groups' column sums, in group order, as the block's part
 #pragma unroll
-  for (int o = 0; o < 3; ++o) {
+  for (int o = 0; o < (FULL ? 2 : 3); ++o) {
     if (!(a.want & (1 << o))) continue;
     float* part = a.part + ((int64_t)o * gridDim.x + blockIdx.x) * H;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      float* mine = o == 0 ? apre[i] : o == 1 ? apost[i] : agate[i];
+      float* mine = o == 0 ? apre[i] : o == 1 ? apost[i] : agate[FULL ? 0 : i];
       if (G > 1) {
         __syncthreads();
 #pragma unroll
@@ -427,12 +480,27 @@ __global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(const Norm
       add_up();
       row_sums<kWideThreads, 3>(s, buf3[turn]);
     }
-    const GradRow r = grad_row(a, s, fx, fy, token_gate<DT>(a, row));
     float e[N], dpre[N], dpost[N], dg[N], q[2] = {0.0f, 0.0f};
+    const GradRow r = grad_row(a, s, fx, fy);
+    const float gt = token_gate<DT>(a, row);
+    auto columns = [&](int col) {
+      float wpre[N], wpost[N], g[N];
+      load(col);
+      load_weights<DT, W32>(a.w_pre, col, H, a.offset, wpre);
+      load_weights<DT, W32>(a.post ? a.w_post : nullptr, col, H, a.offset, wpost);
+#pragma unroll
+      for (int c = 0; c < N; ++c) g[c] = gt;
+      if (has_y && (a.gate_kind == kGateChannel || a.gate_kind == kGateFull)) {
+        RowVec<DT>::unpack(RowVec<DT>::template load<false>(
+                               a.gate + (a.gate_kind == kGateFull ? at : 0), col, H), g);
+#pragma unroll
+        for (int c = 0; c < N; ++c) g[c] = gate_value(g[c], a.gate_sigmoid);
+      }
+      grad_columns<N>(a, r, x, dh, y, wpre, wpost, g, D, dpre, e, dpost, dg);
+    };
     if (has_y) {
       for (int col = threadIdx.x * N; col < H; col += kWideThreads * N) {
-        load(col);
-        grad_columns<DT, W32>(a, r, at, col, x, dh, y, D, dpre, e, dpost, dg);
+        columns(col);
 #pragma unroll
         for (int c = 0; c < N; ++c) {
           q[0] = fmaf(e[c], y[c] * r.ys, q[0]);
@@ -446,8 +514,7 @@ __global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(const Norm
     const float ym = a.post ? q[0] / (float)H : 0.0f;
     const bool begin = row == blockIdx.x;
     for (int col = threadIdx.x * N; col < H; col += kWideThreads * N) {
-      load(col);
-      grad_columns<DT, W32>(a, r, at, col, x, dh, y, D, dpre, e, dpost, dg);
+      columns(col);
       RowVec<DT>::template store<true>(a.dr + at, col, H, RowVec<DT>::pack(D));
       if (has_y) {
         if (a.gate_kind == kGateFull && a.d_gate != nullptr)
@@ -530,12 +597,15 @@ hipError_t norm_grad_dt(const NormGradArgs& a, int blocks, hipStream_t stream) {
   const int nv = (a.H + RowVec<DT>::N - 1) / RowVec<DT>::N;
   auto go = [&](auto shape) {
     constexpr int BT = decltype(shape)::BT, VPT = decltype(shape)::VPT;
-    norm_grad_kernel<DT, W32, BT, VPT>
-        <<<blocks, BT < kGradThreads ? kGradThreads : BT, 0, stream>>>(a);
+    const int threads = BT < kGradThreads ? kGradThreads : BT;
+    if (a.y != nullptr && a.gate_kind == kGateFull)
+      norm_grad_kernel<DT, W32, BT, VPT, true><<<blocks, threads, 0, stream>>>(a);
+    else
+      norm_grad_kernel<DT, W32, BT, VPT, false><<<blocks, threads, 0, stream>>>(a);
     return hipGetLastError();
   };
   if (nv <= 64) return go(Shape<64, 1>());
-  if (nv <= 128) return go(Shape<64, 2>());
+  if (nv <= 128) return go(Shape<128, 1>());
   if (nv <= 256) return go(Shape<256, 1>());
   if (nv <= 512) return go(Shape<512, 1>());
   if (nv <= kWideVectors) return go(Shape<512, 2>());
@@ -545,7 +615,7 @@ hipError_t norm_grad_dt(const NormGradArgs& a, int blocks, hipStream_t stream) {
 
 int rows_per_block(int H, int dtype) {
   const int n = 16 / dtype_size(dtype), nv = (H + n - 1) / n;
-  return nv <= 128 ? grad_groups(64) : nv <= 256 ? grad_groups(256) : 1;
+  return grad_groups(nv <= 64 ? 64 : nv <= 128 ? 128 : nv <= 256 ? 256 : 512);
 }
 
 }  // namespace
