@@ -49,27 +49,39 @@ __device__ __forceinline__ float inv_rms(float sum, int H, float eps, float f) {
   return f / sqrtf(sum / (float)H + eps * f * f);
 }
 
-// weights of columns [col, col + N): of the rows' type or fp32; o + w
-template <int DT, bool W32, int N>
+// weights of columns [col, col + N): of the rows' type or fp32; o + w, or 1
+// without a weight (columns past the end: o)
+template <class RV, bool W32>
 __device__ __forceinline__ void load_weights(const void* w, int col, int H, float o,
-                                             float (&f)[N]) {
+                                             float (&f)[RV::N]) {
+  constexpr int N = RV::N;
   if (w == nullptr) {
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = 1.0f;
     return;
   }
-  if (W32 && DT != kF32) {
-    float a[4], b[4];
-    const uint8_t* p = (const uint8_t*)w;
-    RowVec<kF32>::unpack(RowVec<kF32>::template load<false>(p, col, H), a);
-    RowVec<kF32>::unpack(RowVec<kF32>::template load<false>(p, col + 4, H), b);
+  const uint8_t* p = (const uint8_t*)w;
+  if constexpr (W32 && N == 8) {                  // two fp32 vectors
+    const int c = RV::inside(col, H);
+    u32x4_t a = RowVec<kF32>::template load_at<false>(p, c);
+    u32x4_t b = RowVec<kF32>::template load_at<false>(p, c + 4);
+    const int k = col - c;                        // shifted in place as rows are
+    RowVec<kF32>::unpack(a, f);
+    RowVec<kF32>::unpack(b, f + 4);
+    if (k > 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = o + (i < 4 ? a[i & 3] : b[i & 3]);
+      for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = (k & d) ? (i + d < 8 ? f[(i + d) & 7] : 0.0f) : f[i];
+    }
   } else {
-    RowVec<DT>::unpack(RowVec<DT>::template load<false>((const uint8_t*)w, col, H), f);
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] += o;
+    typedef std::conditional_t<W32 && N == 1, RowOne<kF32>, RV> WV;
+    typename WV::Raw v = WV::template load<false>(p, col, H);
+    WV::settle(v, col, H);
+    WV::unpack(v, f);
   }
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] += o;
 }
 
 __device__ __forceinline__ float gate_value(float g, bool sigmoid) {
@@ -101,52 +113,59 @@ __device__ __forceinline__ float row_inv_rms(F&& value, int H, float eps, float 
   return inv_rms(s[0], H, eps, f);
 }
 
-template <int DT, bool W32, int BT, int VPT>
+template <class RV, bool W32, int BT, int VPT>
 __global__ __launch_bounds__(BT == 64 ? 256 : BT) void norm_kernel(const NormArgs a) {
-  constexpr int N = RowVec<DT>::N;
+  constexpr int N = RV::N;
   __shared__ float buf[4][1][16];
   const int64_t row = BT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (row >= a.T) return;                       // whole waves (BT 64) or never
   const int first = BT == 64 ? threadIdx.x & 63 : threadIdx.x;
   const int H = a.H;
-  const int64_t at = row * H * RowVec<DT>::kSize;
-  u32x4_t rv[VPT], yv[VPT];
+  const int64_t at = row * H * RV::kSize;
+  typename RV::Raw rv[VPT], yv[VPT];
   float x[VPT][N];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int col = (first + i * BT) * N;
-    rv[i] = RowVec<DT>::template load<true>(a.r + at, col, H);
-    if (a.y != nullptr) yv[i] = RowVec<DT>::template load<true>(a.y + at, col, H);
+    rv[i] = RV::template load<true>(a.r + at, col, H);
+    if (a.y != nullptr) yv[i] = RV::template load<true>(a.y + at, col, H);
   }
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) RowVec<DT>::unpack(rv[i], x[i]);
+  for (int i = 0; i < VPT; ++i) {
+    const int col = (first + i * BT) * N;
+    RV::settle(rv[i], col, H);
+    RV::unpack(rv[i], x[i]);
+    if (a.y != nullptr) RV::settle(yv[i], col, H);
+  }
   if (a.y != nullptr) {
     float ys = 1.0f;
     if (a.post)
-      ys = row_inv_rms<BT, VPT, N>([&](int i, float* v) { RowVec<DT>::unpack(yv[i], v); }, H,
+      ys = row_inv_rms<BT, VPT, N>([&](int i, float* v) { RV::unpack(yv[i], v); }, H,
                                    a.eps, buf);
     float gt = 1.0f;
     if (a.gate_kind == kGateToken)
-      gt = gate_value(RowVec<DT>::load_one(a.gate, row), a.gate_sigmoid);
+      gt = gate_value(RV::load_one(a.gate, row), a.gate_sigmoid);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int col = (first + i * BT) * N;
       if (col >= H) continue;
       float y[N], w[N], g[N];
-      RowVec<DT>::unpack(yv[i], y);
-      load_weights<DT, W32>(a.post ? a.w_post : nullptr, col, H, a.offset, w);
+      RV::unpack(yv[i], y);
+      load_weights<RV, W32>(a.post ? a.w_post : nullptr, col, H, a.offset, w);
 #pragma unroll
       for (int c = 0; c < N; ++c) g[c] = gt;
       if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull) {
-        RowVec<DT>::unpack(RowVec<DT>::template load<false>(
-                               a.gate + (a.gate_kind == kGateFull ? at : 0), col, H), g);
+        typename RV::Raw gv =
+            RV::template load<false>(a.gate + (a.gate_kind == kGateFull ? at : 0), col, H);
+        RV::settle(gv, col, H);
+        RV::unpack(gv, g);
 #pragma unroll
         for (int c = 0; c < N; ++c) g[c] = gate_value(g[c], a.gate_sigmoid);
       }
 #pragma unroll
       for (int c = 0; c < N; ++c)
         x[i][c] = col + c < H ? fmaf(a.alpha * g[c], y[c] * ys * w[c], x[i][c]) : 0.0f;
-      RowVec<DT>::template store<true>(a.r_out + at, col, H, RowVec<DT>::pack(x[i]));
+      RV::template store<true>(a.r_out + at, col, H, RV::pack(x[i]));
     }
   }
   if (a.h == nullptr) return;
@@ -161,10 +180,10 @@ __global__ __launch_bounds__(BT == 64 ? 256 : BT) void norm_kernel(const NormArg
     const int col = (first + i * BT) * N;
     if (col >= H) continue;
     float w[N], h[N];
-    load_weights<DT, W32>(a.w_pre, col, H, a.offset, w);
+    load_weights<RV, W32>(a.w_pre, col, H, a.offset, w);
 #pragma unroll
     for (int c = 0; c < N; ++c) h[c] = x[i][c] * xs * w[c];
-    RowVec<DT>::template store<true>(a.h + at, col, H, RowVec<DT>::pack(h));
+    RV::template store<true>(a.h + at, col, H, RV::pack(h));
   }
 }
 
@@ -186,7 +205,7 @@ struct GradRow {
 
 // D, e and the addends of the column sums of one column vector, from its
 // weights (o + w, or 1) and its gate as it enters the product
-template <int N>
+template <int N, bool HAS_Y>
 __device__ __forceinline__ void grad_columns(const NormGradArgs& a, const GradRow& r,
                                              const float (&x)[N], const float (&dh)[N],
                                              const float (&y)[N], const float (&wpre)[N],
@@ -197,9 +216,9 @@ __device__ __forceinline__ void grad_columns(const NormGradArgs& a, const GradRo
   for (int c = 0; c < N; ++c) {
     const float xh = x[c] * r.xs;
     dpre[c] = dh[c] * xh;
-    if (a.dh != nullptr) D[c] = fmaf(r.xs, fmaf(dh[c], wpre[c], -xh * r.xm), D[c]);
+    D[c] = fmaf(r.xs, fmaf(dh[c], wpre[c], -xh * r.xm), D[c]);
   }
-  if (a.y == nullptr) return;
+  if (!HAS_Y) return;
 #pragma unroll
   for (int c = 0; c < N; ++c) {
     const float yh = y[c] * r.ys, ad = a.alpha * D[c], adg = ad * g[c];
@@ -220,10 +239,10 @@ __device__ __forceinline__ GradRow grad_row(const NormGradArgs& a, const float (
   return r;
 }
 
-template <int DT>
+template <class RV>
 __device__ __forceinline__ float token_gate(const NormGradArgs& a, int64_t row) {
   return a.y != nullptr && a.gate_kind == kGateToken
-             ? gate_value(RowVec<DT>::load_one(a.gate, row), a.gate_sigmoid) : 1.0f;
+             ? gate_value(RV::load_one(a.gate, row), a.gate_sigmoid) : 1.0f;
 }
 
 // Rows in registers: BT lanes per row, kGradThreads / BT rows side by side
@@ -238,76 +257,103 @@ __device__ __forceinline__ float token_gate(const NormGradArgs& a, int64_t row) 
 constexpr int kGradThreads = 512;
 constexpr int grad_groups(int bt) { return bt < kGradThreads ? kGradThreads / bt : 1; }
 
-template <int DT, int VPT>
-struct GradVectors {
-  u32x4_t x[VPT], dh[VPT], dr[VPT], y[VPT], gate[VPT];
-  float gt;
+// Every load is issued whatever the call leaves out: how many loads follow
+// one is then known, and waiting for this row's leaves the next row's in
+// flight (a null gradient's loads go to x and are dropped).
+enum GradForm { kNoBlock, kBlock, kBlockFullGate };
 
-  // the row's vectors of this lane, zeros for a row that is not there
-  template <int BT, bool FULL>
+template <class RV, int VPT, GradForm FORM>
+struct GradVectors {
+  typename RV::Raw x[VPT], dh[VPT], dr[VPT], y[VPT], gate[VPT];
+  float gt;                                   // the token's gate as stored
+
+  // the row's vectors of this lane (the last row's for one past it)
+  template <int BT>
   __device__ __forceinline__ void load(const NormGradArgs& a, int64_t row, int first) {
-    const u32x4_t zero = {0u, 0u, 0u, 0u};
-    const bool live = row < a.T;
-    const int h = live ? a.H : 0;
-    const int64_t at = row * a.H * RowVec<DT>::kSize;
+    if (row >= a.T) row = a.T - 1;
+    const int64_t at = row * a.H * RV::kSize;
+    const uint8_t* pdh = a.dh != nullptr ? a.dh : a.x;
+    const uint8_t* pdr = a.dr_in != nullptr ? a.dr_in : a.x;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int col = (first + i * BT) * RowVec<DT>::N;
-      x[i] = RowVec<DT>::template load<true>(a.x + at, col, h);
-      dh[i] = a.dh != nullptr ? RowVec<DT>::template load<true>(a.dh + at, col, h) : zero;
-      dr[i] = a.dr_in != nullptr ? RowVec<DT>::template load<true>(a.dr_in + at, col, h) : zero;
-      y[i] = a.y != nullptr ? RowVec<DT>::template load<true>(a.y + at, col, h) : zero;
-      if (FULL) gate[i] = RowVec<DT>::template load<true>(a.gate + at, col, h);
+      const int col = (first + i * BT) * RV::N;
+      x[i] = RV::template load<true>(a.x + at, col, a.H);
+      dh[i] = RV::template load<true>(pdh + at, col, a.H);
+      dr[i] = RV::template load<true>(pdr + at, col, a.H);
+      if (FORM != kNoBlock) y[i] = RV::template load<true>(a.y + at, col, a.H);
+      if (FORM == kBlockFullGate) gate[i] = RV::template load<true>(a.gate + at, col, a.H);
     }
-    gt = live ? token_gate<DT>(a, row) : 0.0f;
+    if (FORM == kBlock) {
+      const bool token = a.gate_kind == kGateToken;
+      gt = RV::load_one(token ? a.gate : a.x, token ? row : 0);
+    }
+  }
+  // zeros past the row's h columns (0: a row that is not there) and for what
+  // the call leaves out
+  template <int BT>
+  __device__ __forceinline__ void settle(const NormGradArgs& a, int first, int h) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int col = (first + i * BT) * RV::N;
+      if (a.dh == nullptr) dh[i] = typename RV::Raw{};
+      if (a.dr_in == nullptr) dr[i] = typename RV::Raw{};
+      if (col + RV::N <= h) continue;
+      RV::settle(x[i], col, h);
+      RV::settle(dh[i], col, h);
+      RV::settle(dr[i], col, h);
+      if (FORM != kNoBlock) RV::settle(y[i], col, h);
+      if (FORM == kBlockFullGate) RV::settle(gate[i], col, h);
+    }
   }
 };
 
-template <int DT, bool W32, int BT, int VPT, bool FULL>
+template <class RV, bool W32, int BT, int VPT, GradForm FORM>
 __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_grad_kernel(
     const NormGradArgs a) {
-  constexpr int N = RowVec<DT>::N, G = grad_groups(BT), NV = BT * VPT;
+  constexpr int N = RV::N, G = grad_groups(BT), NV = BT * VPT;
+  constexpr int P = N < 4 ? N : 4;            // columns of a plane
+  constexpr bool HAS_Y = FORM != kNoBlock, FULL = FORM == kBlockFullGate;
+  constexpr int SUMS = FORM == kNoBlock ? 1 : FULL ? 2 : 3;   // column sums: pre, post, gate
   __shared__ float buf1[2][G][3][16], buf2[2][G][2][16], buf3[2][G][3][16];
   __shared__ float sums[G][BT * N];
-  __shared__ __align__(16) float wlds[FULL ? 2 : 3][N / 4][NV][4];   // pre, post, gate
+  __shared__ __align__(16) float wlds[SUMS][N / P][NV][P];   // pre, post, gate
   const int sub = threadIdx.x / BT, first = threadIdx.x % BT;
   const int64_t stride = (int64_t)gridDim.x * G;
   const int H = a.H;
-  const bool has_y = a.y != nullptr;
   auto read = [&](int o, int i, float (&f)[N]) {
 #pragma unroll
-    for (int p = 0; p < N / 4; ++p) {
-      const float4 v = *reinterpret_cast<const float4*>(wlds[o][p][first + i * BT]);
-      f[4 * p] = v.x;
-      f[4 * p + 1] = v.y;
-      f[4 * p + 2] = v.z;
-      f[4 * p + 3] = v.w;
-    }
+    for (int p = 0; p < N / P; ++p)
+#pragma unroll
+      for (int c = 0; c < P; ++c) f[P * p + c] = wlds[o][p][first + i * BT][c];
   };
-  GradVectors<DT, VPT> cur;
-  cur.template load<BT, FULL>(a, (int64_t)blockIdx.x * G + sub, first);
+  GradVectors<RV, VPT, FORM> cur;
+  cur.template load<BT>(a, (int64_t)blockIdx.x * G + sub, first);
   for (int v = threadIdx.x; v < NV; v += blockDim.x) {
     float f[3][N];
-    load_weights<DT, W32>(a.w_pre, v * N, H, a.offset, f[0]);
-    load_weights<DT, W32>(a.post ? a.w_post : nullptr, v * N, H, a.offset, f[1]);
+    load_weights<RV, W32>(a.w_pre, v * N, H, a.offset, f[0]);
+    load_weights<RV, W32>(a.post ? a.w_post : nullptr, v * N, H, a.offset, f[1]);
 #pragma unroll
     for (int c = 0; c < N; ++c) f[2][c] = 1.0f;
-    if (!FULL && has_y && a.gate_kind == kGateChannel) {
-      RowVec<DT>::unpack(RowVec<DT>::template load<false>(a.gate, v * N, H), f[2]);
+    if (FORM == kBlock && a.gate_kind == kGateChannel) {
+      typename RV::Raw gv = RV::template load<false>(a.gate, v * N, H);
+      RV::settle(gv, v * N, H);
+      RV::unpack(gv, f[2]);
 #pragma unroll
       for (int c = 0; c < N; ++c) f[2][c] = gate_value(f[2][c], a.gate_sigmoid);
     }
 #pragma unroll
-    for (int o = 0; o < (FULL ? 2 : 3); ++o)
+    for (int o = 0; o < SUMS; ++o)
 #pragma unroll
-      for (int c = 0; c < N; ++c) wlds[o][c / 4][v][c % 4] = f[o][c];
+      for (int c = 0; c < N; ++c) wlds[o][c / P][v][c % P] = f[o][c];
   }
   __syncthreads();
-  float apre[VPT][N], apost[VPT][N], agate[FULL ? 1 : VPT][N];
+  __builtin_amdgcn_s_waitcnt(0);              // the first row, once
+  constexpr int VP = SUMS > 1 ? VPT : 1, VG = SUMS > 2 ? VPT : 1;
+  float apre[VPT][N], apost[VP][N], agate[VG][N];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int c = 0; c < N; ++c) apre[i][c] = apost[i][c] = agate[FULL ? 0 : i][c] = 0.0f;
+    for (int c = 0; c < N; ++c) apre[i][c] = apost[i % VP][c] = agate[i % VG][c] = 0.0f;
   int turn = 0;
   // every group makes the same number of turns (the sums meet at barriers);
   // one past the last row computes on zeros and stores nothing
@@ -315,24 +361,28 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
     const int64_t row = row0 + sub;
     const bool live = row < a.T;
     const int h = live ? H : 0;               // columns of the row
-    const int64_t at = row * H * RowVec<DT>::kSize;
-    GradVectors<DT, VPT> next;
-    next.template load<BT, FULL>(a, row + stride, first);
+    const int64_t at = row * H * RV::kSize;
+    GradVectors<RV, VPT, FORM> next;
+    next.template load<BT>(a, row + stride, first);
+    cur.template settle<BT>(a, first, h);
     float s[3] = {0.0f, 0.0f, 0.0f}, fx = 1.0f, fy = 1.0f;
     auto add_up = [&](auto scaled) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         float x[N], dh[N], y[N], w[N];
-        RowVec<DT>::unpack(cur.x[i], x);
-        RowVec<DT>::unpack(cur.dh[i], dh);
-        RowVec<DT>::unpack(cur.y[i], y);
+        RV::unpack(cur.x[i], x);
+        RV::unpack(cur.dh[i], dh);
+        if (HAS_Y) RV::unpack(cur.y[i], y);
         read(0, i, w);
 #pragma unroll
         for (int c = 0; c < N; ++c) {
-          const float xc = scaled ? x[c] * fx : x[c], yc = scaled ? y[c] * fy : y[c];
+          const float xc = scaled ? x[c] * fx : x[c];
           s[0] = fmaf(xc, xc, s[0]);
           s[1] = fmaf(dh[c] * w[c], xc, s[1]);
-          s[2] = fmaf(yc, yc, s[2]);
+          if (HAS_Y) {
+            const float yc = scaled ? y[c] * fy : y[c];
+            s[2] = fmaf(yc, yc, s[2]);
+          }
         }
       }
     };
@@ -348,43 +398,47 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
       row_sums<BT, 3>(s, buf3[turn][sub]);
     }
     const GradRow r = grad_row(a, s, fx, fy);
+    const float gt = FORM == kBlock && a.gate_kind == kGateToken
+                         ? gate_value(cur.gt, a.gate_sigmoid) : 1.0f;
     float e[VPT][N], q[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       __builtin_amdgcn_sched_barrier(0);      // one vector after the other: registers
       const int col = (first + i * BT) * N;
       float x[N], dh[N], D[N], y[N], wpre[N], wpost[N], g[N], dpre[N], dpost[N], dg[N];
-      RowVec<DT>::unpack(cur.x[i], x);
-      RowVec<DT>::unpack(cur.dh[i], dh);
-      RowVec<DT>::unpack(cur.dr[i], D);
-      RowVec<DT>::unpack(cur.y[i], y);
+      RV::unpack(cur.x[i], x);
+      RV::unpack(cur.dh[i], dh);
+      RV::unpack(cur.dr[i], D);
       read(0, i, wpre);
-      read(1, i, wpost);
-      if constexpr (FULL) {
-        RowVec<DT>::unpack(cur.gate[i], g);
+      if constexpr (HAS_Y) {
+        RV::unpack(cur.y[i], y);
+        read(1, i, wpost);
+        if constexpr (FULL) {
+          RV::unpack(cur.gate[i], g);
 #pragma unroll
-        for (int c = 0; c < N; ++c) g[c] = gate_value(g[c], a.gate_sigmoid);
-      } else {
-        read(2, i, g);
+          for (int c = 0; c < N; ++c) g[c] = gate_value(g[c], a.gate_sigmoid);
+        } else {
+          read(2, i, g);
 #pragma unroll
-        for (int c = 0; c < N; ++c) g[c] *= cur.gt;
+          for (int c = 0; c < N; ++c) g[c] *= gt;
+        }
       }
-      grad_columns<N>(a, r, x, dh, y, wpre, wpost, g, D, dpre, e[i], dpost, dg);
-      if (col < h) RowVec<DT>::template store<true>(a.dr + at, col, H, RowVec<DT>::pack(D));
+      grad_columns<N, HAS_Y>(a, r, x, dh, y, wpre, wpost, g, D, dpre, e[i], dpost, dg);
+      if (col < h) RV::template store<true>(a.dr + at, col, H, RV::pack(D));
 #pragma unroll
       for (int c = 0; c < N; ++c) apre[i][c] += dpre[c];
-      if (!has_y) continue;
+      if constexpr (!HAS_Y) continue;
 #pragma unroll
       for (int c = 0; c < N; ++c) {
-        apost[i][c] += dpost[c];
-        if constexpr (!FULL) agate[i][c] += dg[c];
+        apost[i % VP][c] += dpost[c];
+        agate[i % VG][c] += FULL ? 0.0f : dg[c];
         q[0] = fmaf(e[i][c], y[c] * r.ys, q[0]);
         q[1] += dg[c];
       }
       if (FULL && a.d_gate != nullptr && col < h)
-        RowVec<DT>::template store<true>((uint8_t*)a.d_gate + at, col, H, RowVec<DT>::pack(dg));
+        RV::template store<true>((uint8_t*)a.d_gate + at, col, H, RV::pack(dg));
     }
-    if (has_y) {
+    if constexpr (HAS_Y) {
       row_sums<BT, 2>(q, buf2[turn][sub]);
       if (live && a.gate_kind == kGateToken && a.d_gate != nullptr && first == 0)
         ((float*)a.d_gate)[row] = q[1];
@@ -394,22 +448,22 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
         const int col = (first + i * BT) * N;
         if (col >= h) continue;
         float y[N], d[N];
-        RowVec<DT>::unpack(cur.y[i], y);
+        RV::unpack(cur.y[i], y);
 #pragma unroll
         for (int c = 0; c < N; ++c) d[c] = r.ys * fmaf(-y[c] * r.ys, ym, e[i][c]);
-        RowVec<DT>::template store<true>(a.dy + at, col, H, RowVec<DT>::pack(d));
+        RV::template store<true>(a.dy + at, col, H, RV::pack(d));
       }
     }
     cur = next;
   }
   // the groups' column sums, in group order, as the block's part
 #pragma unroll
-  for (int o = 0; o < (FULL ? 2 : 3); ++o) {
+  for (int o = 0; o < SUMS; ++o) {
     if (!(a.want & (1 << o))) continue;
     float* part = a.part + ((int64_t)o * gridDim.x + blockIdx.x) * H;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      float* mine = o == 0 ? apre[i] : o == 1 ? apost[i] : agate[FULL ? 0 : i];
+      float* mine = o == 0 ? apre[i] : o == 1 ? apost[i % VP] : agate[i % VG];
       if (G > 1) {
         __syncthreads();
 #pragma unroll
@@ -437,31 +491,34 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
 // to write.  The block's column sums are kept in its part itself.
 constexpr int kWideThreads = 1024;
 
-template <int DT, bool W32>
+template <class RV, bool W32>
 __global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(const NormGradArgs a) {
-  constexpr int N = RowVec<DT>::N;
+  constexpr int N = RV::N;
   __shared__ float buf1[2][3][16], buf2[2][2][16], buf3[2][3][16];
   const int H = a.H;
   const bool has_y = a.y != nullptr;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
-    const int64_t at = row * H * RowVec<DT>::kSize;
+    const int64_t at = row * H * RV::kSize;
     float x[N], dh[N], D[N], y[N];
     auto load = [&](int col) {
-      const u32x4_t zero = {0u, 0u, 0u, 0u};
-      RowVec<DT>::unpack(RowVec<DT>::template load<false>(a.x + at, col, H), x);
-      RowVec<DT>::unpack(
-          a.dh != nullptr ? RowVec<DT>::template load<false>(a.dh + at, col, H) : zero, dh);
-      RowVec<DT>::unpack(
-          a.dr_in != nullptr ? RowVec<DT>::template load<false>(a.dr_in + at, col, H) : zero, D);
-      RowVec<DT>::unpack(has_y ? RowVec<DT>::template load<false>(a.y + at, col, H) : zero, y);
+      auto one = [&](const uint8_t* p, float (&f)[N]) {
+        typename RV::Raw v = {};
+        if (p != nullptr) v = RV::template load<false>(p + at, col, H);
+        RV::settle(v, col, H);
+        RV::unpack(v, f);
+      };
+      one(a.x, x);
+      one(a.dh, dh);
+      one(a.dr_in, D);
+      one(a.y, y);
     };
     float s[3] = {0.0f, 0.0f, 0.0f}, fx = 1.0f, fy = 1.0f;
     auto add_up = [&]() {
       for (int col = threadIdx.x * N; col < H; col += kWideThreads * N) {
         float w[N];
         load(col);
-        load_weights<DT, W32>(a.w_pre, col, H, a.offset, w);
+        load_weights<RV, W32>(a.w_pre, col, H, a.offset, w);
 #pragma unroll
         for (int c = 0; c < N; ++c) {
           const float xc = x[c] * fx, yc = y[c] * fy;
@@ -482,21 +539,24 @@ __global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(const Norm
     }
     float e[N], dpre[N], dpost[N], dg[N], q[2] = {0.0f, 0.0f};
     const GradRow r = grad_row(a, s, fx, fy);
-    const float gt = token_gate<DT>(a, row);
+    const float gt = token_gate<RV>(a, row);
     auto columns = [&](int col) {
       float wpre[N], wpost[N], g[N];
       load(col);
-      load_weights<DT, W32>(a.w_pre, col, H, a.offset, wpre);
-      load_weights<DT, W32>(a.post ? a.w_post : nullptr, col, H, a.offset, wpost);
+      load_weights<RV, W32>(a.w_pre, col, H, a.offset, wpre);
+      load_weights<RV, W32>(a.post ? a.w_post : nullptr, col, H, a.offset, wpost);
 #pragma unroll
       for (int c = 0; c < N; ++c) g[c] = gt;
       if (has_y && (a.gate_kind == kGateChannel || a.gate_kind == kGateFull)) {
-        RowVec<DT>::unpack(RowVec<DT>::template load<false>(
-                               a.gate + (a.gate_kind == kGateFull ? at : 0), col, H), g);
+        typename RV::Raw gv =
+            RV::template load<false>(a.gate + (a.gate_kind == kGateFull ? at : 0), col, H);
+        RV::settle(gv, col, H);
+        RV::unpack(gv, g);
 #pragma unroll
         for (int c = 0; c < N; ++c) g[c] = gate_value(g[c], a.gate_sigmoid);
       }
-      grad_columns<N>(a, r, x, dh, y, wpre, wpost, g, D, dpre, e, dpost, dg);
+      if (has_y) grad_columns<N, true>(a, r, x, dh, y, wpre, wpost, g, D, dpre, e, dpost, dg);
+      else grad_columns<N, false>(a, r, x, dh, y, wpre, wpost, g, D, dpre, e, dpost, dg);
     };
     if (has_y) {
       for (int col = threadIdx.x * N; col < H; col += kWideThreads * N) {
@@ -515,14 +575,14 @@ __global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(const Norm
     const bool begin = row == blockIdx.x;
     for (int col = threadIdx.x * N; col < H; col += kWideThreads * N) {
       columns(col);
-      RowVec<DT>::template store<true>(a.dr + at, col, H, RowVec<DT>::pack(D));
+      RV::template store<true>(a.dr + at, col, H, RV::pack(D));
       if (has_y) {
         if (a.gate_kind == kGateFull && a.d_gate != nullptr)
-          RowVec<DT>::template store<true>((uint8_t*)a.d_gate + at, col, H,
-                                           RowVec<DT>::pack(dg));
+          RV::template store<true>((uint8_t*)a.d_gate + at, col, H,
+                                           RV::pack(dg));
 #pragma unroll
         for (int c = 0; c < N; ++c) e[c] = r.ys * fmaf(-y[c] * r.ys, ym, e[c]);
-        RowVec<DT>::template store<true>(a.dy + at, col, H, RowVec<DT>::pack(e));
+        RV::template store<true>(a.dy + at, col, H, RV::pack(e));
       }
 #pragma unroll
       for (int o = 0; o < 3; ++o) {
@@ -564,8 +624,9 @@ __global__ __launch_bounds__(kSumCols* kSumWays) void grad_sum_kernel(const floa
   out[c] = s;
 }
 
-template <int B, int V>
+template <class R, int B, int V>
 struct Shape {
+  typedef R RV;
   static constexpr int BT = B, VPT = V;       // lanes per row, vectors per lane
 };
 
@@ -574,18 +635,20 @@ hipError_t norm_dt(const NormArgs& a, hipStream_t stream) {
   const int nv = (a.H + RowVec<DT>::N - 1) / RowVec<DT>::N;
   auto go = [&](auto shape) {
     constexpr int BT = decltype(shape)::BT, VPT = decltype(shape)::VPT;
+    typedef typename decltype(shape)::RV RV;
     const int64_t grid = BT == 64 ? (a.T + 3) / 4 : a.T;
-    norm_kernel<DT, W32, BT, VPT><<<(unsigned)grid, BT == 64 ? 256 : BT, 0, stream>>>(a);
+    norm_kernel<RV, W32, BT, VPT><<<(unsigned)grid, BT == 64 ? 256 : BT, 0, stream>>>(a);
     return hipGetLastError();
   };
-  if (nv <= 64) return go(Shape<64, 1>());
-  if (nv <= 128) return go(Shape<64, 2>());
-  if (nv <= 256) return go(Shape<64, 4>());
-  if (nv <= 512) return go(Shape<256, 2>());
-  if (nv <= 1024) return go(Shape<256, 4>());
-  if (nv <= 2048) return go(Shape<512, 4>());
-  if (nv <= 4096) return go(Shape<1024, 4>());
-  if constexpr (DT == kF32) return go(Shape<1024, 8>());
+  if (a.H < RowVec<DT>::N) return go(Shape<RowOne<DT>, 64, 1>());
+  if (nv <= 64) return go(Shape<RowVec<DT>, 64, 1>());
+  if (nv <= 128) return go(Shape<RowVec<DT>, 64, 2>());
+  if (nv <= 256) return go(Shape<RowVec<DT>, 64, 4>());
+  if (nv <= 512) return go(Shape<RowVec<DT>, 256, 2>());
+  if (nv <= 1024) return go(Shape<RowVec<DT>, 256, 4>());
+  if (nv <= 2048) return go(Shape<RowVec<DT>, 512, 4>());
+  if (nv <= 4096) return go(Shape<RowVec<DT>, 1024, 4>());
+  if constexpr (DT == kF32) return go(Shape<RowVec<DT>, 1024, 8>());
   return hipErrorInvalidValue;                // 2-byte rows end at 4096 vectors
 }
 
@@ -597,19 +660,23 @@ hipError_t norm_grad_dt(const NormGradArgs& a, int blocks, hipStream_t stream) {
   const int nv = (a.H + RowVec<DT>::N - 1) / RowVec<DT>::N;
   auto go = [&](auto shape) {
     constexpr int BT = decltype(shape)::BT, VPT = decltype(shape)::VPT;
+    typedef typename decltype(shape)::RV RV;
     const int threads = BT < kGradThreads ? kGradThreads : BT;
-    if (a.y != nullptr && a.gate_kind == kGateFull)
-      norm_grad_kernel<DT, W32, BT, VPT, true><<<blocks, threads, 0, stream>>>(a);
+    if (a.y == nullptr)
+      norm_grad_kernel<RV, W32, BT, VPT, kNoBlock><<<blocks, threads, 0, stream>>>(a);
+    else if (a.gate_kind == kGateFull)
+      norm_grad_kernel<RV, W32, BT, VPT, kBlockFullGate><<<blocks, threads, 0, stream>>>(a);
     else
-      norm_grad_kernel<DT, W32, BT, VPT, false><<<blocks, threads, 0, stream>>>(a);
+      norm_grad_kernel<RV, W32, BT, VPT, kBlock><<<blocks, threads, 0, stream>>>(a);
     return hipGetLastError();
   };
-  if (nv <= 64) return go(Shape<64, 1>());
-  if (nv <= 128) return go(Shape<128, 1>());
-  if (nv <= 256) return go(Shape<256, 1>());
-  if (nv <= 512) return go(Shape<512, 1>());
-  if (nv <= kWideVectors) return go(Shape<512, 2>());
-  norm_grad_wide_kernel<DT, W32><<<blocks, kWideThreads, 0, stream>>>(a);
+  if (a.H < RowVec<DT>::N) return go(Shape<RowOne<DT>, 64, 1>());
+  if (nv <= 64) return go(Shape<RowVec<DT>, 64, 1>());
+  if (nv <= 128) return go(Shape<RowVec<DT>, 128, 1>());
+  if (nv <= 256) return go(Shape<RowVec<DT>, 256, 1>());
+  if (nv <= 512) return go(Shape<RowVec<DT>, 512, 1>());
+  if (nv <= kWideVectors) return go(Shape<RowVec<DT>, 512, 2>());
+  norm_grad_wide_kernel<RowVec<DT>, W32><<<blocks, kWideThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

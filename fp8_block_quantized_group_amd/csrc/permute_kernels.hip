@@ -118,39 +118,42 @@ __device__ __forceinline__ Place place(int log_width, int pieces) {
                (int)(piece << log_width) + (int)(threadIdx.x & ((1 << log_width) - 1))};
 }
 
+// A lane's column where its vector would pass the row's end: the row's last
+// N columns.  The columns that the lane before it has too come out the same
+// from both.
+
 // 4: the rows themselves: a token's vector is read once and written to the
 // rows of its routed slots
-template <int DT>
+template <class RV>
 __global__ __launch_bounds__(256) void permute_rows_kernel(const RowsArgs a, int log_width,
                                                            int pieces) {
   const Place p = place(log_width, pieces);
-  const int col = p.v * RowVec<DT>::N;
-  if (p.t >= a.T || col >= a.H) return;
-  const int64_t pitch = (int64_t)a.H * RowVec<DT>::kSize;
-  const u32x4_t v = RowVec<DT>::template load<true>(a.in + p.t * pitch, col, a.H);
+  if (p.t >= a.T || p.v * RV::N >= a.H) return;
+  const int col = RV::inside(p.v * RV::N, a.H);
+  const int64_t pitch = (int64_t)a.H * RV::kSize;
+  const typename RV::Raw v = RV::template load_at<true>(a.in + p.t * pitch, col);
   for (int j = 0; j < a.k; ++j) {
     const int r = a.slot_row[p.t * a.k + j];
-    if (r >= 0 && r < a.slots)
-      RowVec<DT>::template store<true>(a.out + r * pitch, col, a.H, v);
+    if (r >= 0 && r < a.slots) RV::template store_at<true>(a.out + r * pitch, col, v);
   }
 }
 
 // the sum of a token's rows, weighted when weights are given
-template <int DT>
+template <class RV>
 __global__ __launch_bounds__(256) void combine_rows_kernel(const RowsArgs a, int log_width,
                                                            int pieces) {
-  constexpr int N = RowVec<DT>::N;
+  constexpr int N = RV::N;
   const Place p = place(log_width, pieces);
-  const int col = p.v * N;
-  if (p.t >= a.T || col >= a.H) return;
-  const int64_t pitch = (int64_t)a.H * RowVec<DT>::kSize;
+  if (p.t >= a.T || p.v * N >= a.H) return;
+  const int col = RV::inside(p.v * N, a.H);
+  const int64_t pitch = (int64_t)a.H * RV::kSize;
   float acc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = 0.0f;
   for (int j0 = 0; j0 < a.k; j0 += 8) {
     int r[8];
     float w[8];
-    u32x4_t v[8];
+    typename RV::Raw v[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       r[u] = -1;
@@ -163,33 +166,33 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(const RowsArgs a, int
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      if (r[u] >= 0) v[u] = RowVec<DT>::template load<true>(a.in + r[u] * pitch, col, a.H);
+      if (r[u] >= 0) v[u] = RV::template load_at<true>(a.in + r[u] * pitch, col);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       if (r[u] < 0) continue;
       float f[N];
-      RowVec<DT>::unpack(v[u], f);
+      RV::unpack(v[u], f);
 #pragma unroll
       for (int i = 0; i < N; ++i) acc[i] = fmaf(w[u], f[i], acc[i]);
     }
   }
-  RowVec<DT>::template store<true>(a.out + p.t * pitch, col, a.H, RowVec<DT>::pack(acc));
+  RV::template store_at<true>(a.out + p.t * pitch, col, RV::pack(acc));
 }
 
 // Gradients of the weighted sum, WIDTH lanes (a wave or the block) per
 // token: for 8 slots at a time, the row's gradient is written and its
 // product with the token's gradient summed as the rows go by.
-template <int DT, int WIDTH>
+template <class RV, int WIDTH>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const RowsArgs a,
                                                            const uint8_t* __restrict__ rows,
                                                            float* __restrict__ grad_w) {
-  constexpr int N = RowVec<DT>::N;
+  constexpr int N = RV::N;
   __shared__ float part[4][8];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * (256 / WIDTH) + (WIDTH == 64 ? wave : 0);
   if (t >= a.T) return;                  // whole waves (WIDTH 64) or never
   const int first = WIDTH == 64 ? lane : (int)threadIdx.x;
-  const int64_t pitch = (int64_t)a.H * RowVec<DT>::kSize;
+  const int64_t pitch = (int64_t)a.H * RV::kSize;
   for (int j0 = 0; j0 < a.k; j0 += 8) {
     int r[8];
     float w[8], dot[8];
@@ -204,24 +207,29 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const RowsArgs a,
         if (a.weights != nullptr) w[u] = a.weights[t * a.k + j0 + u];
       }
     }
-    for (int col = first * N; col < a.H; col += WIDTH * N) {
-      float g[N];
-      RowVec<DT>::unpack(RowVec<DT>::template load<false>(a.in + t * pitch, col, a.H), g);
-      u32x4_t v[8];
+    for (int v0 = first * N; v0 < a.H; v0 += WIDTH * N) {
+      const int col = RV::inside(v0, a.H);
+      // columns that the lane before has too stay out of the products
+      const typename RV::Raw mine = RV::mask_from(v0 - col);
+      float g[N], own[N];
+      RV::unpack(RV::template load_at<false>(a.in + t * pitch, col), g);
+      typename RV::Raw v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (r[u] >= 0) v[u] = RowVec<DT>::template load<true>(rows + r[u] * pitch, col, a.H);
+        if (r[u] >= 0) v[u] = RV::template load_at<true>(rows + r[u] * pitch, col);
+#pragma unroll
+      for (int i = 0; i < N; ++i) own[i] = col + i >= v0 ? g[i] : 0.0f;
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         if (r[u] < 0) continue;
         float f[N], d[N];
-        RowVec<DT>::unpack(v[u], f);
+        RV::unpack(v[u] & mine, f);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          dot[u] = fmaf(g[i], f[i], dot[u]);
+          dot[u] = fmaf(own[i], f[i], dot[u]);
           d[i] = w[u] * g[i];
         }
-        RowVec<DT>::template store<true>(a.out + r[u] * pitch, col, a.H, RowVec<DT>::pack(d));
+        RV::template store_at<true>(a.out + r[u] * pitch, col, RV::pack(d));
       }
     }
 #pragma unroll
@@ -252,25 +260,34 @@ void split_row(int H, int N, int* log_width, int* pieces) {
   *pieces = (nv + (1 << *log_width) - 1) >> *log_width;
 }
 
-template <int DT>
-hipError_t rows_dt(const RowsArgs& a, bool permute, hipStream_t stream) {
+template <class RV>
+hipError_t stream_rows(const RowsArgs& a, bool permute, hipStream_t stream) {
   int log_width, pieces;
-  split_row(a.H, RowVec<DT>::N, &log_width, &pieces);
+  split_row(a.H, RV::N, &log_width, &pieces);
   const int per_block = 256 >> log_width;
   const int64_t grid = (a.T + per_block - 1) / per_block * pieces;
   if (grid >= (int64_t)1 << 31) return hipErrorInvalidValue;
-  if (permute) permute_rows_kernel<DT><<<(unsigned)grid, 256, 0, stream>>>(a, log_width, pieces);
-  else combine_rows_kernel<DT><<<(unsigned)grid, 256, 0, stream>>>(a, log_width, pieces);
+  if (permute) permute_rows_kernel<RV><<<(unsigned)grid, 256, 0, stream>>>(a, log_width, pieces);
+  else combine_rows_kernel<RV><<<(unsigned)grid, 256, 0, stream>>>(a, log_width, pieces);
   return hipGetLastError();
+}
+
+template <int DT>
+hipError_t rows_dt(const RowsArgs& a, bool permute, hipStream_t stream) {
+  return a.H < RowVec<DT>::N ? stream_rows<RowOne<DT>>(a, permute, stream)
+                             : stream_rows<RowVec<DT>>(a, permute, stream);
 }
 
 template <int DT>
 hipError_t combine_grad_dt(const RowsArgs& a, const uint8_t* rows, float* grad_w,
                            hipStream_t stream) {
-  if (a.H <= 256 * RowVec<DT>::N)
-    combine_grad_kernel<DT, 64><<<(unsigned)((a.T + 3) / 4), 256, 0, stream>>>(a, rows, grad_w);
+  const unsigned waves = (unsigned)((a.T + 3) / 4);
+  if (a.H < RowVec<DT>::N)
+    combine_grad_kernel<RowOne<DT>, 64><<<waves, 256, 0, stream>>>(a, rows, grad_w);
+  else if (a.H <= 256 * RowVec<DT>::N)
+    combine_grad_kernel<RowVec<DT>, 64><<<waves, 256, 0, stream>>>(a, rows, grad_w);
   else
-    combine_grad_kernel<DT, 256><<<(unsigned)a.T, 256, 0, stream>>>(a, rows, grad_w);
+    combine_grad_kernel<RowVec<DT>, 256><<<(unsigned)a.T, 256, 0, stream>>>(a, rows, grad_w);
   return hipGetLastError();
 }
 

@@ -58,10 +58,15 @@ __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E
                                             float (&x)[VPL]) {
   const uint8_t* row = (const uint8_t*)logits + t * E * RowVec<DT>::kSize;
   constexpr int N = RowVec<DT>::N;
-  if constexpr (VPL % N == 0) {
+  if constexpr (VPL % N == 0) {             // E > 64: at least one vector
+    u32x4_t v[VPL / N];
 #pragma unroll
-    for (int i = 0; i < VPL; i += N)
-      RowVec<DT>::unpack(RowVec<DT>::template load<true>(row, e0 + i, E), x + i);
+    for (int i = 0; i < VPL / N; ++i) v[i] = RowVec<DT>::template load<true>(row, e0 + i * N, E);
+#pragma unroll
+    for (int i = 0; i < VPL / N; ++i) {
+      RowVec<DT>::settle(v[i], e0 + i * N, E);
+      RowVec<DT>::unpack(v[i], x + i * N);
+    }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) x[i] = e0 + i < E ? clean_logit(x[i]) : -INFINITY;
   } else {

@@ -1,10 +1,14 @@
 // Rows of bf16, fp16 or fp32 values in 16-byte vectors, for the kernels
 // around the expert layer (rows of any width, starting at any element).
 //
-// A vector holds 8 (bf16, fp16) or 4 (fp32) consecutive columns.  Rows of an
-// odd width start at odd addresses: gfx950 loads and stores 16 bytes at any
-// address, so one form serves every width, and only a row's last, partial
-// vector goes element by element.
+// A vector holds N = 8 (bf16, fp16) or 4 (fp32) consecutive columns.  Rows of
+// an odd width start at odd addresses: gfx950 loads and stores 16 bytes at
+// any address, so one form serves every width.  A row's last vector, where it
+// is partial, is loaded from the row's last N columns and shifted into place
+// when it is used (settle), so that no load depends on a branch and all of a
+// lane's loads are in flight together: a branch per load with the elements
+// one by one on its other side made the compiler wait after each.  Rows
+// narrower than a vector go element by element (RowOne).
 #pragma once
 
 #include "device_common.h"
@@ -21,38 +25,66 @@ typedef u32x4_t __attribute__((aligned(2))) u32x4_any;   // 16 bytes at any 2-by
 
 template <int DT>
 struct RowVec {
+  static constexpr int kDt = DT;
   static constexpr int kSize = dtype_size(DT);
   static constexpr int N = 16 / kSize;             // columns of a vector
+  typedef u32x4_t Raw;
 
-  // columns [col, col + N) of a row of H; those past the row's end are 0
+  // the first column of a vector moved so that it ends inside the row (H >= N)
+  static __device__ __forceinline__ int inside(int col, int H) { return min(col, H - N); }
+
   template <bool NT>
-  static __device__ __forceinline__ u32x4_t load(const uint8_t* row, int col, int H) {
-    const uint8_t* p = row + (int64_t)col * kSize;
-    if (col + N <= H) {
-      const u32x4_any* q = reinterpret_cast<const u32x4_any*>(p);
-      return NT ? __builtin_nontemporal_load(q) : *q;
-    }
-    u32x4_t v = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (col + i >= H) continue;
-      if (kSize == 4) v[i] = reinterpret_cast<const uint32_t*>(p)[i];
-      else v[i / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-    }
-    return v;
+  static __device__ __forceinline__ Raw load_at(const uint8_t* row, int c) {
+    const u32x4_any* q = reinterpret_cast<const u32x4_any*>(row + (int64_t)c * kSize);
+    return NT ? __builtin_nontemporal_load(q) : *q;
   }
   template <bool NT>
-  static __device__ __forceinline__ void store(uint8_t* row, int col, int H, u32x4_t v) {
-    uint8_t* p = row + (int64_t)col * kSize;
+  static __device__ __forceinline__ void store_at(uint8_t* row, int c, Raw v) {
+    u32x4_any* q = reinterpret_cast<u32x4_any*>(row + (int64_t)c * kSize);
+    if (NT) __builtin_nontemporal_store(v, q);
+    else *q = v;
+  }
+  // columns [col, col + N) of a row of H, once settled
+  template <bool NT>
+  static __device__ __forceinline__ Raw load(const uint8_t* row, int col, int H) {
+    return load_at<NT>(row, inside(col, H));
+  }
+  // all bits but those of the first k columns
+  static __device__ __forceinline__ Raw mask_from(int k) {
+    Raw m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      m[i] = kSize == 4 ? (i >= k ? ~0u : 0u)
+                        : (2 * i >= k ? 0xFFFFu : 0u) | (2 * i + 1 >= k ? 0xFFFF0000u : 0u);
+    return m;
+  }
+  // columns past the row's end become 0
+  static __device__ __forceinline__ void settle(Raw& v, int col, int H) {
+    const int k = col + N - H;                     // columns past the end
+    if (k <= 0) return;
+    if (kSize == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = (k & 1) ? (v[i] >> 16) | (i < 3 ? v[(i + 1) & 3] << 16 : 0u) : v[i];
+    }
+    const int w = kSize == 2 ? k >> 1 : k;         // whole words
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (w & 1) ? (i < 3 ? v[(i + 1) & 3] : 0u) : v[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (w & 2) ? (i < 2 ? v[(i + 2) & 3] : 0u) : v[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = k >= N ? 0u : v[i];
+  }
+  template <bool NT>
+  static __device__ __forceinline__ void store(uint8_t* row, int col, int H, Raw v) {
     if (col + N <= H) {
-      u32x4_any* q = reinterpret_cast<u32x4_any*>(p);
-      if (NT) __builtin_nontemporal_store(v, q);
-      else *q = v;
+      store_at<NT>(row, col, v);
       return;
     }
+    uint8_t* p = row + (int64_t)col * kSize;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (col + i >= H) continue;
+      if (col + i >= H) return;
       if (kSize == 4) reinterpret_cast<uint32_t*>(p)[i] = v[i];
       else reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
     }
@@ -95,6 +127,43 @@ struct RowVec {
     if (DT == kF32) reinterpret_cast<float*>(base)[i] = f;
     else if (DT == kBf16) reinterpret_cast<uint16_t*>(base)[i] = (uint16_t)f32_to_bf16_bits(f);
     else reinterpret_cast<uint16_t*>(base)[i] = __builtin_bit_cast(uint16_t, (_Float16)f);
+  }
+};
+
+// The same for rows narrower than a vector: one column at a time.
+template <int DT>
+struct RowOne {
+  static constexpr int kDt = DT;
+  static constexpr int kSize = dtype_size(DT);
+  static constexpr int N = 1;
+  typedef uint32_t Raw;
+  static __device__ __forceinline__ int inside(int col, int H) { return min(col, H - 1); }
+  template <bool NT>
+  static __device__ __forceinline__ Raw load_at(const uint8_t* row, int c) {
+    return __float_as_uint(RowVec<DT>::load_one(row, c));
+  }
+  template <bool NT>
+  static __device__ __forceinline__ void store_at(uint8_t* row, int c, Raw v) {
+    RowVec<DT>::store_one(row, c, __uint_as_float(v));
+  }
+  template <bool NT>
+  static __device__ __forceinline__ Raw load(const uint8_t* row, int col, int H) {
+    return load_at<NT>(row, inside(col, H));
+  }
+  static __device__ __forceinline__ Raw mask_from(int k) { return k > 0 ? 0u : ~0u; }
+  static __device__ __forceinline__ void settle(Raw& v, int col, int H) {
+    if (col >= H) v = 0u;
+  }
+  template <bool NT>
+  static __device__ __forceinline__ void store(uint8_t* row, int col, int H, Raw v) {
+    if (col < H) store_at<NT>(row, col, v);
+  }
+  static __device__ __forceinline__ void unpack(const Raw v, float f[1]) {
+    f[0] = __uint_as_float(v);
+  }
+  static __device__ __forceinline__ Raw pack(const float f[1]) { return __float_as_uint(f[0]); }
+  static __device__ __forceinline__ float load_one(const uint8_t* base, int64_t i) {
+    return RowVec<DT>::load_one(base, i);
   }
 };
 
