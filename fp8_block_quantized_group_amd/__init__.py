@@ -541,13 +541,22 @@ def _scratch(ws: Optional[torch.Tensor], device):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+# The current stream's address; the raw form costs a tenth of a microsecond,
+# building a torch.cuda.Stream most of two, as much as a kernel of these takes.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _run(fn, device: torch.device, *args):
     """fn(*args, stream) on the device and its current stream."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+            status = fn(*args, _raw_stream(index))
+    if status:
+        _check(status)
 
 
 def router_topk(r: Router, logits, topk_ids, topk_weights, bias=None, is_padding=None):

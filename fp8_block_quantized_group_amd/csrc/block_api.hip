@@ -213,10 +213,8 @@ moe_status_t moe_permute(const moe_rows_t* p, const void* x, const int32_t* topk
   s.expert_offsets = expert_offsets;
   s.slot_row = slot_row;
   s.row_slot = row_slot;
-  hipError_t err = moe::launch_sort(s, (hipStream_t)stream);
-  if (err == hipSuccess && p->num_tokens > 0)
-    err = moe::launch_permute_rows(rows_args(p, x, rows, slot_row, nullptr), p->dtype,
-                                   (hipStream_t)stream);
+  const hipError_t err = moe::launch_permute(s, rows_args(p, x, rows, slot_row, nullptr),
+                                             p->dtype, (hipStream_t)stream);
   return launch_status(err, "moe_permute");
 }
 

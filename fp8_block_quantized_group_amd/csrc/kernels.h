@@ -245,7 +245,6 @@ struct SortArgs {
   int32_t* slot_row;           // [slots], -1 unrouted
   int32_t* row_slot;           // [slots], entries past the routed rows not written
 };
-hipError_t launch_sort(const SortArgs& a, hipStream_t stream);
 
 struct RowsArgs {
   const uint8_t* in;           // tokens [T, H] or expert rows [slots, H]
@@ -255,7 +254,9 @@ struct RowsArgs {
   int64_t T, slots;
   int k, H;
 };
-hipError_t launch_permute_rows(const RowsArgs& a, int dtype, hipStream_t stream);
+// the sort (a.slot_row is its output) and the rows
+hipError_t launch_permute(const SortArgs& sort, const RowsArgs& a, int dtype,
+                          hipStream_t stream);
 hipError_t launch_combine_rows(const RowsArgs& a, int dtype, hipStream_t stream);
 // a.in: the gradient of the tokens; a.out: of the rows
 hipError_t launch_combine_grad(const RowsArgs& a, const void* rows, float* grad_w, int dtype,

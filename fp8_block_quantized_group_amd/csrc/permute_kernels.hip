@@ -9,6 +9,8 @@
 //   its gradients      grad_rows[r] = w grad_out[t], grad_w[t, j] = <grad_out[t], rows[r]>
 // Sums run over j ascending in fp32 and are rounded once.  Every kernel is a
 // stream over the rows: one 16-byte vector per lane and row.
+#include <type_traits>
+
 #include "kernels.h"
 #include "row_vec.h"
 
@@ -17,17 +19,22 @@ namespace moe {
 namespace {
 
 constexpr int kSortThreads = 256;
+constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortRounds = kSortChunk / kSortThreads;
+// Up to this many chunks every ranking block adds up the chunks before it;
+// above, one block turns the counts into first rows for all of them.
+constexpr int kSortInline = 64;
 
+// the slot's expert, -1 when it is unrouted
 __device__ __forceinline__ int routed_id(const int32_t* ids, const uint8_t* pad, int64_t slot,
                                          int k, int E) {
   const int id = ids[slot];
   if (id < 0 || id >= E) return -1;
-  if (pad != nullptr && pad[slot / k] != 0) return -1;
+  if (pad != nullptr && pad[(uint32_t)slot / (uint32_t)k] != 0) return -1;   // slots < 2^31
   return id;
 }
 
-// 1: per chunk of slots, how many go to each expert
+// per chunk of slots, how many go to each expert
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const SortArgs a) {
   extern __shared__ int32_t h[];
   for (int e = threadIdx.x; e < a.E; e += kSortThreads) h[e] = 0;
@@ -44,63 +51,143 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const SortArgs
     a.hist[(int64_t)blockIdx.x * a.E + e] = h[e];
 }
 
-// 2: one block; thread e turns its expert's counts into the chunks' first
-// rows and the experts' offsets
-__global__ __launch_bounds__(1024) void sort_scan_kernel(const SortArgs a, int chunks) {
-  __shared__ int wave_total[16];
-  const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
-  int count = 0;
-  if (e < a.E)
-    for (int b = 0; b < chunks; ++b) count += a.hist[(int64_t)b * a.E + e];
-  int incl = count;
+// exclusive scan of one value per thread over the block
+__device__ __forceinline__ int block_exclusive_scan(int v, int* wave_total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int incl = v;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d);
-    if (lane >= d) incl += v;
+    const int o = __shfl_up(incl, d);
+    if (lane >= d) incl += o;
   }
   if (lane == 63) wave_total[wave] = incl;
   __syncthreads();
   for (int w = 0; w < wave; ++w) incl += wave_total[w];
+  return incl - v;
+}
+
+// One block: thread e turns its expert's counts into the chunks' first rows
+// and the experts' offsets.
+__global__ __launch_bounds__(1024) void sort_scan_kernel(const SortArgs a, int chunks) {
+  __shared__ int wave_total[16];
+  const int e = threadIdx.x;
+  int count = 0;
   if (e < a.E) {
-    int base = incl - count;
-    a.expert_offsets[e] = base;
-    if (e == a.E - 1) a.expert_offsets[a.E] = incl;
-    for (int b = 0; b < chunks; ++b) {
-      const int n = a.hist[(int64_t)b * a.E + e];
-      a.hist[(int64_t)b * a.E + e] = base;
-      base += n;
-    }
+#pragma unroll 16
+    for (int b = 0; b < chunks; ++b) count += a.hist[(int64_t)b * a.E + e];
+  }
+  int base = block_exclusive_scan(count, wave_total);
+  if (e >= a.E) return;
+  a.expert_offsets[e] = base;
+  if (e == a.E - 1) a.expert_offsets[a.E] = base + count;
+  for (int b = 0; b < chunks; ++b) {
+    const int n = a.hist[(int64_t)b * a.E + e];
+    a.hist[(int64_t)b * a.E + e] = base;
+    base += n;
   }
 }
 
-// 3: the row of every slot: the chunk's first row of its expert plus the
-// slots of that expert before it in the chunk
-__global__ __launch_bounds__(kSortThreads) void sort_rank_kernel(const SortArgs a) {
-  extern __shared__ int32_t next[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < a.E; e += kSortThreads)
-    next[e] = a.hist[(int64_t)blockIdx.x * a.E + e];
-  __syncthreads();
+// The row of every slot of a chunk: the first row of its expert in the chunk
+// plus the slots of that expert before it.  A wave ranks 256 consecutive
+// slots, 64 at a time: lanes with the same expert find each other by ballots
+// over its bits, and the wave's own counter per expert carries the rest;
+// then the threads turn the waves' counts into first rows.  SCANNED: hist holds
+// the chunk's first rows; else the counts, which every block adds up itself.
+template <bool SCANNED, int PER>
+__global__ __launch_bounds__(kSortThreads) void sort_rank_kernel(const SortArgs a, int chunks) {
+  extern __shared__ int32_t counts[];       // [kSortWaves][E]
+  __shared__ int wave_total[kSortWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = a.E;
+  int32_t* mine = counts + wave * E;
+  for (int e = lane; e < E; e += 64) mine[e] = 0;
+  __builtin_amdgcn_wave_barrier();
+  const int64_t slot0 = (int64_t)blockIdx.x * kSortChunk + wave * (64 * kSortRounds) + lane;
   const uint64_t below = lane == 0 ? 0ull : ~0ull >> (64 - lane);
+  int id[kSortRounds], rank[kSortRounds];
+#pragma unroll
   for (int r = 0; r < kSortRounds; ++r) {
-    const int64_t slot = (int64_t)blockIdx.x * kSortChunk + r * kSortThreads + threadIdx.x;
-    const int id = slot < a.slots ? routed_id(a.ids, a.is_padding, slot, a.k, a.E) : -1;
-    uint64_t same = __ballot(id >= 0);
+    const int64_t slot = slot0 + 64 * r;
+    id[r] = slot < a.slots ? routed_id(a.ids, a.is_padding, slot, a.k, E) : -1;
+  }
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) {
+    uint64_t same = __ballot(id[r] >= 0);
+#pragma unroll
     for (int b = 0; b < 10; ++b) {
-      const uint64_t m = __ballot((id >> b) & 1);
-      same &= ((id >> b) & 1) ? m : ~m;
+      const uint64_t m = __ballot((id[r] >> b) & 1);
+      same &= ((id[r] >> b) & 1) ? m : ~m;
     }
     const int before = __popcll(same & below);
-    for (int w = 0; w < kSortThreads / 64; ++w) {
-      if (wave == w && id >= 0) {
-        const int row = next[id] + before;
-        if (before == 0) next[id] = row + __popcll(same);
-        a.slot_row[slot] = row;
-        a.row_slot[row] = (int)slot;
-      }
-      __syncthreads();
+    rank[r] = 0;
+    if (id[r] >= 0) {
+      rank[r] = mine[id[r]] + before;
+      __builtin_amdgcn_wave_barrier();
+      if (before == 0) mine[id[r]] = rank[r] + __popcll(same);
     }
-    if (id < 0 && slot < a.slots) a.slot_row[slot] = -1;
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  // a thread per PER consecutive experts: the first row of the chunk's slots
+  // of each, then of each wave's (an expert past the last reads the last one's
+  // counts: no load behind a branch)
+  const int e0 = threadIdx.x * PER;
+  int total[PER] = {}, prior[PER] = {}, sum = 0;
+  if (!SCANNED) {
+    int at[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) at[i] = min(e0 + i, E - 1);
+    if (chunks == 1) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) total[i] += counts[w * E + at[i]];
+    } else {
+      constexpr int kBatch = 16;              // chunks whose counts load together
+      for (int b0 = 0; b0 < chunks; b0 += kBatch) {
+        int n[kBatch][PER];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+          for (int i = 0; i < PER; ++i)
+            n[u][i] = a.hist[(int64_t)min(b0 + u, chunks - 1) * E + at[i]];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            prior[i] += b0 + u < (int)blockIdx.x ? n[u][i] : 0;
+            total[i] += b0 + u < chunks ? n[u][i] : 0;
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum += e0 + i < E ? total[i] : 0;
+  }
+  int first = SCANNED ? 0 : block_exclusive_scan(sum, wave_total);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = e0 + i;
+    if (e >= E) continue;
+    int base = SCANNED ? a.hist[(int64_t)blockIdx.x * E + e] : first + prior[i];
+    if (!SCANNED && blockIdx.x == 0) {
+      a.expert_offsets[e] = first;
+      if (e == E - 1) a.expert_offsets[E] = first + total[i];
+    }
+    first += total[i];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int n = counts[w * E + e];
+      counts[w * E + e] = base;
+      base += n;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) {
+    const int64_t slot = slot0 + 64 * r;
+    if (slot >= a.slots) continue;
+    const int row = id[r] >= 0 ? mine[id[r]] + rank[r] : -1;
+    a.slot_row[slot] = row;
+    if (row >= 0) a.row_slot[row] = (int)slot;
   }
 }
 
@@ -136,6 +223,72 @@ __global__ __launch_bounds__(256) void permute_rows_kernel(const RowsArgs a, int
     const int r = a.slot_row[p.t * a.k + j];
     if (r >= 0 && r < a.slots) RV::template store_at<true>(a.out + r * pitch, col, v);
   }
+}
+
+constexpr int kSmallBatch = 256;
+
+// Sort and rows in one launch, for few slots: every block finds the rows of
+// its own tokens' slots by comparing each with all slots (lanes hold slots,
+// a ballot counts 64 comparisons), and copies.  Blocks of the first piece of
+// a token write the slots' rows; the waves share out the offsets, each the
+// count of slots of lower experts.
+template <class RV>
+__global__ __launch_bounds__(256) void permute_small_kernel(const RowsArgs a, const SortArgs s,
+                                                            int log_width, int pieces) {
+  extern __shared__ int32_t lds[];          // ids [ids], then rows [tokens * k]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int kBatch = kSmallBatch;       // slots compared per loop turn
+  const int n = (int)a.slots, k = a.k, tokens = 256 >> log_width;
+  const int ids = (n + kBatch - 1) / kBatch * kBatch;
+  int32_t* rows = lds + ids;
+  const Place p = place(log_width, pieces);
+  const int col = RV::inside(min(p.v * RV::N, a.H - 1), a.H);
+  const int64_t pitch = (int64_t)a.H * RV::kSize;
+  const typename RV::Raw v =
+      RV::template load_at<true>(a.in + min(p.t, a.T - 1) * pitch, col);
+  for (int i = threadIdx.x; i < ids; i += 256)
+    lds[i] = i < n ? routed_id(s.ids, s.is_padding, i, k, s.E) : -1;
+  __syncthreads();
+  const int t0 = (int)(blockIdx.x / pieces) * tokens;
+  const bool write = blockIdx.x % pieces == 0;
+  for (int q = wave; q < tokens * k; q += 4) {           // a wave per slot
+    const int slot = t0 * k + q;
+    const int id = slot < n ? __builtin_amdgcn_readfirstlane(lds[slot]) : -1;
+    int row = -1;
+    if (id >= 0) {
+      row = 0;
+      for (int i = 0; i < ids; i += kBatch) {
+#pragma unroll
+        for (int u = 0; u < kBatch; u += 64) {
+          const int o = lds[i + u + lane];
+          row += __popcll(__ballot(o >= 0 && (o < id || (o == id && i + u + lane < slot))));
+        }
+      }
+    }
+    if (lane == 0) {
+      rows[q] = row;
+      if (write && slot < n) {
+        s.slot_row[slot] = row;
+        if (row >= 0) s.row_slot[row] = slot;
+      }
+    }
+  }
+  for (int e = blockIdx.x * 4 + wave; e <= s.E; e += gridDim.x * 4) {
+    int c = 0;
+    for (int i = 0; i < ids; i += kBatch) {
+#pragma unroll
+      for (int u = 0; u < kBatch; u += 64) {
+        const int o = lds[i + u + lane];
+        c += __popcll(__ballot(o >= 0 && o < e));
+      }
+    }
+    if (lane == 0) s.expert_offsets[e] = c;
+  }
+  __syncthreads();
+  if (p.t >= a.T || p.v * RV::N >= a.H) return;
+  const int32_t* mine = rows + (threadIdx.x >> log_width) * k;
+  for (int j = 0; j < k; ++j)
+    if (mine[j] >= 0) RV::template store_at<true>(a.out + mine[j] * pitch, col, v);
 }
 
 // the sum of a token's rows, weighted when weights are given
@@ -260,22 +413,56 @@ void split_row(int H, int N, int* log_width, int* pieces) {
   *pieces = (nv + (1 << *log_width) - 1) >> *log_width;
 }
 
+hipError_t launch_sort(const SortArgs& a, hipStream_t stream) {
+  const int64_t chunks = (a.slots + kSortChunk - 1) / kSortChunk;
+  const size_t lds = kSortWaves * a.E * sizeof(int32_t);
+  const bool scan = chunks == 0 || chunks > kSortInline;
+  if (chunks > 1)
+    sort_count_kernel<<<(unsigned)chunks, kSortThreads, a.E * sizeof(int32_t), stream>>>(a);
+  if (scan) sort_scan_kernel<<<1, 1024, 0, stream>>>(a, (int)chunks);
+  if (chunks == 0) return hipGetLastError();
+  auto rank = [&](auto per) {
+    constexpr int PER = decltype(per)::value;
+    if (scan)
+      sort_rank_kernel<true, PER><<<(unsigned)chunks, kSortThreads, lds, stream>>>(a, (int)chunks);
+    else
+      sort_rank_kernel<false, PER><<<(unsigned)chunks, kSortThreads, lds, stream>>>(a, (int)chunks);
+    return hipGetLastError();
+  };
+  if (a.E <= kSortThreads) return rank(std::integral_constant<int, 1>());
+  if (a.E <= 2 * kSortThreads) return rank(std::integral_constant<int, 2>());
+  return rank(std::integral_constant<int, 4>());
+}
+
+// One launch for the sort and the rows up to this many comparisons per block
+// (its slots times all slots).
+constexpr int64_t kSmallCompares = 16384;
+
+// sort != nullptr: permute, after the sort; else combine
 template <class RV>
-hipError_t stream_rows(const RowsArgs& a, bool permute, hipStream_t stream) {
+hipError_t stream_rows(const RowsArgs& a, const SortArgs* sort, hipStream_t stream) {
   int log_width, pieces;
   split_row(a.H, RV::N, &log_width, &pieces);
   const int per_block = 256 >> log_width;
   const int64_t grid = (a.T + per_block - 1) / per_block * pieces;
   if (grid >= (int64_t)1 << 31) return hipErrorInvalidValue;
-  if (permute) permute_rows_kernel<RV><<<(unsigned)grid, 256, 0, stream>>>(a, log_width, pieces);
-  else combine_rows_kernel<RV><<<(unsigned)grid, 256, 0, stream>>>(a, log_width, pieces);
+  if (sort == nullptr) {
+    combine_rows_kernel<RV><<<(unsigned)grid, 256, 0, stream>>>(a, log_width, pieces);
+  } else if (per_block * a.k * a.slots <= kSmallCompares) {
+    const size_t lds = (size_t)(a.slots + kSmallBatch - 1 + per_block * a.k) * sizeof(int32_t);
+    permute_small_kernel<RV><<<(unsigned)grid, 256, lds, stream>>>(a, *sort, log_width, pieces);
+  } else {
+    const hipError_t err = launch_sort(*sort, stream);
+    if (err != hipSuccess) return err;
+    permute_rows_kernel<RV><<<(unsigned)grid, 256, 0, stream>>>(a, log_width, pieces);
+  }
   return hipGetLastError();
 }
 
 template <int DT>
-hipError_t rows_dt(const RowsArgs& a, bool permute, hipStream_t stream) {
-  return a.H < RowVec<DT>::N ? stream_rows<RowOne<DT>>(a, permute, stream)
-                             : stream_rows<RowVec<DT>>(a, permute, stream);
+hipError_t rows_dt(const RowsArgs& a, const SortArgs* sort, hipStream_t stream) {
+  return a.H < RowVec<DT>::N ? stream_rows<RowOne<DT>>(a, sort, stream)
+                             : stream_rows<RowVec<DT>>(a, sort, stream);
 }
 
 template <int DT>
@@ -293,29 +480,21 @@ hipError_t combine_grad_dt(const RowsArgs& a, const uint8_t* rows, float* grad_w
 
 }  // namespace
 
-hipError_t launch_sort(const SortArgs& a, hipStream_t stream) {
-  const int chunks = (int)((a.slots + kSortChunk - 1) / kSortChunk);
-  if (chunks > 0)
-    sort_count_kernel<<<chunks, kSortThreads, a.E * sizeof(int32_t), stream>>>(a);
-  sort_scan_kernel<<<1, 1024, 0, stream>>>(a, chunks);
-  if (chunks > 0)
-    sort_rank_kernel<<<chunks, kSortThreads, a.E * sizeof(int32_t), stream>>>(a);
-  return hipGetLastError();
-}
-
-hipError_t launch_permute_rows(const RowsArgs& a, int dtype, hipStream_t stream) {
+hipError_t launch_permute(const SortArgs& sort, const RowsArgs& a, int dtype,
+                          hipStream_t stream) {
+  if (a.T == 0) return launch_sort(sort, stream);        // the offsets alone
   switch (dtype) {
-    case kBf16: return rows_dt<kBf16>(a, true, stream);
-    case kF16: return rows_dt<kF16>(a, true, stream);
-    default: return rows_dt<kF32>(a, true, stream);
+    case kBf16: return rows_dt<kBf16>(a, &sort, stream);
+    case kF16: return rows_dt<kF16>(a, &sort, stream);
+    default: return rows_dt<kF32>(a, &sort, stream);
   }
 }
 
 hipError_t launch_combine_rows(const RowsArgs& a, int dtype, hipStream_t stream) {
   switch (dtype) {
-    case kBf16: return rows_dt<kBf16>(a, false, stream);
-    case kF16: return rows_dt<kF16>(a, false, stream);
-    default: return rows_dt<kF32>(a, false, stream);
+    case kBf16: return rows_dt<kBf16>(a, nullptr, stream);
+    case kF16: return rows_dt<kF16>(a, nullptr, stream);
+    default: return rows_dt<kF32>(a, nullptr, stream);
   }
 }
 
