@@ -218,7 +218,7 @@ __global__ __launch_bounds__(256) void permute_rows_kernel(const RowsArgs a, int
   if (p.t >= a.T || p.v * RV::N >= a.H) return;
   const int col = RV::inside(p.v * RV::N, a.H);
   const int64_t pitch = (int64_t)a.H * RV::kSize;
-  const typename RV::Raw v = RV::template load_at<true>(a.in + p.t * pitch, col);
+  const typename RV::Raw v = RV::template load_at<false>(a.in + p.t * pitch, col);
   for (int j = 0; j < a.k; ++j) {
     const int r = a.slot_row[p.t * a.k + j];
     if (r >= 0 && r < a.slots) RV::template store_at<true>(a.out + r * pitch, col, v);
