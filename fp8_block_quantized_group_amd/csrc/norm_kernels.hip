@@ -49,39 +49,58 @@ __device__ __forceinline__ float inv_rms(float sum, int H, float eps, float f) {
   return f / sqrtf(sum / (float)H + eps * f * f);
 }
 
-// weights of columns [col, col + N): of the rows' type or fp32; o + w, or 1
-// without a weight (columns past the end: o)
+// A vector of weights, of the rows' type or fp32: its loads, then, when it is
+// used, o + w, or 1 without a weight (columns past the end: o).
+template <class RV, bool W32>
+struct Weights {
+  static constexpr int N = RV::N;
+  static constexpr bool kPair = W32 && N == 8;    // two fp32 vectors
+  typedef std::conditional_t<W32 && N == 1, RowOne<kF32>, RV> WV;
+  u32x4_t a, b;                                   // kPair
+  typename WV::Raw v;
+
+  __device__ __forceinline__ void load(const void* w, int col, int H) {
+    if (w == nullptr) return;
+    const uint8_t* p = (const uint8_t*)w;
+    if constexpr (kPair) {
+      const int c = RV::inside(col, H);
+      a = RowVec<kF32>::template load_at<false>(p, c);
+      b = RowVec<kF32>::template load_at<false>(p, c + 4);
+    } else {
+      v = WV::template load<false>(p, col, H);
+    }
+  }
+  __device__ __forceinline__ void use(const void* w, int col, int H, float o, float (&f)[N]) {
+    if (w == nullptr) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = 1.0f;
+      return;
+    }
+    if constexpr (kPair) {
+      RowVec<kF32>::unpack(a, f);
+      RowVec<kF32>::unpack(b, f + 4);
+      const int k = col - RV::inside(col, H);     // shifted into place as rows are
+      if (k > 0) {
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            f[i] = (k & d) ? (i + d < 8 ? f[(i + d) & 7] : 0.0f) : f[i];
+      }
+    } else {
+      WV::settle(v, col, H);
+      WV::unpack(v, f);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] += o;
+  }
+};
 template <class RV, bool W32>
 __device__ __forceinline__ void load_weights(const void* w, int col, int H, float o,
                                              float (&f)[RV::N]) {
-  constexpr int N = RV::N;
-  if (w == nullptr) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = 1.0f;
-    return;
-  }
-  const uint8_t* p = (const uint8_t*)w;
-  if constexpr (W32 && N == 8) {                  // two fp32 vectors
-    const int c = RV::inside(col, H);
-    u32x4_t a = RowVec<kF32>::template load_at<false>(p, c);
-    u32x4_t b = RowVec<kF32>::template load_at<false>(p, c + 4);
-    const int k = col - c;                        // shifted in place as rows are
-    RowVec<kF32>::unpack(a, f);
-    RowVec<kF32>::unpack(b, f + 4);
-    if (k > 0) {
-#pragma unroll
-      for (int d = 1; d < 8; d <<= 1)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = (k & d) ? (i + d < 8 ? f[(i + d) & 7] : 0.0f) : f[i];
-    }
-  } else {
-    typedef std::conditional_t<W32 && N == 1, RowOne<kF32>, RV> WV;
-    typename WV::Raw v = WV::template load<false>(p, col, H);
-    WV::settle(v, col, H);
-    WV::unpack(v, f);
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i] += o;
+  Weights<RV, W32> v;
+  v.load(w, col, H);
+  v.use(w, col, H, o, f);
 }
 
 __device__ __forceinline__ float gate_value(float g, bool sigmoid) {
@@ -113,22 +132,44 @@ __device__ __forceinline__ float row_inv_rms(F&& value, int H, float eps, float 
   return inv_rms(s[0], H, eps, f);
 }
 
+// Weights and gate are loaded with the row (EARLY: up to two vectors per
+// lane), as a load after each of the two sums would be waited for in full;
+// with four the registers cost more waves than that gains (1024 x 7168: 13.7
+// us, 10.4 without).
 template <class RV, bool W32, int BT, int VPT>
 __global__ __launch_bounds__(BT == 64 ? 256 : BT) void norm_kernel(const NormArgs a) {
   constexpr int N = RV::N;
+  constexpr bool EARLY = VPT <= 2;
   __shared__ float buf[4][1][16];
   const int64_t row = BT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (row >= a.T) return;                       // whole waves (BT 64) or never
   const int first = BT == 64 ? threadIdx.x & 63 : threadIdx.x;
   const int H = a.H;
   const int64_t at = row * H * RV::kSize;
-  typename RV::Raw rv[VPT], yv[VPT];
-  float x[VPT][N];
+  const void* w_post = a.post ? a.w_post : nullptr;
+  const uint8_t* gates = a.gate_kind == kGateFull ? a.gate + at
+                         : a.gate_kind == kGateChannel ? a.gate : nullptr;
+  typename RV::Raw rv[VPT], yv[VPT], gv[VPT];
+  Weights<RV, W32> wpost[VPT], wpre[VPT];
+  float x[VPT][N], gt = 1.0f;
+  auto load_gate = [&](int i) {
+    const int col = (first + i * BT) * N;
+    if (gates != nullptr) gv[i] = RV::template load<false>(gates, col, H);
+    wpost[i].load(w_post, col, H);
+  };
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int col = (first + i * BT) * N;
     rv[i] = RV::template load<true>(a.r + at, col, H);
     if (a.y != nullptr) yv[i] = RV::template load<true>(a.y + at, col, H);
+  }
+  if (a.gate_kind == kGateToken) gt = RV::load_one(a.gate, row);
+  if (EARLY) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      load_gate(i);
+      wpre[i].load(a.w_pre, (first + i * BT) * N, H);
+    }
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -142,23 +183,19 @@ __global__ __launch_bounds__(BT == 64 ? 256 : BT) void norm_kernel(const NormArg
     if (a.post)
       ys = row_inv_rms<BT, VPT, N>([&](int i, float* v) { RV::unpack(yv[i], v); }, H,
                                    a.eps, buf);
-    float gt = 1.0f;
-    if (a.gate_kind == kGateToken)
-      gt = gate_value(RV::load_one(a.gate, row), a.gate_sigmoid);
+    if (a.gate_kind == kGateToken) gt = gate_value(gt, a.gate_sigmoid);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int col = (first + i * BT) * N;
-      if (col >= H) continue;
+      if (!EARLY) load_gate(i);
       float y[N], w[N], g[N];
       RV::unpack(yv[i], y);
-      load_weights<RV, W32>(a.post ? a.w_post : nullptr, col, H, a.offset, w);
+      wpost[i].use(w_post, col, H, a.offset, w);
 #pragma unroll
       for (int c = 0; c < N; ++c) g[c] = gt;
-      if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull) {
-        typename RV::Raw gv =
-            RV::template load<false>(a.gate + (a.gate_kind == kGateFull ? at : 0), col, H);
-        RV::settle(gv, col, H);
-        RV::unpack(gv, g);
+      if (gates != nullptr) {
+        RV::settle(gv[i], col, H);
+        RV::unpack(gv[i], g);
 #pragma unroll
         for (int c = 0; c < N; ++c) g[c] = gate_value(g[c], a.gate_sigmoid);
       }
@@ -178,9 +215,9 @@ __global__ __launch_bounds__(BT == 64 ? 256 : BT) void norm_kernel(const NormArg
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int col = (first + i * BT) * N;
-    if (col >= H) continue;
+    if (!EARLY) wpre[i].load(a.w_pre, col, H);
     float w[N], h[N];
-    load_weights<RV, W32>(a.w_pre, col, H, a.offset, w);
+    wpre[i].use(a.w_pre, col, H, a.offset, w);
 #pragma unroll
     for (int c = 0; c < N; ++c) h[c] = x[i][c] * xs * w[c];
     RV::template store<true>(a.h + at, col, H, RV::pack(h));
@@ -630,6 +667,11 @@ struct Shape {
   static constexpr int BT = B, VPT = V;       // lanes per row, vectors per lane
 };
 
+// Up to this many rows (two per CU) a row gets more lanes: the call's time is
+// one row's.  Measured with / without, bf16: 32 x 7168 4.6 / 5.9 us, 256 x
+// 2048 3.5 / 5.8, 512 x 7168 7.1 / 7.5, 600 x 7168 8.7 / 8.4.
+constexpr int kFewRows = 512;
+
 template <int DT, bool W32>
 hipError_t norm_dt(const NormArgs& a, hipStream_t stream) {
   const int nv = (a.H + RowVec<DT>::N - 1) / RowVec<DT>::N;
@@ -643,6 +685,12 @@ hipError_t norm_dt(const NormArgs& a, hipStream_t stream) {
   if (a.H < RowVec<DT>::N) return go(Shape<RowOne<DT>, 64, 1>());
   if (nv <= 64) return go(Shape<RowVec<DT>, 64, 1>());
   if (nv <= 128) return go(Shape<RowVec<DT>, 64, 2>());
+  if (a.T <= kFewRows) {
+    if (nv <= 256) return go(Shape<RowVec<DT>, 256, 1>());
+    if (nv <= 512) return go(Shape<RowVec<DT>, 512, 1>());
+    if (nv <= 1024) return go(Shape<RowVec<DT>, 512, 2>());
+    if (nv <= 2048) return go(Shape<RowVec<DT>, 1024, 2>());
+  }
   if (nv <= 256) return go(Shape<RowVec<DT>, 64, 4>());
   if (nv <= 512) return go(Shape<RowVec<DT>, 256, 2>());
   if (nv <= 1024) return go(Shape<RowVec<DT>, 256, 4>());

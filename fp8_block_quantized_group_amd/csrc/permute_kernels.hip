@@ -225,70 +225,62 @@ __global__ __launch_bounds__(256) void permute_rows_kernel(const RowsArgs a, int
   }
 }
 
-constexpr int kSmallBatch = 256;
+// Sort and rows in one launch, for few slots: a block per 256 vectors of a
+// token finds the rows of the token's slots by comparing each with all slots
+// (lanes hold slots, a ballot counts 64 comparisons), and copies.  The blocks
+// of a token's first vectors write its slots' rows; the waves share out the
+// offsets, each the count of the slots of lower experts.
+constexpr int kSmallBatch = 256;            // slots compared per loop turn
 
-// Sort and rows in one launch, for few slots: every block finds the rows of
-// its own tokens' slots by comparing each with all slots (lanes hold slots,
-// a ballot counts 64 comparisons), and copies.  Blocks of the first piece of
-// a token write the slots' rows; the waves share out the offsets, each the
-// count of slots of lower experts.
 template <class RV>
 __global__ __launch_bounds__(256) void permute_small_kernel(const RowsArgs a, const SortArgs s,
-                                                            int log_width, int pieces) {
-  extern __shared__ int32_t lds[];          // ids [ids], then rows [tokens * k]
+                                                            int pieces) {
+  extern __shared__ int32_t lds[];          // ids [ids], then rows [k]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  constexpr int kBatch = kSmallBatch;       // slots compared per loop turn
-  const int n = (int)a.slots, k = a.k, tokens = 256 >> log_width;
-  const int ids = (n + kBatch - 1) / kBatch * kBatch;
+  const int n = (int)a.slots, k = a.k;
+  const int ids = (n + kSmallBatch - 1) / kSmallBatch * kSmallBatch;
   int32_t* rows = lds + ids;
-  const Place p = place(log_width, pieces);
-  const int col = RV::inside(min(p.v * RV::N, a.H - 1), a.H);
+  const int t = blockIdx.x / pieces, piece = blockIdx.x - t * pieces;
+  const int v0 = (piece * 256 + threadIdx.x) * RV::N;
+  const int col = RV::inside(min(v0, a.H - 1), a.H);
   const int64_t pitch = (int64_t)a.H * RV::kSize;
-  const typename RV::Raw v =
-      RV::template load_at<true>(a.in + min(p.t, a.T - 1) * pitch, col);
+  const typename RV::Raw v = RV::template load_at<false>(a.in + t * pitch, col);
   for (int i = threadIdx.x; i < ids; i += 256)
     lds[i] = i < n ? routed_id(s.ids, s.is_padding, i, k, s.E) : -1;
   __syncthreads();
-  const int t0 = (int)(blockIdx.x / pieces) * tokens;
-  const bool write = blockIdx.x % pieces == 0;
-  for (int q = wave; q < tokens * k; q += 4) {           // a wave per slot
-    const int slot = t0 * k + q;
-    const int id = slot < n ? __builtin_amdgcn_readfirstlane(lds[slot]) : -1;
-    int row = -1;
-    if (id >= 0) {
-      row = 0;
-      for (int i = 0; i < ids; i += kBatch) {
+  // how many slots go before (id, slot): those of lower experts, and of the
+  // same one those with a lower slot
+  auto before = [&](int id, int slot) {
+    int c = 0;
+    for (int i = 0; i < ids; i += kSmallBatch) {
 #pragma unroll
-        for (int u = 0; u < kBatch; u += 64) {
-          const int o = lds[i + u + lane];
-          row += __popcll(__ballot(o >= 0 && (o < id || (o == id && i + u + lane < slot))));
-        }
+      for (int u = 0; u < kSmallBatch; u += 64) {
+        const int o = lds[i + u + lane];
+        c += __popcll(__ballot(o >= 0 && (o < id || (o == id && i + u + lane < slot))));
       }
     }
+    return c;
+  };
+  for (int j = wave; j < k; j += 4) {
+    const int slot = t * k + j;
+    const int id = __builtin_amdgcn_readfirstlane(lds[slot]);
+    const int row = id >= 0 ? before(id, slot) : -1;
     if (lane == 0) {
-      rows[q] = row;
-      if (write && slot < n) {
+      rows[j] = row;
+      if (piece == 0) {
         s.slot_row[slot] = row;
         if (row >= 0) s.row_slot[row] = slot;
       }
     }
   }
   for (int e = blockIdx.x * 4 + wave; e <= s.E; e += gridDim.x * 4) {
-    int c = 0;
-    for (int i = 0; i < ids; i += kBatch) {
-#pragma unroll
-      for (int u = 0; u < kBatch; u += 64) {
-        const int o = lds[i + u + lane];
-        c += __popcll(__ballot(o >= 0 && o < e));
-      }
-    }
+    const int c = before(e, 0);
     if (lane == 0) s.expert_offsets[e] = c;
   }
   __syncthreads();
-  if (p.t >= a.T || p.v * RV::N >= a.H) return;
-  const int32_t* mine = rows + (threadIdx.x >> log_width) * k;
+  if (v0 >= a.H) return;
   for (int j = 0; j < k; ++j)
-    if (mine[j] >= 0) RV::template store_at<true>(a.out + mine[j] * pitch, col, v);
+    if (rows[j] >= 0) RV::template store_at<true>(a.out + rows[j] * pitch, col, v);
 }
 
 // the sum of a token's rows, weighted when weights are given
@@ -434,9 +426,12 @@ hipError_t launch_sort(const SortArgs& a, hipStream_t stream) {
   return rank(std::integral_constant<int, 4>());
 }
 
-// One launch for the sort and the rows up to this many comparisons per block
-// (its slots times all slots).
-constexpr int64_t kSmallCompares = 16384;
+// One launch for the sort and the rows up to this many slots and comparisons
+// per block (a token's slots times all slots).  Measured in one launch and in
+// two or three, 256 experts: 64 tokens x 8 slots of 7168 columns 6.4 / 8.5
+// us, 256 x 8 12.4 / 14.2, 500 x 8 27.1 / 18.9; 2000 x 1 of 1024 columns 7.7
+// / 11.1, 4000 x 1 21.0 / 12.1.
+constexpr int64_t kSmallSlots = 2048, kSmallCompares = 16384;
 
 // sort != nullptr: permute, after the sort; else combine
 template <class RV>
@@ -448,9 +443,9 @@ hipError_t stream_rows(const RowsArgs& a, const SortArgs* sort, hipStream_t stre
   if (grid >= (int64_t)1 << 31) return hipErrorInvalidValue;
   if (sort == nullptr) {
     combine_rows_kernel<RV><<<(unsigned)grid, 256, 0, stream>>>(a, log_width, pieces);
-  } else if (per_block * a.k * a.slots <= kSmallCompares) {
-    const size_t lds = (size_t)(a.slots + kSmallBatch - 1 + per_block * a.k) * sizeof(int32_t);
-    permute_small_kernel<RV><<<(unsigned)grid, 256, lds, stream>>>(a, *sort, log_width, pieces);
+  } else if (a.slots <= kSmallSlots && a.k * a.slots <= kSmallCompares) {
+    const size_t lds = (size_t)(a.slots + kSmallBatch - 1 + a.k) * sizeof(int32_t);
+    permute_small_kernel<RV><<<(unsigned)(a.T * pieces), 256, lds, stream>>>(a, *sort, pieces);
   } else {
     const hipError_t err = launch_sort(*sort, stream);
     if (err != hipSuccess) return err;
