@@ -365,23 +365,39 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
   };
   GradVectors<RV, VPT, FORM> cur;
   cur.template load<BT>(a, (int64_t)blockIdx.x * G + sub, first);
-  for (int v = threadIdx.x; v < NV; v += blockDim.x) {
-    float f[3][N];
-    load_weights<RV, W32>(a.w_pre, v * N, H, a.offset, f[0]);
-    load_weights<RV, W32>(a.post ? a.w_post : nullptr, v * N, H, a.offset, f[1]);
+  {
+    constexpr int IT = (NV + kGradThreads - 1) / kGradThreads;
+    Weights<RV, W32> w[2][IT];
+    typename RV::Raw gv[IT];
+    const void* w_post = a.post ? a.w_post : nullptr;
+    const bool channel = FORM == kBlock && a.gate_kind == kGateChannel;
 #pragma unroll
-    for (int c = 0; c < N; ++c) f[2][c] = 1.0f;
-    if (FORM == kBlock && a.gate_kind == kGateChannel) {
-      typename RV::Raw gv = RV::template load<false>(a.gate, v * N, H);
-      RV::settle(gv, v * N, H);
-      RV::unpack(gv, f[2]);
-#pragma unroll
-      for (int c = 0; c < N; ++c) f[2][c] = gate_value(f[2][c], a.gate_sigmoid);
+    for (int i = 0; i < IT; ++i) {
+      const int v = threadIdx.x + i * kGradThreads;
+      w[0][i].load(a.w_pre, v * N, H);
+      if (HAS_Y) w[1][i].load(w_post, v * N, H);
+      if (channel) gv[i] = RV::template load<false>(a.gate, v * N, H);
     }
 #pragma unroll
-    for (int o = 0; o < SUMS; ++o)
+    for (int i = 0; i < IT; ++i) {
+      const int v = threadIdx.x + i * kGradThreads;
+      if (v >= NV) continue;
+      float f[3][N];
+      w[0][i].use(a.w_pre, v * N, H, a.offset, f[0]);
+      if (HAS_Y) w[1][i].use(w_post, v * N, H, a.offset, f[1]);
 #pragma unroll
-      for (int c = 0; c < N; ++c) wlds[o][c / P][v][c % P] = f[o][c];
+      for (int c = 0; c < N; ++c) f[2][c] = 1.0f;
+      if (channel) {
+        RV::settle(gv[i], v * N, H);
+        RV::unpack(gv[i], f[2]);
+#pragma unroll
+        for (int c = 0; c < N; ++c) f[2][c] = gate_value(f[2][c], a.gate_sigmoid);
+      }
+#pragma unroll
+      for (int o = 0; o < SUMS; ++o)
+#pragma unroll
+        for (int c = 0; c < N; ++c) wlds[o][c / P][v][c % P] = f[o][c];
+    }
   }
   __syncthreads();
   __builtin_amdgcn_s_waitcnt(0);              // the first row, once
@@ -516,9 +532,14 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
         }
       }
       const int col = (first + i * BT) * N;
+      if constexpr (N == 1) {
+        if (col < H) part[col] = mine[0];
+      } else {
 #pragma unroll
-      for (int c = 0; c < N; ++c)
-        if (col + c < H) part[col + c] = mine[c];
+        for (int c = 0; c < N; c += 4)
+          RowVec<kF32>::template store<false>((uint8_t*)part, col + c, H,
+                                              RowVec<kF32>::pack(mine + c));
+      }
     }
   }
 }
@@ -636,10 +657,10 @@ __global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(const Norm
   }
 }
 
-constexpr int kSumCols = 64, kSumWays = 16;
+constexpr int kSumCols = 64, kSumWays = 16, kSumBatch = 16;
 
-// column c of output o: the parts of every block in order, 16 interleaved
-// runs of them side by side
+// Column c of output o: 16 interleaved runs of the blocks' parts side by
+// side, each with 16 loads in flight, then the runs in order.
 __global__ __launch_bounds__(kSumCols* kSumWays) void grad_sum_kernel(const float* part,
                                                                      int parts, int H, float* g0,
                                                                      float* g1, float* g2) {
@@ -648,10 +669,16 @@ __global__ __launch_bounds__(kSumCols* kSumWays) void grad_sum_kernel(const floa
   if (out == nullptr) return;
   part += (int64_t)blockIdx.y * parts * H;
   const int x = threadIdx.x % kSumCols, w = threadIdx.x / kSumCols;
-  const int c = blockIdx.x * kSumCols + x;
+  const int c = blockIdx.x * kSumCols + x, at = min(c, H - 1);
   float s = 0.0f;
-  if (c < H)
-    for (int p = w; p < parts; p += kSumWays) s += part[(int64_t)p * H + c];
+  for (int p0 = w; p0 < parts; p0 += kSumWays * kSumBatch) {
+    float v[kSumBatch];
+#pragma unroll
+    for (int u = 0; u < kSumBatch; ++u)
+      v[u] = part[(int64_t)min(p0 + u * kSumWays, parts - 1) * H + at];
+#pragma unroll
+    for (int u = 0; u < kSumBatch; ++u) s += p0 + u * kSumWays < parts ? v[u] : 0.0f;
+  }
   run[w][x] = s;
   __syncthreads();
   if (w != 0 || c >= H) return;
