@@ -350,6 +350,8 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
   constexpr int N = RV::N, G = grad_groups(BT), NV = BT * VPT;
   constexpr int P = N < 4 ? N : 4;            // columns of a plane
   constexpr bool HAS_Y = FORM != kNoBlock, FULL = FORM == kBlockFullGate;
+  constexpr bool AHEAD = BT <= kGradThreads;
+  constexpr int THREADS = BT < kGradThreads ? kGradThreads : BT;
   constexpr int SUMS = FORM == kNoBlock ? 1 : FULL ? 2 : 3;   // column sums: pre, post, gate
   __shared__ float buf1[2][G][3][16], buf2[2][G][2][16], buf3[2][G][3][16];
   __shared__ float sums[G][BT * N];
@@ -366,21 +368,21 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
   GradVectors<RV, VPT, FORM> cur;
   cur.template load<BT>(a, (int64_t)blockIdx.x * G + sub, first);
   {
-    constexpr int IT = (NV + kGradThreads - 1) / kGradThreads;
+    constexpr int IT = (NV + THREADS - 1) / THREADS;
     Weights<RV, W32> w[2][IT];
     typename RV::Raw gv[IT];
     const void* w_post = a.post ? a.w_post : nullptr;
     const bool channel = FORM == kBlock && a.gate_kind == kGateChannel;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int v = threadIdx.x + i * kGradThreads;
+      const int v = threadIdx.x + i * THREADS;
       w[0][i].load(a.w_pre, v * N, H);
       if (HAS_Y) w[1][i].load(w_post, v * N, H);
       if (channel) gv[i] = RV::template load<false>(a.gate, v * N, H);
     }
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int v = threadIdx.x + i * kGradThreads;
+      const int v = threadIdx.x + i * THREADS;
       if (v >= NV) continue;
       float f[3][N];
       w[0][i].use(a.w_pre, v * N, H, a.offset, f[0]);
@@ -416,7 +418,7 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
     const int h = live ? H : 0;               // columns of the row
     const int64_t at = row * H * RV::kSize;
     GradVectors<RV, VPT, FORM> next;
-    next.template load<BT>(a, row + stride, first);
+    if constexpr (AHEAD) next.template load<BT>(a, row + stride, first);
     cur.template settle<BT>(a, first, h);
     float s[3] = {0.0f, 0.0f, 0.0f}, fx = 1.0f, fy = 1.0f;
     auto add_up = [&](auto scaled) {
@@ -507,7 +509,8 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
         RV::template store<true>(a.dy + at, col, H, RV::pack(d));
       }
     }
-    cur = next;
+    if constexpr (AHEAD) cur = next;
+    else cur.template load<BT>(a, row + stride, first);
   }
   // the groups' column sums, in group order, as the block's part
 #pragma unroll
@@ -727,9 +730,6 @@ hipError_t norm_dt(const NormArgs& a, hipStream_t stream) {
   return hipErrorInvalidValue;                // 2-byte rows end at 4096 vectors
 }
 
-// vectors per row above which a row does not fit the registers of a block
-constexpr int kWideVectors = 1024;
-
 template <int DT, bool W32>
 hipError_t norm_grad_dt(const NormGradArgs& a, int blocks, hipStream_t stream) {
   const int nv = (a.H + RowVec<DT>::N - 1) / RowVec<DT>::N;
@@ -750,7 +750,15 @@ hipError_t norm_grad_dt(const NormGradArgs& a, int blocks, hipStream_t stream) {
   if (nv <= 128) return go(Shape<RowVec<DT>, 128, 1>());
   if (nv <= 256) return go(Shape<RowVec<DT>, 256, 1>());
   if (nv <= 512) return go(Shape<RowVec<DT>, 512, 1>());
-  if (nv <= kWideVectors) return go(Shape<RowVec<DT>, 512, 2>());
+  if (nv <= 1024) return go(Shape<RowVec<DT>, 512, 2>());
+  // 1024 x 2 vectors: as fp32; of a 2-byte type, with twice the columns, only
+  // without a block's sums
+  if constexpr (DT == kF32) {
+    if (nv <= 2048) return go(Shape<RowVec<DT>, 1024, 2>());
+  } else if (nv <= 2048 && a.y == nullptr) {
+    norm_grad_kernel<RowVec<DT>, W32, 1024, 2, kNoBlock><<<blocks, 1024, 0, stream>>>(a);
+    return hipGetLastError();
+  }
   norm_grad_wide_kernel<RowVec<DT>, W32><<<blocks, kWideThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
