@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 from typing import Optional
 
 import torch
@@ -711,3 +711,65 @@ def block_norm_backward(p: BlockNorm, residual_out, grad_normed, grad_residual, 
          _arg(grad_post_weight, "grad_post_weight", torch.float32, (H,), d),
          _arg(grad_gate, "grad_gate", p.dtype if p.gate == "full" else torch.float32,
               p.gate_shape or (), d), wp, wn)
+
+
+class MoeBlock:
+    """One block of a model around its expert layer: pre norm, router, MoeLayer,
+    then post norm, gate, residual scale and add, and the next block's pre norm
+    in the same pass.  Buffers between the steps are kept with the block, as the
+    layer keeps its workspace: calls of one block must not overlap.
+
+    ``norm`` describes both norms (dtype bfloat16, the layer's); ``router_weight``
+    is [num_experts, hidden] and makes the logits, router.dtype, by a product of
+    torch's.  The batched layout has no place here: its slabs come from a
+    dispatch that already routed.
+    """
+
+    def __init__(self, layer: MoeLayer, router: Router, router_weight, norm: BlockNorm,
+                 pre_weight=None, post_weight=None, bias=None):
+        p = layer.p
+        if p.layout == LAYOUT_BATCHED:
+            raise ValueError("MoeBlock needs the contiguous or the indexed layout")
+        if norm.dtype != torch.bfloat16:
+            raise ValueError(f"the layer's streams are bfloat16, got {norm.dtype}")
+        sizes_ = (p.num_tokens, p.hidden, p.top_k)
+        for what, have in (("router", (router.num_tokens, p.hidden, router.top_k)),
+                           ("norm", (norm.num_tokens, norm.hidden, p.top_k))):
+            if have != sizes_:
+                raise ValueError(f"{what} and layer differ in (tokens, hidden, top_k): "
+                                 f"{have}, {sizes_}")
+        if tuple(router_weight.shape) != (router.num_experts, p.hidden) \
+                or router_weight.dtype != router.dtype:
+            raise ValueError(f"router_weight must be {router.dtype} "
+                             f"{(router.num_experts, p.hidden)}, got {router_weight.dtype} "
+                             f"{tuple(router_weight.shape)}")
+        self.layer, self.router, self.norm = layer, router, norm
+        self.pre = replace(norm, post_norm=False, gate="none")
+        self.router_weight, self.bias = router_weight, bias
+        self.pre_weight, self.post_weight = pre_weight, post_weight
+        dev, shape = router_weight.device, (p.num_tokens, p.hidden)
+        self.hidden = torch.empty(shape, dtype=norm.dtype, device=dev)
+        self.y = torch.empty(shape, dtype=norm.dtype, device=dev)
+        k = (p.num_tokens, p.top_k)
+        self.topk_ids = torch.empty(k, dtype=torch.int32, device=dev)
+        self.topk_weights = torch.empty(k, dtype=torch.float32, device=dev)
+
+    def __call__(self, residual, normed=None, gate=None, is_padding=None, eplb=None,
+                 residual_out=None, next_normed=None, next_weight=None):
+        """residual_out (new unless given; may be residual).  ``normed``: the
+        residual's pre norm where the block before this one left it; with
+        ``next_normed`` the next block's is written there, by next_weight."""
+        with torch.cuda.device(_device(residual, "residual")):
+            if normed is None:
+                normed = self.hidden
+                block_norm(self.pre, residual, normed, pre_weight=self.pre_weight)
+            logits = torch.matmul(normed.to(self.router.dtype), self.router_weight.t())
+            router_topk(self.router, logits, self.topk_ids, self.topk_weights, bias=self.bias,
+                        is_padding=is_padding)
+            self.layer(normed, self.topk_ids, self.topk_weights, out=self.y,
+                       is_padding=is_padding, eplb=eplb)
+            if residual_out is None:
+                residual_out = torch.empty_like(residual)
+            block_norm(self.norm, residual, next_normed, y=self.y, residual_out=residual_out,
+                       pre_weight=next_weight, post_weight=self.post_weight, gate=gate)
+        return residual_out

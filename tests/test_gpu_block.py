@@ -794,3 +794,101 @@ def test_chain_of_gradients_against_autograd(gpu):
     for n, t in d.items():
         err = float((g[n].cpu().double() - t.grad).norm())
         assert err <= 8 * 72 * U * mag[n], (n, err, mag[n])
+
+
+# ---- a block around the layer ---------------------------------------------------------
+
+def make_block(T=40, layout=moe.LAYOUT_CONTIGUOUS, post=True, gate="token"):
+    import moe_synth
+    cfg = moe_synth.custom(name="block", T=T, E=8, top_k=2, K=256, N=256, seed=91)
+    inp = moe_synth.make_inputs(cfg, "cuda")
+    p = moe.Problem(T, 256, 256, 8, 2, layout)
+    layer = moe.MoeLayer(p, inp["w13"], inp["w13_sf"], inp["w2"], inp["w2_sf"])
+    rng = np.random.default_rng(17)
+    norm = moe.BlockNorm(T, 256, weight_dtype=torch.float32, post_norm=post, gate=gate,
+                         gate_sigmoid=True, residual_scale=0.4)
+    w = {n: rand(rng, (256,), torch.float32).cuda() for n in ("pre", "post", "next")}
+    block = moe.MoeBlock(layer, moe.Router(T, 8, 2, score="sigmoid", scale=2.0),
+                         rand(rng, (8, 256), torch.float32, 0.1).cuda(), norm, w["pre"],
+                         w["post"] if post else None, rand(rng, (8,), torch.float32, 0.1).cuda())
+    x = rand(rng, (T, 256), torch.bfloat16, 2.0).cuda()
+    g = rand(rng, (T,), torch.bfloat16).cuda()
+    pad = torch.from_numpy((rng.random(T) < 0.1).astype(np.uint8)).cuda()
+    return block, layer, norm, w, x, g, pad
+
+
+@pytest.mark.parametrize("layout", [moe.LAYOUT_CONTIGUOUS, moe.LAYOUT_INDEXED])
+def test_block_runs_its_steps(gpu, layout):
+    """Every step's result inside the block against the oracle (the layer
+    itself against its own direct call, bit for bit)."""
+    block, layer, norm, w, x, g, pad = make_block(layout=layout)
+    nxt = torch.empty_like(x)
+    out = block(x, gate=g, is_padding=pad, next_normed=nxt, next_weight=w["next"])
+    h = B.block_norm(f64(x), w_pre=f64(w["pre"]), eps=float(np.float32(1e-6)))["normed"]
+    close(block.hidden, *h, 2 * REL_NORM, "hidden")
+    logits = torch.matmul(block.hidden.float(), block.router_weight.t())
+    ids, wt = B.router_topk(f64(logits), 2, "sigmoid", bias=f64(block.bias), scale=2.0,
+                            pad=pad.cpu().numpy())
+    assert np.array_equal(block.topk_ids.cpu().numpy(), ids)
+    close(block.topk_weights, wt, np.abs(wt), REL_EXP, "weights")
+    y = layer(block.hidden, block.topk_ids, block.topk_weights, is_padding=pad)
+    assert torch.equal(y, block.y)
+    assert (block.y[pad.bool()] == 0).all() and block.y.abs().sum() > 0
+    want = B.block_norm(f64(x), f64(y), True, f64(w["post"]), f64(g), "token", True,
+                        f64(w["next"]), float(np.float32(1e-6)), float(np.float32(0.4)))
+    close(out, *want["residual_out"], REL_NORM, "residual_out")
+    close(nxt, *want["normed"], 2 * REL_NORM, "next_normed")
+    # the norm that the block before left, and the stream updated in place
+    again = x.clone()
+    assert block(again, normed=block.hidden.clone(), gate=g, is_padding=pad,
+                 residual_out=again) is again
+    assert torch.equal(again, out)
+
+
+def test_block_in_a_graph(gpu):
+    """Router and norms captured with the layer between them (the logits'
+    product, a library call, is made outside)."""
+    block, layer, norm, w, x, g, pad = make_block()
+    out = block(x, gate=g, is_padding=pad)
+    logits = torch.matmul(block.hidden.float(), block.router_weight.t())
+    got = torch.empty_like(x)
+    torch.cuda.synchronize()
+
+    def rest():
+        moe.block_norm(block.pre, x, block.hidden, pre_weight=w["pre"])
+        moe.router_topk(block.router, logits, block.topk_ids, block.topk_weights,
+                        bias=block.bias, is_padding=pad)
+        layer(block.hidden, block.topk_ids, block.topk_weights, out=block.y, is_padding=pad)
+        moe.block_norm(norm, x, y=block.y, residual_out=got, post_weight=w["post"], gate=g)
+
+    rest()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rest()
+    for _ in range(3):
+        got.zero_()
+        block.y.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, out)
+
+
+def test_block_refusals(gpu):
+    block, layer, norm, w, x, g, pad = make_block()
+    r, rw = block.router, block.router_weight
+    for kw, word in [(dict(router=moe.Router(41, 8, 2)), "router"),
+                     (dict(router=moe.Router(40, 8, 1)), "router"),
+                     (dict(norm=moe.BlockNorm(40, 128)), "norm"),
+                     (dict(norm=moe.BlockNorm(40, 256, dtype=torch.float16)), "bfloat16"),
+                     (dict(router_weight=rw[:7]), "router_weight"),
+                     (dict(router_weight=rw.half()), "router_weight")]:
+        with pytest.raises(ValueError, match=word):
+            moe.MoeBlock(**{**dict(layer=layer, router=r, router_weight=rw, norm=norm), **kw})
+    batched = moe.MoeLayer(moe.Problem(40, 256, 256, 8, 2, moe.LAYOUT_BATCHED, 80), layer.w13,
+                           layer.w13_sf, layer.w2, layer.w2_sf)
+    with pytest.raises(ValueError, match="layout"):
+        moe.MoeBlock(batched, r, rw, norm)
+    with pytest.raises(ValueError, match="gate"):
+        block(x, gate=g[:-1])
+    with pytest.raises(moe.MoeError, match="gate is NULL"):
+        block(x)
