@@ -52,6 +52,22 @@ __device__ __forceinline__ bool near_keys(uint32_t b, uint32_t c, float near) {
   return fb - from_ordered(c) <= near * (1.0f + fabsf(fb));
 }
 
+// 2, 4 or 8 bytes at any 2-byte address
+template <int BYTES>
+struct Few;
+template <>
+struct Few<2> {
+  typedef uint16_t Any;
+};
+template <>
+struct Few<4> {
+  typedef uint32_t __attribute__((aligned(2))) Any;
+};
+template <>
+struct Few<8> {
+  typedef uint32_t __attribute__((ext_vector_type(2))) __attribute__((aligned(2))) Any;
+};
+
 // the VPL logits of a lane as the definition counts them; past E: masked
 template <int DT, int VPL>
 __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E, int e0,
@@ -70,9 +86,19 @@ __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E
 #pragma unroll
     for (int i = 0; i < VPL; ++i) x[i] = e0 + i < E ? clean_logit(x[i]) : -INFINITY;
   } else {
+    float f[VPL];
+    if (E % VPL == 0) {                     // one load per lane
+      typedef Few<VPL * RowVec<DT>::kSize> F;
+      const typename F::Any v =
+          *reinterpret_cast<const typename F::Any*>(row + min(e0, E - VPL) * RowVec<DT>::kSize);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      x[i] = e0 + i < E ? clean_logit(RowVec<DT>::load_one(row, e0 + i)) : -INFINITY;
+      for (int i = 0; i < VPL; ++i) f[i] = RowVec<DT>::load_one((const uint8_t*)&v, i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) f[i] = RowVec<DT>::load_one(row, min(e0 + i, E - 1));
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) x[i] = e0 + i < E ? clean_logit(f[i]) : -INFINITY;
   }
 }
 
@@ -463,19 +489,24 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_grad_kernel(
   if (t >= a.T) return;
   const int E = a.E, k = a.k, e0 = lane * VPL;
   const bool dense = !a.sigmoid && !a.renormalize;
-  float xs[VPL];
+  float out[VPL], xs[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) out[i] = 0.0f;
   if (dense) load_logits<DT, VPL>(a.logits, t, E, e0, xs);
   int id = lane < k ? ids[t * k + lane] : -1;
   if (id < 0 || id >= E) id = -1;
-  float x = id >= 0 ? clean_logit(RowVec<DT>::load_one((const uint8_t*)a.logits, t * E + id))
-                    : -INFINITY;
-  if (x == -INFINITY) id = -1;
-  const float g = id >= 0 ? grad_w[t * k + lane] : 0.0f;
-  float out[VPL];
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) out[i] = 0.0f;
-  float d = 0.0f;                           // the chosen experts' gradients
-  if (__ballot(id >= 0) != 0) {
+  // the chosen experts' gradients: of their logits, or, for a softmax over all
+  // experts, still of their weights (no load then waits for the ids)
+  float d = lane < k ? grad_w[t * k + lane] : 0.0f;
+  if (id < 0) d = 0.0f;
+  if (!dense && __ballot(id >= 0) != 0) {
+    float x = -INFINITY;
+    if (id >= 0) x = clean_logit(RowVec<DT>::load_one((const uint8_t*)a.logits, t * E + id));
+    if (x == -INFINITY) {
+      id = -1;
+      d = 0.0f;
+    }
+    const float g = d;
     if (a.sigmoid) {
       const float s = id >= 0 ? sigmoid_f32(x) : 0.0f;
       // 1 - s as sigmoid(-x): no cancellation for large x
@@ -486,35 +517,38 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_grad_kernel(
       } else {
         d = g * ds;
       }
-    } else if (a.renormalize) {
+    } else {
       const float mx = wave_max(x);         // every lane takes part
       const float p0 = id >= 0 ? expf(x - mx) : 0.0f;
       const float p = p0 / wave_sum(p0);
       d = p * (g - wave_sum(g * p));
-    } else {
-      float m = xs[0], total = 0.0f;
-#pragma unroll
-      for (int i = 1; i < VPL; ++i) m = fmaxf(m, xs[i]);
-      m = wave_max(m);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        xs[i] = xs[i] > -INFINITY ? expf(xs[i] - m) : 0.0f;
-        total += xs[i];
-      }
-      total = wave_sum(total);
-      const float p = id >= 0 ? expf(x - m) / total : 0.0f;
-      const float dot = wave_sum(g * p) * a.scale;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) out[i] = -dot * (xs[i] / total);
-      d = p * g;
     }
     d = id >= 0 ? d * a.scale : 0.0f;
-    for (int j = 0; j < k; ++j) {           // slot order: a repeated id adds up
-      const int ej = __builtin_amdgcn_readlane(id, j) - e0;
-      const float dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(d), j));
+  }
+  for (int j = 0; j < k; ++j) {             // slot order: a repeated id adds up
+    const int ej = __builtin_amdgcn_readlane(id, j) - e0;
+    const float dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(d), j));
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) out[i] += ej == i ? dj : 0.0f;
+    for (int i = 0; i < VPL; ++i) out[i] += ej == i ? dj : 0.0f;
+  }
+  if (dense) {
+    float m = xs[0], total = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, xs[i]);
+    m = wave_max(m);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      xs[i] = xs[i] > -INFINITY ? expf(xs[i] - m) : 0.0f;
+      if (xs[i] == 0.0f) out[i] = 0.0f;     // masked: whatever its weight's gradient
+      total += xs[i];
+      dot = fmaf(xs[i], out[i], dot);
     }
+    total = wave_sum(total);
+    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+    dot = wave_sum(dot) * inv;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      out[i] = xs[i] == 0.0f ? 0.0f : xs[i] * inv * a.scale * (out[i] - dot);
   }
   uint8_t* row = grad_logits + t * E * RowVec<DT>::kSize;
   constexpr int N = RowVec<DT>::N;
@@ -522,6 +556,12 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_grad_kernel(
 #pragma unroll
     for (int i = 0; i < VPL; i += N)
       if (e0 + i < E) RowVec<DT>::template store<true>(row, e0 + i, E, RowVec<DT>::pack(out + i));
+  } else if (E % VPL == 0) {
+    typedef Few<VPL * RowVec<DT>::kSize> F;
+    typename F::Any v;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) RowVec<DT>::store_one((uint8_t*)&v, i, out[i]);
+    if (e0 < E) *reinterpret_cast<typename F::Any*>(row + e0 * RowVec<DT>::kSize) = v;
   } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
