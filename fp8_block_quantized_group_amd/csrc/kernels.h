@@ -279,7 +279,7 @@ struct NormArgs {
 };
 hipError_t launch_norm(const NormArgs& a, int dtype, bool w32, hipStream_t stream);
 
-// blocks of the norm gradient at most, each walking its rows
+// blocks of the norm gradient at most (one per CU), each walking its rows
 constexpr int kNormGradBlocks = 256;
 struct NormGradArgs {
   const uint8_t* x;            // [T, H] the stored residual stream

@@ -9,6 +9,12 @@
 // hold VPT vectors each, the row sums cross the lanes of a wave by shuffles
 // and, for BT over 64, the waves through LDS.  Everything is fp32; h is made
 // from r' before r' is rounded.
+//
+// Bound by HBM: every stream is read or written once, non-temporal.  MI355X,
+// where a 2 GiB copy moves 5.1 TB/s: forward 16381 x 4096 bf16 91 us (537 MB,
+// 5.9 TB/s); gradients 4095 x 7168 bf16 77-84 us (352 MB, 4.2-4.6 TB/s: the
+// row sums' barriers leave gaps, and the column sums of 256 blocks cost 22 MB
+// each way).
 #include <type_traits>
 
 #include "kernels.h"
@@ -285,7 +291,8 @@ __device__ __forceinline__ float token_gate(const NormGradArgs& a, int64_t row) 
 // Rows in registers: BT lanes per row, kGradThreads / BT rows side by side
 // (one for BT above), each lane with the column sums of its VPT vectors.
 //
-// One block per CU: the column sums and the next row, which is loaded while
+// One block per CU (two cost more in weights and column sums than they hide:
+// 120 us against 100): the column sums and the next row, which is loaded while
 // this one is worked on, take the registers (FULL, a gate of the rows' own
 // shape, takes the place of the gate's column sums).  The weights and a
 // per-channel gate lie in LDS as fp32, so that nothing but rows goes through
@@ -547,9 +554,11 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
   }
 }
 
-// Rows too wide for registers: one block per row, which is read three times
-// (from the caches after the first): for its first sums, for its second, and
-// to write.  The block's column sums are kept in its part itself.
+// Rows too wide for registers (2-byte types past 8192 columns, fp32 past
+// 8192): one block per row, which is read three times (from the caches after
+// the first): for its first sums, for its second, and to write.  The block's
+// column sums are kept in its part itself.  2048 x 16384 bf16: 423 us, 0.95
+// TB/s of what the call has to move; 63 us without a block, in registers.
 constexpr int kWideThreads = 1024;
 
 template <class RV, bool W32>

@@ -7,8 +7,17 @@
 //   its gradient       grad_x[t] = sum_j grad_rows[slot_row[t, j]]
 //   unpermute          out[t] = sum_j w[t, j] rows[slot_row[t, j]]
 //   its gradients      grad_rows[r] = w grad_out[t], grad_w[t, j] = <grad_out[t], rows[r]>
-// Sums run over j ascending in fp32 and are rounded once.  Every kernel is a
-// stream over the rows: one 16-byte vector per lane and row.
+// Sums run over j ascending in fp32 and are rounded once.
+//
+// The rows' kernels are streams, bound by HBM: one 16-byte vector per lane
+// and row, a token's rows all in flight together.  Rows are read and written
+// once and are larger than the caches: non-temporal, both ways (loads through
+// the caches: 204 us against 188 for the combine below); a permuted token was
+// just written by the kernel before and is read through the caches (108 us
+// with non-temporal loads, 91 without).  MI355X, where a 2 GiB copy moves
+// 5.1 TB/s: permute 4096 x 8 rows of 7168 bf16 columns 89 us (505 MB, 5.7
+// TB/s), combine 16384 x 8 x 4096 bf16 188 us (1.15 GB, 6.1 TB/s), its
+// gradients 417 us (2.17 GB, 5.2 TB/s).
 #include <type_traits>
 
 #include "kernels.h"
@@ -21,8 +30,9 @@ namespace {
 constexpr int kSortThreads = 256;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortRounds = kSortChunk / kSortThreads;
-// Up to this many chunks every ranking block adds up the chunks before it;
-// above, one block turns the counts into first rows for all of them.
+// Up to this many chunks every ranking block adds up the chunks before it, 16
+// loads in flight; above, one block turns the counts into first rows for all
+// of them (at 32 chunks, 256 experts: 5.9 us here, 11.4 + 5.5 in two kernels).
 constexpr int kSortInline = 64;
 
 // the slot's expert, -1 when it is unrouted
@@ -33,6 +43,9 @@ __device__ __forceinline__ int routed_id(const int32_t* ids, const uint8_t* pad,
   if (pad != nullptr && pad[(uint32_t)slot / (uint32_t)k] != 0) return -1;   // slots < 2^31
   return id;
 }
+
+// Slots are ranked in chunks by a block each: latency, not bytes (4096 x 8
+// slots: 4.6 us to count, 5.9 to rank).
 
 // per chunk of slots, how many go to each expert
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const SortArgs a) {
@@ -209,8 +222,8 @@ __device__ __forceinline__ Place place(int log_width, int pieces) {
 // N columns.  The columns that the lane before it has too come out the same
 // from both.
 
-// 4: the rows themselves: a token's vector is read once and written to the
-// rows of its routed slots
+// the rows themselves: a token's vector is read once and written to the rows
+// of its routed slots
 template <class RV>
 __global__ __launch_bounds__(256) void permute_rows_kernel(const RowsArgs a, int log_width,
                                                            int pieces) {

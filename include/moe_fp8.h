@@ -514,7 +514,7 @@ typedef struct {
  *  - Experts are ordered by a key, largest first, ties by the lower index:
  *    the logit, or, with a bias or group_top 2, score + bias[e] evaluated in
  *    64 bits (bias fp32 [E] or NULL; for the choice alone, it does not enter
- *    the weights).
+ *    the weights; a bias of NaN or -inf keeps its expert from being chosen).
  *  - With groups, a group's value is the sum of its group_top largest
  *    unmasked keys; only experts of the topk_groups largest groups (ties by
  *    the lower index) are chosen from.
@@ -556,9 +556,9 @@ moe_status_t moe_permute_workspace_size(const moe_rows_t* p, size_t* bytes);
  * int32 [E+1], slot_row int32 [T, top_k] (-1 when unrouted), row_slot int32
  * [T*top_k] (the flat slot of each row).  rows and row_slot entries behind
  * the last routed row (expert_offsets[E]) stay as they were.  T = 0 still
- * writes expert_offsets (zeros).  ws: device scratch of
- * moe_permute_workspace_size bytes, 4-byte aligned; calls sharing one must
- * not overlap. */
+ * writes expert_offsets (zeros).  rows must not overlap x.  ws: device
+ * scratch of moe_permute_workspace_size bytes, 4-byte aligned; calls sharing
+ * one must not overlap. */
 moe_status_t moe_permute(const moe_rows_t* p, const void* x, const int32_t* topk_ids,
                          const uint8_t* is_padding, void* rows, int32_t* expert_offsets,
                          int32_t* slot_row, int32_t* row_slot, void* ws, size_t ws_bytes,

@@ -200,6 +200,23 @@ def test_router_keys_closer_than_32_bits(gpu):
     check_router(x, 2, bias, None, score="softmax", renormalize=False)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_router_special_biases(gpu, score, groups):
+    """Infinite, NaN and large biases (the score drowns in them, in 64 bits
+    too: ties by the index)."""
+    rng = np.random.default_rng(14)
+    x = rand(rng, (40, 64), torch.float32, 2.0)
+    x[3, ::3] = -np.inf
+    bias = rand(rng, (64,), torch.float32, 0.1)
+    for i, v in enumerate((np.inf, -np.inf, np.nan, 1e30, 1e30, -1e30, 1e9, 1e9, 3e38)):
+        bias[7 * i % 64] = v
+    with np.errstate(invalid="ignore"):
+        check_router(x, 7, bias, None, score=score, groups=groups,
+                     topk_groups=min(3, groups), group_top=2)
+        check_router(x, 64, bias, None, score=score)
+
+
 def test_router_gradient_of_repeated_and_foreign_ids(gpu):
     """Ids the forward call never returns: repeated ones add up, ids outside
     the experts and masked experts contribute nothing."""
@@ -367,6 +384,28 @@ def test_rows_unaligned(gpu):
     close(gw, want_w, mag_w, (H / 64 + 24) * U, "grad_weights")
 
 
+@pytest.mark.parametrize("T,E,k", [(2000, 400, 2), (30000, 300, 3), (9000, 1024, 8),
+                                   (70000, 7, 1), (700, 33, 3), (683, 256, 3)])
+def test_sort_of_many_slots(gpu, T, E, k):
+    """Every way the sort takes, by its number of slots and experts, against a
+    stable sort."""
+    rng = np.random.default_rng(T)
+    ids, pad = make_ids(rng, T, E, k)
+    p = moe.ExpertRows(T, 8, E, k, dtype=torch.float32)
+    x = rand(rng, (T, 8), torch.float32)
+    out = run_permute(p, x.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(pad).cuda())
+    e = np.where((ids < 0) | (ids >= E) | (pad[:, None] != 0), E, ids).reshape(-1)
+    order = np.argsort(e, kind="stable")
+    off = np.searchsorted(e[order], np.arange(E + 1))
+    R = off[E]
+    slot_row = np.full(T * k, -1)
+    slot_row[order[:R]] = np.arange(R)
+    assert np.array_equal(out["expert_offsets"].cpu().numpy(), off)
+    assert np.array_equal(out["slot_row"].cpu().numpy().reshape(-1), slot_row)
+    assert np.array_equal(out["row_slot"][:R].cpu().numpy(), order[:R])
+    assert torch.equal(out["rows"][:R].cpu(), x[torch.from_numpy(order[:R] // k)])
+
+
 def test_sort_of_no_tokens(gpu):
     p = moe.ExpertRows(0, 64, 9, 4)
     out = run_permute(p, torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"),
@@ -512,7 +551,8 @@ def test_block_norm(gpu, H, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
-@pytest.mark.parametrize("T,H", [(1, 96), (700, 40), (2100, 200), (1030, 4096), (600, 7168)])
+@pytest.mark.parametrize("T,H", [(1, 96), (700, 40), (2100, 200), (1030, 4096), (600, 7168),
+                                 (530, 1800), (514, 12000)])
 def test_block_norm_many_rows(gpu, T, H, dtype):
     """More rows than blocks: every block walks several."""
     rng = np.random.default_rng(T)
