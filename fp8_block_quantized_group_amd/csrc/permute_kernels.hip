@@ -339,10 +339,12 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(const RowsArgs a, int
 
 // Gradients of the weighted sum, WIDTH lanes (a wave or the block) per
 // token: for 8 slots at a time, the row's gradient is written and its
-// product with the token's gradient summed as the rows go by.
+// product with the token's gradient summed as the rows go by.  The rows may be
+// overwritten by their gradients: a lane writes the columns that it alone
+// reads (the last vector's first ones may still be waited for by another wave).
 template <class RV, int WIDTH>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const RowsArgs a,
-                                                           const uint8_t* __restrict__ rows,
+                                                           const uint8_t* rows,
                                                            float* __restrict__ grad_w) {
   constexpr int N = RV::N;
   __shared__ float part[4][8];
@@ -387,7 +389,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const RowsArgs a,
           dot[u] = fmaf(own[i], f[i], dot[u]);
           d[i] = w[u] * g[i];
         }
-        RV::template store_at<true>(a.out + r[u] * pitch, col, RV::pack(d));
+        RV::template store_tail<true>(a.out + r[u] * pitch, col, v0, RV::pack(d));
       }
     }
 #pragma unroll

@@ -90,6 +90,22 @@ struct RowVec {
     }
   }
 
+  // columns [v0, c + N) of the vector at c, c <= v0
+  template <bool NT>
+  static __device__ __forceinline__ void store_tail(uint8_t* row, int c, int v0, Raw v) {
+    if (c == v0) {
+      store_at<NT>(row, c, v);
+      return;
+    }
+    uint8_t* p = row + (int64_t)c * kSize;
+#pragma unroll
+    for (int i = 1; i < N; ++i) {
+      if (c + i < v0) continue;
+      if (kSize == 4) reinterpret_cast<uint32_t*>(p)[i] = v[i & 3];
+      else reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+    }
+  }
+
   static __device__ __forceinline__ void unpack(const u32x4_t v, float f[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -157,6 +173,10 @@ struct RowOne {
   template <bool NT>
   static __device__ __forceinline__ void store(uint8_t* row, int col, int H, Raw v) {
     if (col < H) store_at<NT>(row, col, v);
+  }
+  template <bool NT>
+  static __device__ __forceinline__ void store_tail(uint8_t* row, int c, int, Raw v) {
+    store_at<NT>(row, c, v);
   }
   static __device__ __forceinline__ void unpack(const Raw v, float f[1]) {
     f[0] = __uint_as_float(v);

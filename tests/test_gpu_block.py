@@ -358,6 +358,26 @@ def test_unpermute_backward_in_place(gpu):
     assert torch.equal(gr, rows) and torch.equal(gw, gw2)
 
 
+@pytest.mark.parametrize("dtype,H", [(torch.bfloat16, 2049), (torch.bfloat16, 2563),
+                                     (torch.float16, 4103), (torch.bfloat16, 4101),
+                                     (torch.float32, 1025), (torch.float32, 1283)])
+def test_unpermute_backward_in_place_of_ragged_rows(gpu, dtype, H):
+    """A row's last, partial vector is another wave's, or the next turn's: it
+    must not write columns that the vector before it still reads."""
+    rng = np.random.default_rng(H)
+    T, E, k = 700, 8, 9
+    ids, pad = make_ids(rng, T, E, k)
+    _, slot_row, _ = B.sort_slots(ids, E, pad)
+    sr = torch.from_numpy(slot_row).int().cuda()
+    rows, g = rand(rng, (T * k, H), dtype).cuda(), rand(rng, (T, H), dtype).cuda()
+    w = torch.rand((T, k), device="cuda")
+    p = moe.ExpertRows(T, H, E, k, dtype=dtype)
+    gr, gw, gw2 = rows.clone(), torch.zeros_like(w), torch.zeros_like(w)
+    moe.unpermute_backward(p, g, rows, sr, w, gr, gw)
+    moe.unpermute_backward(p, g, rows, sr, w, rows, gw2)
+    assert torch.equal(gr, rows) and torch.equal(gw, gw2)
+
+
 def test_rows_unaligned(gpu):
     rng = np.random.default_rng(12)
     T, E, k, H = 40, 8, 2, 264
