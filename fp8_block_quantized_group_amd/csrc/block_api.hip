@@ -68,7 +68,7 @@ moe_status_t check_rows(const moe_rows_t* p) {
   if ((int64_t)p->num_tokens * p->top_k >= (int64_t)1 << 31)
     return fail(MOE_ERR_UNSUPPORTED, "num_tokens * top_k must be < 2^31");
   if (!valid_dtype(p->dtype)) return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", p->dtype);
-  // the streaming kernels' one-dimensional grids: at most 32 pieces of a row
+  // the streaming kernels count their blocks, at most 32 pieces of a row, in 32 bits
   if ((int64_t)p->num_tokens * ((p->hidden + 1023) / 1024) >= (int64_t)1 << 31)
     return fail(MOE_ERR_UNSUPPORTED, "num_tokens * hidden / 1024 must be < 2^31");
   return MOE_OK;

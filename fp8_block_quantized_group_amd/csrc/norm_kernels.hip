@@ -147,7 +147,7 @@ __global__ __launch_bounds__(BT == 64 ? 256 : BT) void norm_kernel(const NormArg
   constexpr int N = RV::N;
   constexpr bool EARLY = VPT <= 2;
   __shared__ float buf[4][1][16];
-  const int64_t row = BT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t row = BT == 64 ? (int64_t)block_index() * 4 + (threadIdx.x >> 6) : block_index();
   if (row >= a.T) return;                       // whole waves (BT 64) or never
   const int first = BT == 64 ? threadIdx.x & 63 : threadIdx.x;
   const int H = a.H;
@@ -718,7 +718,7 @@ hipError_t norm_dt(const NormArgs& a, hipStream_t stream) {
     constexpr int BT = decltype(shape)::BT, VPT = decltype(shape)::VPT;
     typedef typename decltype(shape)::RV RV;
     const int64_t grid = BT == 64 ? (a.T + 3) / 4 : a.T;
-    norm_kernel<RV, W32, BT, VPT><<<(unsigned)grid, BT == 64 ? 256 : BT, 0, stream>>>(a);
+    norm_kernel<RV, W32, BT, VPT><<<grid_of(grid), BT == 64 ? 256 : BT, 0, stream>>>(a);
     return hipGetLastError();
   };
   if (a.H < RowVec<DT>::N) return go(Shape<RowOne<DT>, 64, 1>());

@@ -113,7 +113,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_rank_kernel(const SortArgs 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = a.E;
   int32_t* mine = counts + wave * E;
   for (int e = lane; e < E; e += 64) mine[e] = 0;
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_order();
   const int64_t slot0 = (int64_t)blockIdx.x * kSortChunk + wave * (64 * kSortRounds) + lane;
   const uint64_t below = lane == 0 ? 0ull : ~0ull >> (64 - lane);
   int id[kSortRounds], rank[kSortRounds];
@@ -134,10 +134,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_rank_kernel(const SortArgs 
     rank[r] = 0;
     if (id[r] >= 0) {
       rank[r] = mine[id[r]] + before;
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_order();
       if (before == 0) mine[id[r]] = rank[r] + __popcll(same);
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
   }
   __syncthreads();
   // a thread per PER consecutive experts: the first row of the chunk's slots
@@ -211,10 +211,9 @@ struct Place {
   int v;          // vector of the row
 };
 __device__ __forceinline__ Place place(int log_width, int pieces) {
-  const int64_t b = blockIdx.x;
-  const int64_t piece = b % pieces;
-  const int64_t group = b / pieces;
-  return Place{(group << (8 - log_width)) + (threadIdx.x >> log_width),
+  const uint32_t b = block_index();
+  const uint32_t group = b / (uint32_t)pieces, piece = b - group * (uint32_t)pieces;
+  return Place{((int64_t)group << (8 - log_width)) + (threadIdx.x >> log_width),
                (int)(piece << log_width) + (int)(threadIdx.x & ((1 << log_width) - 1))};
 }
 
@@ -349,7 +348,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const RowsArgs a,
   constexpr int N = RV::N;
   __shared__ float part[4][8];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * (256 / WIDTH) + (WIDTH == 64 ? wave : 0);
+  const int64_t t = (int64_t)block_index() * (256 / WIDTH) + (WIDTH == 64 ? wave : 0);
   if (t >= a.T) return;                  // whole waves (WIDTH 64) or never
   const int first = WIDTH == 64 ? lane : (int)threadIdx.x;
   const int64_t pitch = (int64_t)a.H * RV::kSize;
@@ -455,16 +454,15 @@ hipError_t stream_rows(const RowsArgs& a, const SortArgs* sort, hipStream_t stre
   split_row(a.H, RV::N, &log_width, &pieces);
   const int per_block = 256 >> log_width;
   const int64_t grid = (a.T + per_block - 1) / per_block * pieces;
-  if (grid >= (int64_t)1 << 31) return hipErrorInvalidValue;
   if (sort == nullptr) {
-    combine_rows_kernel<RV><<<(unsigned)grid, 256, 0, stream>>>(a, log_width, pieces);
+    combine_rows_kernel<RV><<<grid_of(grid), 256, 0, stream>>>(a, log_width, pieces);
   } else if (a.slots <= kSmallSlots && a.k * a.slots <= kSmallCompares) {
     const size_t lds = (size_t)(a.slots + kSmallBatch - 1 + a.k) * sizeof(int32_t);
     permute_small_kernel<RV><<<(unsigned)(a.T * pieces), 256, lds, stream>>>(a, *sort, pieces);
   } else {
     const hipError_t err = launch_sort(*sort, stream);
     if (err != hipSuccess) return err;
-    permute_rows_kernel<RV><<<(unsigned)grid, 256, 0, stream>>>(a, log_width, pieces);
+    permute_rows_kernel<RV><<<grid_of(grid), 256, 0, stream>>>(a, log_width, pieces);
   }
   return hipGetLastError();
 }
@@ -478,13 +476,13 @@ hipError_t rows_dt(const RowsArgs& a, const SortArgs* sort, hipStream_t stream) 
 template <int DT>
 hipError_t combine_grad_dt(const RowsArgs& a, const uint8_t* rows, float* grad_w,
                            hipStream_t stream) {
-  const unsigned waves = (unsigned)((a.T + 3) / 4);
+  const dim3 waves = grid_of((a.T + 3) / 4);
   if (a.H < RowVec<DT>::N)
     combine_grad_kernel<RowOne<DT>, 64><<<waves, 256, 0, stream>>>(a, rows, grad_w);
   else if (a.H <= 256 * RowVec<DT>::N)
     combine_grad_kernel<RowVec<DT>, 64><<<waves, 256, 0, stream>>>(a, rows, grad_w);
   else
-    combine_grad_kernel<RowVec<DT>, 256><<<(unsigned)a.T, 256, 0, stream>>>(a, rows, grad_w);
+    combine_grad_kernel<RowVec<DT>, 256><<<grid_of(a.T), 256, 0, stream>>>(a, rows, grad_w);
   return hipGetLastError();
 }
 

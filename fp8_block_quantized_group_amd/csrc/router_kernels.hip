@@ -152,7 +152,7 @@ __device__ __forceinline__ bool keep_groups(const RouterArgs& a, uint32_t (&key)
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (lane * VPL + i < a.E) wkeys[lane * VPL + i] = key[i];
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
     if (lane < a.groups)
       for (int j = 0; j < size; ++j) merge_top2(b, s, wkeys[lane * size + j], 0);
   }
@@ -258,7 +258,7 @@ __device__ int choose_exactly(const RouterArgs& a, const float (&x)[VPL], float 
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (lane * VPL + i < a.E) wkeys[lane * VPL + i] = key[i];
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
     uint64_t best = 0, second = 0;          // lane g: of group g
     if (lane < a.groups) {
 #pragma unroll 8
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(const Ro
   extern __shared__ uint64_t lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = (int64_t)blockIdx.x * kRouterWaves + wave;
+  const int64_t t = (int64_t)block_index() * kRouterWaves + wave;
   if (t >= a.T) return;
   uint64_t* wkeys = lds + (int64_t)wave * a.E;
   const int E = a.E, k = a.k, e0 = lane * VPL;
@@ -494,7 +494,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_grad_kernel(
     uint8_t* __restrict__ grad_logits) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = (int64_t)blockIdx.x * kRouterWaves + wave;
+  const int64_t t = (int64_t)block_index() * kRouterWaves + wave;
   if (t >= a.T) return;
   const int E = a.E, k = a.k, e0 = lane * VPL;
   const bool dense = !a.sigmoid && !a.renormalize;
@@ -590,7 +590,7 @@ hipError_t per_lane(int E, F&& go) {
 
 template <int DT>
 hipError_t topk_dt(RouterArgs a, hipStream_t stream) {
-  const unsigned grid = (unsigned)((a.T + kRouterWaves - 1) / kRouterWaves);
+  const dim3 grid = grid_of((a.T + kRouterWaves - 1) / kRouterWaves);
   const size_t lds = a.groups > 1 ? (size_t)kRouterWaves * a.E * sizeof(uint64_t) : 0;
   return per_lane(a.E, [&](auto vpl) {
     constexpr int VPL = decltype(vpl)::value;
@@ -606,7 +606,7 @@ hipError_t topk_dt(RouterArgs a, hipStream_t stream) {
 template <int DT>
 hipError_t grad_dt(const RouterArgs& a, const int32_t* ids, const float* grad_w, void* grad_logits,
                    hipStream_t stream) {
-  const unsigned grid = (unsigned)((a.T + kRouterWaves - 1) / kRouterWaves);
+  const dim3 grid = grid_of((a.T + kRouterWaves - 1) / kRouterWaves);
   return per_lane(a.E, [&](auto vpl) {
     router_grad_kernel<DT, decltype(vpl)::value>
         <<<grid, 64 * kRouterWaves, 0, stream>>>(a, ids, grad_w, (uint8_t*)grad_logits);

@@ -187,6 +187,25 @@ struct RowOne {
   }
 };
 
+// Grids in two dimensions: a dimension holds fewer than 2^32 lanes, 2^22
+// blocks of 1024.  A kernel compares its block's index (at most 2^31 blocks,
+// rounded up to rows of the grid) with what there is.
+constexpr int64_t kGridX = 1 << 20;
+inline dim3 grid_of(int64_t blocks) {
+  return dim3((unsigned)(blocks < kGridX ? blocks : kGridX),
+              (unsigned)((blocks + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ uint32_t block_index() {
+  return blockIdx.y * (uint32_t)kGridX + blockIdx.x;
+}
+
+// Between a wave's stores to LDS and other lanes' loads: LDS takes a wave's
+// accesses in order, the compiler has to as well.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Reductions over the 64 lanes of a wave, the same in every lane, in a fixed
 // order: four steps shift inside the rows of 16 lanes, two carry a row's
 // result to the next ones (DPP operands of the adds themselves, where a

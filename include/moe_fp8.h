@@ -476,8 +476,9 @@ moe_status_t moe_forward_static(const moe_problem_t* p, const void* hidden,
  * (moe_dtype_t); data pointers need their element's alignment only, index
  * arrays 4 bytes.  Sums, softmax statistics and norms are held in fp32 and
  * rounded once on the way out.  Results do not depend on timing: no sum's
- * order does.  An empty batch (num_tokens 0) is a no-op except where a call
- * below says what it still writes. */
+ * order does.  Outputs must not overlap inputs or each other except where a
+ * call says so (then as the same pointer).  An empty batch (num_tokens 0) is
+ * a no-op except where a call below says what it still writes. */
 
 /* Element types of the calls below. */
 typedef enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1, MOE_DT_F32 = 2 } moe_dtype_t;
@@ -536,7 +537,8 @@ moe_status_t moe_router_topk_backward(const moe_router_t* p, const void* logits,
                                       void* grad_logits, void* stream);
 
 /* Rows sorted by expert (host struct).  Requirements: 1 <= hidden <= 32768;
- * 1 <= num_experts <= 1024; top_k >= 1; num_tokens * top_k < 2^31. */
+ * 1 <= num_experts <= 1024; top_k >= 1; num_tokens * top_k < 2^31;
+ * num_tokens * ceil(hidden / 1024) < 2^31. */
 typedef struct {
   int32_t num_tokens;
   int32_t hidden;
@@ -556,9 +558,9 @@ moe_status_t moe_permute_workspace_size(const moe_rows_t* p, size_t* bytes);
  * int32 [E+1], slot_row int32 [T, top_k] (-1 when unrouted), row_slot int32
  * [T*top_k] (the flat slot of each row).  rows and row_slot entries behind
  * the last routed row (expert_offsets[E]) stay as they were.  T = 0 still
- * writes expert_offsets (zeros).  rows must not overlap x.  ws: device
- * scratch of moe_permute_workspace_size bytes, 4-byte aligned; calls sharing
- * one must not overlap. */
+ * writes expert_offsets (zeros).  ws: device scratch of
+ * moe_permute_workspace_size bytes, 4-byte aligned; calls sharing one must not
+ * overlap. */
 moe_status_t moe_permute(const moe_rows_t* p, const void* x, const int32_t* topk_ids,
                          const uint8_t* is_padding, void* rows, int32_t* expert_offsets,
                          int32_t* slot_row, int32_t* row_slot, void* ws, size_t ws_bytes,

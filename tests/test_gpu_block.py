@@ -487,6 +487,46 @@ def test_rows_past_four_gib(gpu):
     assert ((gw[at].double() - want).abs() <= want * (H / 64 + 24) * U).all()
 
 
+def test_more_tokens_than_a_grid_dimension_holds(gpu):
+    """64 lanes per token and 2^26 tokens: 2^32 lanes."""
+    T, H, E = (1 << 26) + 5, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn((T, E), generator=g, device="cuda", dtype=torch.bfloat16)
+    ids = torch.empty((T, 1), dtype=torch.int32, device="cuda")
+    w = torch.empty((T, 1), device="cuda")
+    r = moe.Router(T, E, 1, dtype=torch.bfloat16)
+    moe.router_topk(r, x, ids, w)
+    assert torch.equal(ids[:, 0], (x[:, 1] > x[:, 0]).int()) and (w == 1).all()
+    gx = torch.full_like(x, 7)
+    moe.router_topk_backward(r, x, ids, w, gx)             # of a constant weight
+    assert (gx == 0).all()
+    del gx, x
+    # rows in their tokens' order, twice the token, weights of 2
+    w.fill_(2.0)
+    tokens = torch.randn((T, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    p = moe.ExpertRows(T, H, 1, 1)
+    out = moe.alloc_permute_outputs(p)
+    moe.permute(p, tokens, ids.zero_(), **out)
+    assert torch.equal(out["rows"], tokens)
+    y = torch.empty_like(tokens)
+    moe.unpermute(p, out["rows"], out["slot_row"], w, y)
+    assert torch.equal(y, tokens * 2)
+    gw = torch.empty_like(w)
+    moe.unpermute_backward(p, tokens, out["rows"], out["slot_row"], w, y.zero_(), gw)
+    assert torch.equal(y, tokens * 2)
+    # eight products, each exact in fp32, and seven or more additions
+    want = torch.cat([(c.float() ** 2).sum(1) for c in tokens.split(1 << 24)])
+    assert ((gw[:, 0] - want).abs() <= 16 * U * want).all()
+    del out, gw, want, w, ids
+    n = moe.BlockNorm(T, H)
+    moe.block_norm(n, tokens, y)
+    for c, d in zip(tokens.split(1 << 24), y.split(1 << 24)):
+        f = c.float()
+        f = f * torch.rsqrt((f * f).mean(1, keepdim=True) + 1e-6)
+        # both within REL_NORM of the norm in 64 bits, then half a step
+        assert ((d.float() - f).abs() <= (2 * REL_NORM + 2 ** -8) * f.abs()).all()
+
+
 # ---- block norms ------------------------------------------------------------------
 
 WIDTHS = [1, 5, 64, 511, 520, 1001, 2048, 3000, 4104, 7168, 8200, 16400, 32768]
