@@ -47,16 +47,19 @@ __device__ __forceinline__ float sigmoid_f32(float x) { return 1.0f / (1.0f + ex
 // Errors of the 32-bit keys.  A sigmoid from v_exp and v_rcp is off by less
 // than 2^-22: its argument's rounding moves it by s (1 - s) |x| 2^-24 at most,
 // exp and reciprocal add a step of s each.  A softmax adds the rounding of
-// its sum, below 2^-19 of s for 1024 terms.  Adding the bias rounds once more.
-// Two keys further apart than kNear * (1 + |key|), and two groups' values
-// further apart than twice that, are in the order of their 64-bit values.
+// its sum, below 2^-19 of s for 1024 terms, and no s is above 1 / total.
+// near is twice that error; adding the bias rounds once more, kNearRound.
+// Two keys further apart than near + kNearRound |key| are in the order of
+// their 64-bit values; so are two groups' values v1 > v2 with v1 - E1 above v2
+// + E2, E = near + kNearRound * the magnitudes added up (they may cancel).
 constexpr float kNearSigmoid = 0x1p-20f;
-constexpr float kNearSoftmax = 0x1p-18f;
+constexpr float kNearSoftmax = 0x1p-18f;    // * 1 / total
+constexpr float kNearRound = 0x1p-22f;
 
 // whether the larger key `b` and the smaller `c` (0: none) may change places
 __device__ __forceinline__ bool near_keys(uint32_t b, uint32_t c, float near) {
   const float fb = from_ordered(b);
-  return fb - from_ordered(c) <= near * (1.0f + fabsf(fb));
+  return fb - from_ordered(c) <= fmaf(kNearRound, fabsf(fb), near);
 }
 
 // 2, 4 or 8 bytes at any 2-byte address
@@ -164,10 +167,14 @@ __device__ __forceinline__ bool keep_groups(const RouterArgs& a, uint32_t (&key)
   }
   const bool keep = better < a.topk_groups && group < a.groups;
   bool unclear = false;
-  if (near > 0.0f) {                      // the last group kept, the best one dropped
-    const float best_dropped = from_ordered(wave_max(keep ? 0u : v));
-    const float last_kept = from_ordered(~wave_max(keep && v != 0u ? ~v : 0u));
-    unclear = last_kept - best_dropped <= 2.0f * near * (1.0f + fabsf(last_kept));
+  if (near > 0.0f) {                      // the least of those kept, the best one dropped
+    const float fv = from_ordered(v);
+    float mag = fabsf(from_ordered(b));
+    if (a.group_top > 1 && s != 0u) mag += fabsf(from_ordered(s));
+    const float err = fminf(fmaf(kNearRound, mag, near), FLT_MAX);
+    const uint32_t dropped = wave_max(keep || v == 0u ? 0u : ordered_bits(fv + err));
+    const uint32_t kept = ~wave_max(keep && v != 0u ? ~ordered_bits(fv - err) : 0u);
+    unclear = kept <= dropped;
   }
   if (by_lanes) {
 #pragma unroll
@@ -392,7 +399,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(const Ro
     for (int i = 0; i < VPL; ++i) total += x[i] > -INFINITY ? expf(x[i] - m) : 0.0f;
     total = wave_sum(total);
   }
-  const float near = !scored ? 0.0f : a.sigmoid ? kNearSigmoid : kNearSoftmax;
+  const float near = !scored ? 0.0f : a.sigmoid ? kNearSigmoid : kNearSoftmax / total;
   float f[VPL];
   if (scored) {
     float bias[VPL];

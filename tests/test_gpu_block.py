@@ -201,6 +201,31 @@ def test_router_keys_closer_than_32_bits(gpu):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,group_top", [(1, 1), (8, 1), (8, 2), (64, 2)])
+@pytest.mark.parametrize("spread", [2.0 ** -21, 2.0 ** -14, 0.5])
+def test_router_scores_close_together(gpu, score, groups, group_top, spread):
+    """Logits that differ by a few to many steps of fp32, with a bias of the
+    scores' size: the order of 64 bits among experts and among groups."""
+    rng = np.random.default_rng(15)
+    x = rand(rng, (300, 128), torch.float32, spread)
+    bias = rand(rng, (128,), torch.float32, spread / 128)
+    check_router(x, 5, bias, None, score=score, groups=groups,
+                 topk_groups=max(1, 3 * groups // 8), group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [2, 8, 13])
+def test_router_group_values_that_cancel(gpu, score, size):
+    """A group's two keys of opposite signs and nearly the same magnitude: in
+    fp32 their sum is off by steps of the keys, not of the sum."""
+    rng = np.random.default_rng(16)
+    x = rand(rng, (200, 8 * size), torch.float32, 2.0 ** -10)
+    bias = torch.full((8 * size,), -2000.0)
+    bias[::size], bias[size - 1::size] = 1000.0, -1000.0
+    check_router(x, 4, bias, None, score=score, groups=8, topk_groups=4, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups", [1, 4])
 def test_router_special_biases(gpu, score, groups):
     """Infinite, NaN and large biases (the score drowns in them, in 64 bits
