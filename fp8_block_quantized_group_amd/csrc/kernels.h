@@ -225,7 +225,8 @@ struct RouterArgs {
   int E, k;
   int groups, topk_groups, group_top;
   int group_size;              // set by the launcher: E / groups, and the log of the
-  int group_lanes_log;         // lanes that hold a group, -1 when they are not 2^0..2^4
+  int group_lanes_log;         // lanes that hold a group, -1 when they are not 2^0..2^4,
+  int row_lanes_log;           // with a wave or a row of 16 lanes per token
   bool sigmoid, renormalize;
   float scale;
 };

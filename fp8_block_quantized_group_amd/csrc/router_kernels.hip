@@ -12,11 +12,12 @@
 //
 // One wave per token; lane l holds the VPL consecutive experts from l * VPL.
 // Bound by vector instructions: about 520 per token of 256 experts, top 8 of
-// 4 of 8 groups (the bytes would take 3.5 us for 16384 tokens, the
-// instructions take 14, the kernel 19).  So reductions are lane exchanges in
-// registers (with shuffles through LDS and 64-bit keys throughout the same
-// call took 60 us), a lane's keys are sorted once, and nothing is in 64 bits
-// that 32 can tell.
+// 4 of 8 groups.  So reductions are lane exchanges in registers (with shuffles
+// through LDS and 64-bit keys throughout 16384 such tokens took 60 us, now
+// 18), a lane's keys are sorted once, nothing is in 64 bits that 32 can tell,
+// and large batches put four tokens into a wave (router_rows_kernel, 15 us,
+// 17 with 5 % padding; the bytes would take 3.5): about 220 per token, then
+// bound by the steps that follow one another in a wave.
 //
 // The choice runs on 32-bit keys as ordered integers, k rounds of a wave
 // maximum; 64-bit keys are computed only for a token where two keys that
@@ -79,7 +80,7 @@ struct Few<8> {
 };
 
 // the VPL logits of a lane as the definition counts them; past E: masked
-template <int DT, int VPL>
+template <int DT, int VPL, bool NT>
 __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E, int e0,
                                             float (&x)[VPL]) {
   const uint8_t* row = (const uint8_t*)logits + t * E * RowVec<DT>::kSize;
@@ -87,7 +88,7 @@ __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E
   if constexpr (VPL % N == 0) {             // E > 64: at least one vector
     u32x4_t v[VPL / N];
 #pragma unroll
-    for (int i = 0; i < VPL / N; ++i) v[i] = RowVec<DT>::template load<true>(row, e0 + i * N, E);
+    for (int i = 0; i < VPL / N; ++i) v[i] = RowVec<DT>::template load<NT>(row, e0 + i * N, E);
 #pragma unroll
     for (int i = 0; i < VPL / N; ++i) {
       RowVec<DT>::settle(v[i], e0 + i * N, E);
@@ -129,65 +130,6 @@ __device__ __forceinline__ uint32_t group_value(uint32_t b, uint32_t s, int grou
   return ordered_bits(from_ordered(b) + from_ordered(s));
 }
 
-// Drops the keys (sets them to 0) of all but the topk_groups best groups.
-// Returns whether two groups' values lie too close to tell.
-template <int VPL>
-__device__ __forceinline__ bool keep_groups(const RouterArgs& a, uint32_t (&key)[VPL],
-                                            uint32_t* wkeys, float near) {
-  const int lane = threadIdx.x & 63;
-  const int size = a.group_size;
-  // groups of 1, 2, 4, 8 or 16 whole lanes meet by lane exchanges; others
-  // through LDS, lane g walking group g
-  const bool by_lanes = a.group_lanes_log >= 0;
-  uint32_t b = 0, s = 0;
-  int group = lane, pitch = 1;
-  if (by_lanes) {
-    const int lanes = 1 << a.group_lanes_log;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) merge_top2(b, s, key[i], 0);
-    if (lanes > 1) merge_lanes<0xB1>(b, s);       // quad_perm [1,0,3,2]
-    if (lanes > 2) merge_lanes<0x4E>(b, s);       // quad_perm [2,3,0,1]
-    if (lanes > 4) merge_lanes<0x141>(b, s);      // row_half_mirror
-    if (lanes > 8) merge_lanes<0x140>(b, s);      // row_mirror
-    group = lane >> a.group_lanes_log;
-    pitch = lanes;
-  } else {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane * VPL + i < a.E) wkeys[lane * VPL + i] = key[i];
-    wave_lds_order();
-    if (lane < a.groups)
-      for (int j = 0; j < size; ++j) merge_top2(b, s, wkeys[lane * size + j], 0);
-  }
-  const uint32_t v = group < a.groups ? group_value(b, s, a.group_top) : 0u;
-  int better = 0;
-  for (int g = 0; g < a.groups; ++g) {
-    const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)v, g * pitch);
-    better += (o > v || (o == v && g < group)) ? 1 : 0;
-  }
-  const bool keep = better < a.topk_groups && group < a.groups;
-  bool unclear = false;
-  if (near > 0.0f) {                      // the least of those kept, the best one dropped
-    const float fv = from_ordered(v);
-    float mag = fabsf(from_ordered(b));
-    if (a.group_top > 1 && s != 0u) mag += fabsf(from_ordered(s));
-    const float err = fminf(fmaf(kNearRound, mag, near), FLT_MAX);
-    const uint32_t dropped = wave_max(keep || v == 0u ? 0u : ordered_bits(fv + err));
-    const uint32_t kept = ~wave_max(keep && v != 0u ? ~ordered_bits(fv - err) : 0u);
-    unclear = kept <= dropped;
-  }
-  if (by_lanes) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = keep ? key[i] : 0u;
-  } else {
-    const uint64_t kept = __ballot(keep);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (!((kept >> ((lane * VPL + i) / size & 63)) & 1)) key[i] = 0u;
-  }
-  return unclear;
-}
-
 // fp64 values as integers of the same order; 0 is below every one of them
 __device__ __forceinline__ uint64_t ordered_bits64(double f) {
   const uint64_t b = (uint64_t)__double_as_longlong(f + 0.0);
@@ -223,6 +165,139 @@ __device__ double exact_key(const RouterArgs& a, float x, float m, double total,
   return s + (double)bias;
 }
 
+// the 64-bit keys of a lane as ordered integers; 0: masked
+template <int VPL>
+__device__ __forceinline__ void exact_keys(const RouterArgs& a, const float (&x)[VPL], float m,
+                                           uint64_t (&key)[VPL]) {
+  const double total = exact_total<VPL>(a, x, m);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    key[i] = 0;
+    if (x[i] > -INFINITY) {
+      const double f = exact_key(a, x[i], m, total,
+                                 a.bias != nullptr ? a.bias[(threadIdx.x & 63) * VPL + i] : 0.0f);
+      if (f > -INFINITY) key[i] = ordered_bits64(f);           // NaN masks
+    }
+  }
+}
+
+// Sets the keys of all but the kept groups to 0; keep: of the lane's group
+// where groups are whole lanes, else of group `lane`.
+template <int VPL, class K>
+__device__ __forceinline__ void drop_groups(const RouterArgs& a, bool keep, K (&key)[VPL]) {
+  if (a.group_lanes_log >= 0) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = keep ? key[i] : 0u;
+  } else {
+    const uint64_t kept = __ballot(keep);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (!((kept >> (((threadIdx.x & 63) * VPL + i) / a.group_size & 63)) & 1)) key[i] = 0u;
+  }
+}
+
+// Which groups are kept, by 64-bit keys (see drop_groups).
+template <int VPL>
+__device__ bool keep_exactly(const RouterArgs& a, const uint64_t (&key)[VPL], uint64_t* wkeys) {
+  const int lane = threadIdx.x & 63;
+  const int size = a.group_size;
+  const bool by_lanes = a.group_lanes_log >= 0;
+  uint64_t best = 0, second = 0;
+  int group = lane, pitch = 1;
+  if (by_lanes) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      second = max(second, min(best, key[i]));
+      best = max(best, key[i]);
+    }
+    pitch = 1 << a.group_lanes_log;
+    for (int d = 1; d < pitch; d <<= 1) {
+      const uint64_t b = __shfl_xor((unsigned long long)best, d);
+      const uint64_t s = __shfl_xor((unsigned long long)second, d);
+      second = max(min(best, b), max(second, s));
+      best = max(best, b);
+    }
+    group = lane >> a.group_lanes_log;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane * VPL + i < a.E) wkeys[lane * VPL + i] = key[i];
+    wave_lds_order();
+    if (lane < a.groups) {
+#pragma unroll 8
+      for (int j = 0; j < size; ++j) {
+        const uint64_t v = wkeys[lane * size + j];
+        second = max(second, min(best, v));
+        best = max(best, v);
+      }
+    }
+  }
+  if (a.group_top > 1 && second != 0)
+    best = ordered_bits64(from_ordered64(best) + from_ordered64(second));
+  int better = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const uint64_t o = read_lane(best, g * pitch);
+    better += (o > best || (o == best && g < group)) ? 1 : 0;
+  }
+  return better < a.topk_groups && group < a.groups;
+}
+
+// Drops the keys (sets them to 0) of all but the topk_groups best groups,
+// where two groups' values lie too close to tell by their 64-bit keys.
+template <int VPL>
+__device__ __forceinline__ void keep_groups(const RouterArgs& a, uint32_t (&key)[VPL],
+                                            const float (&x)[VPL], float m, uint64_t* lds,
+                                            float near) {
+  uint32_t* wkeys = (uint32_t*)lds;
+  const int lane = threadIdx.x & 63;
+  const int size = a.group_size;
+  // groups of 1, 2, 4, 8 or 16 whole lanes meet by lane exchanges; others
+  // through LDS, lane g walking group g
+  const bool by_lanes = a.group_lanes_log >= 0;
+  uint32_t b = 0, s = 0;
+  int group = lane, pitch = 1;
+  if (by_lanes) {
+    const int lanes = 1 << a.group_lanes_log;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) merge_top2(b, s, key[i], 0);
+    if (lanes > 1) merge_lanes<0xB1>(b, s);       // quad_perm [1,0,3,2]
+    if (lanes > 2) merge_lanes<0x4E>(b, s);       // quad_perm [2,3,0,1]
+    if (lanes > 4) merge_lanes<0x141>(b, s);      // row_half_mirror
+    if (lanes > 8) merge_lanes<0x140>(b, s);      // row_mirror
+    group = lane >> a.group_lanes_log;
+    pitch = lanes;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane * VPL + i < a.E) wkeys[lane * VPL + i] = key[i];
+    wave_lds_order();
+    if (lane < a.groups)
+      for (int j = 0; j < size; ++j) merge_top2(b, s, wkeys[lane * size + j], 0);
+  }
+  const uint32_t v = group < a.groups ? group_value(b, s, a.group_top) : 0u;
+  int better = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)v, g * pitch);
+    better += (o > v || (o == v && g < group)) ? 1 : 0;
+  }
+  bool keep = better < a.topk_groups && group < a.groups;
+  if (near > 0.0f) {                      // the least of those kept, the best one dropped
+    const float fv = from_ordered(v);
+    float mag = fabsf(from_ordered(b));
+    if (a.group_top > 1 && s != 0u) mag += fabsf(from_ordered(s));
+    const float err = fminf(fmaf(kNearRound, mag, near), FLT_MAX);
+    const uint32_t dropped = wave_max(keep || v == 0u ? 0u : ordered_bits(fv + err));
+    const uint32_t kept = ~wave_max(keep && v != 0u ? ~ordered_bits(fv - err) : 0u);
+    if (kept <= dropped) {
+      uint64_t exact[VPL];
+      exact_keys<VPL>(a, x, m, exact);
+      wave_lds_order();
+      keep = keep_exactly<VPL>(a, exact, lds);
+    }
+  }
+  drop_groups<VPL>(a, keep, key);
+}
+
 // The n candidates, one per lane, ordered by their 64-bit keys.  Every
 // expert outside is clearly below the first k.
 template <int VPL>
@@ -243,50 +318,13 @@ __device__ int rank_exactly(const RouterArgs& a, const float (&x)[VPL], float m,
 }
 
 // The choice from 64-bit keys: lane j gets the j-th expert (-1: none left).
-// Few tokens come here (two groups too close to tell), but a kernel ends with
-// its slowest wave: the same steps as for 32-bit keys, on integers.
 template <int VPL>
 __device__ int choose_exactly(const RouterArgs& a, const float (&x)[VPL], float m,
                               uint64_t* wkeys) {
   const int lane = threadIdx.x & 63;
-  const double total = exact_total<VPL>(a, x, m);
   uint64_t key[VPL];
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    key[i] = 0;
-    if (x[i] > -INFINITY) {
-      const double f = exact_key(a, x[i], m, total,
-                                 a.bias != nullptr ? a.bias[lane * VPL + i] : 0.0f);
-      if (f > -INFINITY) key[i] = ordered_bits64(f);           // NaN masks
-    }
-  }
-  if (a.groups > 1) {
-    const int size = a.group_size;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane * VPL + i < a.E) wkeys[lane * VPL + i] = key[i];
-    wave_lds_order();
-    uint64_t best = 0, second = 0;          // lane g: of group g
-    if (lane < a.groups) {
-#pragma unroll 8
-      for (int j = 0; j < size; ++j) {
-        const uint64_t v = wkeys[lane * size + j];
-        second = max(second, min(best, v));
-        best = max(best, v);
-      }
-      if (a.group_top > 1 && second != 0)
-        best = ordered_bits64(from_ordered64(best) + from_ordered64(second));
-    }
-    int better = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const uint64_t o = read_lane(best, g);
-      better += (o > best || (o == best && g < lane)) ? 1 : 0;
-    }
-    const uint64_t kept = __ballot(lane < a.groups && better < a.topk_groups);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (!((kept >> ((lane * VPL + i) / size & 63)) & 1)) key[i] = 0;
-  }
+  exact_keys<VPL>(a, x, m, key);
+  if (a.groups > 1) drop_groups<VPL>(a, keep_exactly<VPL>(a, key, wkeys), key);
   int my_id = -1;
   for (int j = 0; j < a.k; ++j) {
     uint64_t b = key[0];
@@ -367,14 +405,10 @@ struct LaneKeys {
   }
 };
 
+// One token, by a whole wave; wkeys: LDS of E 64-bit keys, with groups.
 template <int DT, int VPL>
-__global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(const RouterArgs a) {
-  extern __shared__ uint64_t lds[];
+__device__ __forceinline__ void route_token(const RouterArgs& a, int64_t t, uint64_t* wkeys) {
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = (int64_t)block_index() * kRouterWaves + wave;
-  if (t >= a.T) return;
-  uint64_t* wkeys = lds + (int64_t)wave * a.E;
   const int E = a.E, k = a.k, e0 = lane * VPL;
   const bool pad = a.is_padding != nullptr && a.is_padding[t] != 0;
   if (pad) {
@@ -385,7 +419,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(const Ro
     return;
   }
   float x[VPL];
-  load_logits<DT, VPL>(a.logits, t, E, e0, x);
+  load_logits<DT, VPL, true>(a.logits, t, E, e0, x);
   const bool scored = a.bias != nullptr || a.group_top > 1;
   float m = 0.0f, total = 1.0f;             // of the softmax over all experts
   const bool over_all = !a.sigmoid && (scored || !a.renormalize);
@@ -423,8 +457,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(const Ro
 #pragma unroll
   for (int i = 0; i < VPL; ++i)           // a bias of NaN or -inf masks its expert too
     key[i] = x[i] > -INFINITY && f[i] > -INFINITY ? ordered_bits(f[i]) : 0u;
-  bool near_groups = false;
-  if (a.groups > 1) near_groups = keep_groups<VPL>(a, key, (uint32_t*)wkeys, near);
+  if (a.groups > 1) keep_groups<VPL>(a, key, x, m, wkeys, near);
   // lane j keeps the j-th largest key and its expert
   int my_id = -1;
   uint32_t my_key = 0;
@@ -456,10 +489,10 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(const Ro
     const float prev_x = __shfl_up(my_x, 1), prev_bias = __shfl_up(bias, 1);
     const bool unclear = lane > 0 && my_id >= 0 && near_keys(prev, my_key, near) &&
                          !(prev_x == my_x && prev_bias == bias);
-    if (near_groups || __ballot(unclear) != 0) {
+    if (__ballot(unclear) != 0) {
       // (a lane is left for every expert that may be among the chosen unless
       // 64 keys in a row are close)
-      if (near_groups || n == 64) my_id = choose_exactly<VPL>(a, x, m, wkeys);
+      if (n == 64) my_id = choose_exactly<VPL>(a, x, m, wkeys);
       else my_id = rank_exactly<VPL>(a, x, m, my_x, bias, my_id, n);
       my_x = -INFINITY;
       if (my_id >= 0) my_x = clean_logit(RowVec<DT>::load_one(logits, t * E + my_id));
@@ -488,6 +521,226 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(const Ro
   }
 }
 
+template <int DT, int VPL>
+__global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(const RouterArgs a) {
+  extern __shared__ uint64_t lds[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = (int64_t)block_index() * kRouterWaves + wave;
+  if (t >= a.T) return;
+  route_token<DT, VPL>(a, t, lds + (int64_t)wave * a.E);
+}
+
+// Reductions over the 16 lanes of a row, the same in every lane.
+template <int CTRL>
+__device__ __forceinline__ uint32_t rotated(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = max(v, rotated<0x128>(v));         // row_ror:8, 4, 2, 1
+  v = max(v, rotated<0x124>(v));
+  v = max(v, rotated<0x122>(v));
+  return max(v, rotated<0x121>(v));
+}
+__device__ __forceinline__ float row_max(float v) {
+  return from_ordered(row_max(ordered_bits(v)));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += __uint_as_float(rotated<0x128>(__float_as_uint(v)));
+  v += __uint_as_float(rotated<0x124>(__float_as_uint(v)));
+  v += __uint_as_float(rotated<0x122>(__float_as_uint(v)));
+  return v + __uint_as_float(rotated<0x121>(__float_as_uint(v)));
+}
+
+// N keys in descending order: odd-even merges
+template <int N>
+__device__ __forceinline__ void sort_descending(uint32_t (&key)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2) {
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2) {
+#pragma unroll
+      for (int i = 0; i + q < N; ++i) {
+        const int first = q % p;
+        if (i < first || ((i - first) / q) % 2 != 0 || i / (2 * p) != (i + q) / (2 * p)) continue;
+        const uint32_t hi = max(key[i], key[i + q]);
+        key[i + q] = min(key[i], key[i + q]);
+        key[i] = hi;
+      }
+    }
+  }
+}
+
+// Four tokens per wave, a row of 16 lanes each, for batches that fill the
+// chip: what a wave spends beside the experts' scores it spends once for
+// four.  Lane l of a row holds the VPL experts from l * VPL, their ordered
+// keys with the place in the lane in the low bits, sorted once: a round takes
+// the row's largest head, whose lane shifts its keys up.  What the low bits
+// carried, or two keys' errors, leave open sends a token to the whole wave, as
+// a router_topk_kernel wave takes it.  Keys that are 2-byte logits are exact
+// in the bits above.
+constexpr float kNearPlaces = 0x1p-17f;  // 16 steps of a group's two keys and of their sum
+
+template <int DT, int VPL, int WAVE_VPL>
+__global__ __launch_bounds__(64 * kRouterWaves) void router_rows_kernel(const RouterArgs a) {
+  extern __shared__ uint64_t lds[];
+  __shared__ uint2 taken[kRouterWaves][4][16];
+  const int lane = threadIdx.x & 63, row = lane >> 4, l = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t0 = ((int64_t)block_index() * kRouterWaves + wave) * 4;
+  if (t0 >= a.T) return;
+  const int64_t t = t0 + row;
+  const int E = a.E, k = a.k, e0 = l * VPL;
+  const int64_t at = t < a.T ? t : a.T - 1;
+  const bool live = t < a.T && (a.is_padding == nullptr || a.is_padding[at] == 0);
+  float x[VPL];
+  load_logits<DT, VPL, false>(a.logits, at, E, e0, x);   // a row's vectors share lines
+  const bool scored = a.bias != nullptr || a.group_top > 1;
+  const bool exact = !scored && DT != kF32;
+  float m = 0.0f, total = 1.0f;             // of the softmax over all experts
+  if (!a.sigmoid && (scored || !a.renormalize)) {
+    m = x[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, x[i]);
+    m = row_max(m);
+    total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) total += x[i] > -INFINITY ? expf(x[i] - m) : 0.0f;
+    total = row_sum(total);
+  }
+  const float near = !scored ? 0.0f : a.sigmoid ? kNearSigmoid : kNearSoftmax / total;
+  uint32_t key[VPL];
+  if (scored) {
+    float f[VPL];
+    if (a.bias == nullptr) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) f[i] = 0.0f;
+    } else if (E % VPL == 0) {
+      const int first = min(e0, E - VPL);
+#pragma unroll
+      for (int i = 0; i < VPL; i += 4)
+        RowVec<kF32>::unpack(RowVec<kF32>::template load_at<false>((const uint8_t*)a.bias, first + i),
+                             f + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) f[i] = a.bias[min(e0 + i, E - 1)];
+    }
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) f[i] += __builtin_amdgcn_rcpf(1.0f + __expf(-x[i]));
+    } else {
+      const float inv_total = 1.0f / total;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) f[i] = fmaf(expf(x[i] - m), inv_total, f[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      key[i] = x[i] > -INFINITY && f[i] > -INFINITY ? ordered_bits(f[i]) : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = x[i] > -INFINITY ? ordered_bits(x[i]) : 0u;
+  }
+  constexpr uint32_t PLACE = VPL - 1;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)             // equal keys: the lower place is the larger
+    key[i] = live && key[i] != 0u ? (key[i] & ~PLACE) | (PLACE - i) : 0u;
+  sort_descending<VPL>(key);
+  bool unclear = false;
+  if (a.groups > 1) {                       // of 1, 2, 4, 8 or 16 whole lanes
+    const int lanes = 1 << a.row_lanes_log;
+    uint32_t b = key[0] & ~PLACE, s = key[1] & ~PLACE;
+    if (lanes > 1) merge_lanes<0xB1>(b, s);       // quad_perm [1,0,3,2]
+    if (lanes > 2) merge_lanes<0x4E>(b, s);       // quad_perm [2,3,0,1]
+    if (lanes > 4) merge_lanes<0x141>(b, s);      // row_half_mirror
+    if (lanes > 8) merge_lanes<0x140>(b, s);      // row_mirror
+    const int group = l >> a.row_lanes_log;
+    // the group in the low bits: values differ, and the lower group's is larger
+    const uint32_t v = group < a.groups
+                           ? (group_value(b, s, a.group_top) & ~15u) | (uint32_t)(15 - group) : 0u;
+    int better = 0;                         // lanes of better groups
+#define MOE_STEP(d) \
+  if ((d & (lanes - 1)) == 0) better += rotated<0x120 + d>(v) > v ? 1 : 0
+    MOE_STEP(1); MOE_STEP(2); MOE_STEP(3); MOE_STEP(4); MOE_STEP(5);
+    MOE_STEP(6); MOE_STEP(7); MOE_STEP(8); MOE_STEP(9); MOE_STEP(10);
+    MOE_STEP(11); MOE_STEP(12); MOE_STEP(13); MOE_STEP(14); MOE_STEP(15);
+#undef MOE_STEP
+    const bool keep = better < a.topk_groups && group < a.groups;
+    if (!exact) {
+      const bool some = v > 15u;
+      const float fv = from_ordered(v);
+      float mag = fabsf(from_ordered(b));
+      if (a.group_top > 1 && s != 0u) mag += fabsf(from_ordered(s));
+      const float err = fminf(fmaf(kNearPlaces, mag, near), FLT_MAX);
+      const uint32_t dropped = row_max(keep || !some ? 0u : ordered_bits(fv + err));
+      const uint32_t kept = ~row_max(keep && some ? ~ordered_bits(fv - err) : 0u);
+      unclear = kept <= dropped;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = keep ? key[i] : 0u;
+  }
+  // k rounds, and one for the best key that is left
+  const int rounds = min(k + 1, 16);
+  const uint32_t below = ((1u << l) - 1u) << (row & 1) * 16;
+  for (int j = 0; j < rounds; ++j) {
+    const uint32_t head = key[0] & ~PLACE;
+    const uint64_t best = __ballot(head == row_max(head));
+    const uint32_t half = row < 2 ? (uint32_t)best : (uint32_t)(best >> 32);
+    if (((half >> (lane & 31)) & 1u) != 0u && (half & below) == 0u) {   // the lowest lane
+      taken[wave][row][j] = make_uint2(key[0], (uint32_t)e0);
+#pragma unroll
+      for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
+      key[VPL - 1] = 0u;
+    }
+  }
+  wave_lds_order();
+  const uint2 mine = taken[wave][row][min(l, rounds - 1)];
+  uint32_t my_key = l < rounds ? mine.x : 0u;
+  int my_id = my_key != 0u ? (int)(mine.y + (PLACE - (my_key & PLACE))) : -1;
+  my_key &= ~PLACE;
+  float my_x = -INFINITY;
+  if (my_id >= 0) my_x = clean_logit(RowVec<DT>::load_one((const uint8_t*)a.logits, at * E + my_id));
+  if (!exact) {
+    // The chosen in order by their whole keys, unless equal logits and biases
+    // say why not; then the last of them against all that is left, which is
+    // no larger than the best place of the next key.
+    const float bias = a.bias != nullptr && my_id >= 0 ? a.bias[my_id] : 0.0f;
+    float f = my_x;
+    if (scored)
+      f = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-my_x)) + bias
+                    : fmaf(expf(my_x - m), 1.0f / total, bias);
+    const float prev = __uint_as_float(rotated<0x111>(__float_as_uint(f)));    // row_shr:1
+    const float prev_x = __uint_as_float(rotated<0x111>(__float_as_uint(my_x)));
+    const float prev_bias = __uint_as_float(rotated<0x111>(__float_as_uint(bias)));
+    const bool close = l > 0 && my_id >= 0 &&
+                       prev - (l == k ? from_ordered(my_key | PLACE) : f) <=
+                           (scored ? fmaf(kNearRound, fabsf(prev), near) : 0.0f);
+    unclear |= close && (l == k || !(prev_x == my_x && prev_bias == bias));
+  }
+  if (l >= k) {
+    my_id = -1;
+    my_x = -INFINITY;
+  }
+  float w = 0.0f;
+  if (a.sigmoid) {
+    w = my_id >= 0 ? sigmoid_f32(my_x) : 0.0f;
+    if (a.renormalize) w /= row_sum(w) + 1e-20f;
+  } else if (a.renormalize) {
+    const float ms = row_max(my_x);
+    w = my_id >= 0 ? expf(my_x - ms) : 0.0f;
+    const float sum = row_sum(w);
+    w = my_id >= 0 ? w / sum : 0.0f;
+  } else {
+    w = my_id >= 0 ? expf(my_x - m) / total : 0.0f;
+  }
+  const uint64_t open = __ballot(unclear);
+  if (l < k && t < a.T && ((open >> (row * 16)) & 0xFFFFu) == 0) {
+    a.ids[t * k + l] = my_id;
+    a.weights[t * k + l] = w * a.scale;
+  }
+  for (int r = 0; r < 4; ++r)
+    if (((open >> (r * 16)) & 0xFFFFu) != 0)
+      route_token<DT, WAVE_VPL>(a, t0 + r, lds + (int64_t)wave * E);
+}
+
 // One wave per token.  With p the score of the chosen experts and g their
 // weights' gradients: softmax over all experts dx_i = s_i c (g_i - sum g p);
 // renormalized softmax the same over the chosen alone; sigmoid dx_j = c g_j
@@ -508,7 +761,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_grad_kernel(
   float out[VPL], xs[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) out[i] = 0.0f;
-  if (dense) load_logits<DT, VPL>(a.logits, t, E, e0, xs);
+  if (dense) load_logits<DT, VPL, true>(a.logits, t, E, e0, xs);
   int id = lane < k ? ids[t * k + lane] : -1;
   if (id < 0 || id >= E) id = -1;
   // the chosen experts' gradients: of their logits, or, for a softmax over all
@@ -595,16 +848,40 @@ hipError_t per_lane(int E, F&& go) {
   return go(std::integral_constant<int, 16>());
 }
 
+// the log of the lanes of vpl experts that hold a group, -1 when they are not
+// 2^0..2^4 whole lanes
+int group_lanes(int group_size, int vpl) {
+  for (int l = 0; l <= 4; ++l)
+    if (group_size == vpl << l) return l;
+  return -1;
+}
+
+// Tokens from which a wave takes four.  Where keys have errors, some token of
+// nearly every large batch goes to a whole wave after that, and the kernel
+// ends with the last.  Measured one / four per wave, 128 experts, top 8, bf16
+// softmax: 2048 tokens 4.0 / 3.9 us, 4096 4.5 / 3.9, 16384 10.0 / 5.9, 65536
+// 32 / 17; 256 experts, top 8 of 4 of 8 groups, fp32 sigmoid with a bias: 4096
+// 8.7 / 11.3, 8192 10.4 / 11.0, 16384 17.9 / 15.0, 65536 60 / 38.
+constexpr int kRowsTokens = 4096, kRowsTokensScored = 10240;
+
 template <int DT>
 hipError_t topk_dt(RouterArgs a, hipStream_t stream) {
-  const dim3 grid = grid_of((a.T + kRouterWaves - 1) / kRouterWaves);
   const size_t lds = a.groups > 1 ? (size_t)kRouterWaves * a.E * sizeof(uint64_t) : 0;
+  a.group_size = a.E / a.groups;
+  const bool scored = a.bias != nullptr || a.group_top > 1;
   return per_lane(a.E, [&](auto vpl) {
     constexpr int VPL = decltype(vpl)::value;
-    a.group_size = a.E / a.groups;
-    a.group_lanes_log = -1;
-    for (int l = 0; l <= 4; ++l)
-      if (a.group_size == VPL << l) a.group_lanes_log = l;
+    a.group_lanes_log = group_lanes(a.group_size, VPL);
+    if constexpr (VPL <= 4) {
+      constexpr int RVPL = 4 * VPL;         // experts per lane of a row
+      a.row_lanes_log = group_lanes(a.group_size, RVPL);
+      if (a.T >= (scored ? kRowsTokensScored : kRowsTokens) && a.E > 16 && a.k < 16 && (a.groups == 1 || a.row_lanes_log >= 0)) {
+        const dim3 grid = grid_of((a.T + 4 * kRouterWaves - 1) / (4 * kRouterWaves));
+        router_rows_kernel<DT, RVPL, VPL><<<grid, 64 * kRouterWaves, lds, stream>>>(a);
+        return hipGetLastError();
+      }
+    }
+    const dim3 grid = grid_of((a.T + kRouterWaves - 1) / kRouterWaves);
     router_topk_kernel<DT, VPL><<<grid, 64 * kRouterWaves, lds, stream>>>(a);
     return hipGetLastError();
   });

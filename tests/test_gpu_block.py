@@ -94,10 +94,18 @@ def run_router(x, k, bias=None, pad=None, grad_w=None, dtype=None, **kw):
     return ids, w, gx
 
 
-def check_router(x, k, bias=None, pad=None, seed=0, **kw):
+def check_router(x, k, bias=None, pad=None, seed=0, tokens=None, **kw):
+    """tokens: a batch of that many, the rows of x over and over; every copy of
+    a row has to give the same bits."""
     rng = np.random.default_rng(seed + 1000)
-    gw = torch.from_numpy(rng.normal(size=(x.shape[0], k)).astype(np.float32))
-    ids, w, gx = run_router(x, k, bias, pad, gw, **kw)
+    n = x.shape[0]
+    gw = torch.from_numpy(rng.normal(size=(n, k)).astype(np.float32))
+    at = torch.arange(tokens or n) % n
+    ids, w, gx = run_router(x[at], k, bias, None if pad is None else pad[at], gw[at], **kw)
+    if tokens:
+        for t in (ids, w, gx):
+            assert torch.equal(t, t[at.cuda()])
+        ids, w, gx = ids[:n], w[:n], gx[:n]
     bn, pn = None if bias is None else bias.numpy(), None if pad is None else pad.numpy()
     want_ids, want_w = B.router_topk(f64(x), k, bias=bn, pad=pn, **kw)
     assert np.array_equal(ids.cpu().numpy(), want_ids)
@@ -171,6 +179,60 @@ def test_router_masks_and_special_values(gpu, score, renormalize, grouped):
     if grouped:
         kw.update(groups=4, topk_groups=2, group_top=2)
     check_router(x, 6, bias if grouped else None, pad, **kw)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("E,k,kw", [
+    (256, 8, dict(score="sigmoid", bias=True, scale=2.5, **GROUPED)),
+    (128, 8, dict(score="softmax", renormalize=False)),
+    (60, 4, dict(score="softmax", bias=True)),
+    (160, 6, dict(score="softmax", renormalize=False, groups=10, topk_groups=3, scale=16.0)),
+    (17, 15, dict(score="sigmoid")), (100, 15, dict(score="sigmoid", renormalize=False)),
+    (64, 5, dict(score="softmax", groups=16, topk_groups=5, group_top=2)),
+    (128, 1, dict(score="softmax", bias=True, groups=2, topk_groups=1)),
+    (256, 9, dict(score="softmax", bias=True, groups=4, topk_groups=2, group_top=2)),
+    (250, 3, dict(score="sigmoid", bias=True)), (24, 16, dict(score="sigmoid")),
+    (256, 4, dict(score="sigmoid", groups=32, topk_groups=9))])
+def test_router_many_tokens(gpu, E, k, kw, dtype):
+    """Batches that share a wave among four tokens, with a last wave of three."""
+    kw = dict(kw)
+    rng = np.random.default_rng(E + k)
+    T = 701
+    bias = torch.from_numpy(rng.normal(0, 0.1, E).astype(np.float32)) if kw.pop("bias", False) \
+        else None
+    x = rand(rng, (T, E), dtype, 2.0)
+    x[rng.random(T) < 0.05, 2::3] = -np.inf
+    x[rng.random((T, E)) < 1e-3] = np.nan
+    x[rng.random((T, E)) < 1e-3] = np.inf
+    pad = torch.from_numpy((rng.random(T) < 0.1).astype(np.uint8))
+    check_router(x, k, bias, pad, E, tokens=20003, **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,group_top", [(1, 1), (8, 1), (8, 2)])
+def test_router_many_tokens_hard_to_tell(gpu, score, groups, group_top):
+    """The same, with equal keys, keys few steps of fp32 apart, group values
+    that cancel, masked rows: tokens that need the choice of 64 bits lie beside
+    others in a wave."""
+    rng = np.random.default_rng(18)
+    T, E, many = 701, 128, 20002
+    x = rand(rng, (T, E), torch.float32, 1.0)
+    x[0::7] = torch.round(x[0::7])
+    x[1::7] *= 2.0 ** -20
+    x[2::7, 64:] = x[2::7, :64]
+    x[3::7, 5:] = -np.inf
+    x[4::35] = -np.inf
+    x[5::35] = torch.finfo(torch.float32).min
+    kw = dict(score=score, groups=groups, topk_groups=max(1, groups // 2), group_top=group_top)
+    check_router(x, 8, None, None, tokens=many, **kw)
+    check_router(x, 8, torch.zeros(E), None, tokens=many, **kw)
+    check_router(x, 8, rand(rng, (E,), torch.float32, 2.0 ** -10), None, tokens=many, **kw)
+    bias = torch.full((E,), -2000.0)
+    bias[::16], bias[15::16] = 1000.0, -1000.0
+    bias[40:44] = torch.tensor([np.inf, -np.inf, np.nan, 1e30])
+    with np.errstate(invalid="ignore"):
+        check_router(x, 8, bias, None, tokens=many, **kw)
+    check_router(x.bfloat16(), 8, None, None, tokens=many, **kw)
 
 
 def test_router_ties_go_to_the_lower_index(gpu):
