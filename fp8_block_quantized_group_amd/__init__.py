@@ -507,10 +507,11 @@ class BlockNorm(_Descriptor):
                           int(self.gate_sigmoid), self.eps, self.residual_scale,
                           self.weight_offset)
 
-    @property
-    def gate_shape(self):
-        return {"none": None, "token": (self.num_tokens,), "channel": (self.hidden,),
-                "full": (self.num_tokens, self.hidden)}[self.gate]
+    def __post_init__(self):
+        super().__post_init__()
+        T, H = self.num_tokens, self.hidden
+        shape = {"none": (), "token": (T,), "channel": (H,), "full": (T, H)}[self.gate]
+        object.__setattr__(self, "gate_shape", shape)
 
 
 def _arg(t, name: str, dtype, shape, device):
@@ -670,7 +671,7 @@ def _block_args(p: BlockNorm, y, post_weight, gate, pre_weight, d):
     H = p.hidden
     return (_arg(y, "y", p.dtype, (p.num_tokens, H), d),
             _arg(post_weight, "post_weight", wt, (H,), d),
-            _arg(gate, "gate", p.dtype, p.gate_shape or (), d),
+            _arg(gate, "gate", p.dtype, p.gate_shape, d),
             _arg(pre_weight, "pre_weight", wt, (H,), d))
 
 
@@ -710,7 +711,7 @@ def block_norm_backward(p: BlockNorm, residual_out, grad_normed, grad_residual, 
          _arg(grad_pre_weight, "grad_pre_weight", torch.float32, (H,), d),
          _arg(grad_post_weight, "grad_post_weight", torch.float32, (H,), d),
          _arg(grad_gate, "grad_gate", p.dtype if p.gate == "full" else torch.float32,
-              p.gate_shape or (), d), wp, wn)
+              p.gate_shape, d), wp, wn)
 
 
 class MoeBlock:
