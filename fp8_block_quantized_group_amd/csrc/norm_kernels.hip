@@ -706,9 +706,13 @@ struct Shape {
   static constexpr int BT = B, VPT = V;       // lanes per row, vectors per lane
 };
 
-// Up to this many rows (two per CU) a row gets more lanes: the call's time is
-// one row's.  Measured with / without, bf16: 32 x 7168 4.6 / 5.9 us, 256 x
-// 2048 3.5 / 5.8, 512 x 7168 7.1 / 7.5, 600 x 7168 8.7 / 8.4.
+// With many rows the lanes fit the row, two vectors each where a block is
+// small enough (8192 rows, bf16: 5120 columns 59 us with 320 lanes x 2, 79 with
+// 256 x 4; 7168 82 with 448 x 2, 90; 4096 rows of 12288: 77 with 512 x 3, 87
+// with 512 x 4, 92 with 768 x 2).  Up to this many rows (two per CU) a row gets
+// more lanes: the call's time is one row's.  Measured with / without, bf16: 32
+// x 7168 4.6 / 5.9 us, 256 x 2048 3.5 / 5.8, 512 x 7168 7.1 / 7.5, 600 x 7168
+// 8.7 / 8.4.
 constexpr int kFewRows = 512;
 
 template <int DT, bool W32>
@@ -730,9 +734,15 @@ hipError_t norm_dt(const NormArgs& a, hipStream_t stream) {
     if (nv <= 1024) return go(Shape<RowVec<DT>, 512, 2>());
     if (nv <= 2048) return go(Shape<RowVec<DT>, 1024, 2>());
   }
+  if (nv <= 192) return go(Shape<RowVec<DT>, 64, 3>());
   if (nv <= 256) return go(Shape<RowVec<DT>, 64, 4>());
+  if (nv <= 384) return go(Shape<RowVec<DT>, 192, 2>());
   if (nv <= 512) return go(Shape<RowVec<DT>, 256, 2>());
-  if (nv <= 1024) return go(Shape<RowVec<DT>, 256, 4>());
+  if (nv <= 640) return go(Shape<RowVec<DT>, 320, 2>());
+  if (nv <= 768) return go(Shape<RowVec<DT>, 384, 2>());
+  if (nv <= 896) return go(Shape<RowVec<DT>, 448, 2>());
+  if (nv <= 1024) return go(Shape<RowVec<DT>, 512, 2>());
+  if (nv <= 1536) return go(Shape<RowVec<DT>, 512, 3>());
   if (nv <= 2048) return go(Shape<RowVec<DT>, 512, 4>());
   if (nv <= 4096) return go(Shape<RowVec<DT>, 1024, 4>());
   if constexpr (DT == kF32) return go(Shape<RowVec<DT>, 1024, 8>());

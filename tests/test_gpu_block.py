@@ -716,6 +716,15 @@ def test_block_norm_many_rows(gpu, T, H, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("H", [1300, 2600, 4700, 6000, 7000, 8001])
+def test_block_norm_many_rows_of_every_shape(gpu, H, dtype):
+    rng = np.random.default_rng(H)
+    gate = "channel" if H % 8 else "token"
+    p = moe.BlockNorm(515, H, dtype=dtype, weight_dtype=torch.float32, post_norm=True, gate=gate)
+    check_norm(p, make_norm(rng, 515, H, dtype, torch.float32, gate))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("H", [7, 264, 5000])
 def test_norm_without_a_block(gpu, H, dtype):
     rng = np.random.default_rng(H)
