@@ -15,7 +15,7 @@
 // the caches: 204 us against 188 for the combine below); a permuted token was
 // just written by the kernel before and is read through the caches (108 us
 // with non-temporal loads, 91 without).  MI355X, where a 2 GiB copy moves
-// 5.1 TB/s: permute 4096 x 8 rows of 7168 bf16 columns 89 us (505 MB, 5.7
+// 5.1 TB/s: permute 4096 x 8 rows of 7168 bf16 columns 84 us (528 MB, 6.3
 // TB/s), combine 16384 x 8 x 4096 bf16 188 us (1.15 GB, 6.1 TB/s), its
 // gradients 417 us (2.17 GB, 5.2 TB/s).
 #include <type_traits>
