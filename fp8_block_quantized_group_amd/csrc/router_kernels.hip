@@ -299,7 +299,7 @@ __device__ __forceinline__ void keep_groups(const RouterArgs& a, uint32_t (&key)
 }
 
 // The n candidates, one per lane, ordered by their 64-bit keys.  Every
-// expert outside is clearly below the first k.
+// expert outside is clearly below the last of them.
 template <int VPL>
 __device__ int rank_exactly(const RouterArgs& a, const float (&x)[VPL], float m, float my_x,
                             float bias, int my_id, int n) {
@@ -324,7 +324,10 @@ __device__ int choose_exactly(const RouterArgs& a, const float (&x)[VPL], float 
   const int lane = threadIdx.x & 63;
   uint64_t key[VPL];
   exact_keys<VPL>(a, x, m, key);
-  if (a.groups > 1) drop_groups<VPL>(a, keep_exactly<VPL>(a, key, wkeys), key);
+  if (a.groups > 1) {
+    wave_lds_order();                     // the 32-bit keys there have been read
+    drop_groups<VPL>(a, keep_exactly<VPL>(a, key, wkeys), key);
+  }
   int my_id = -1;
   for (int j = 0; j < a.k; ++j) {
     uint64_t b = key[0];
@@ -479,6 +482,12 @@ __device__ __forceinline__ void route_token(const RouterArgs& a, int64_t t, uint
     last = b;
     ++n;
   }
+  // all lanes are taken: what is left may still belong before the last of them
+  bool more = false;
+  if (scored && n == 64) {
+    const uint32_t b = wave_max(mine.head());
+    more = b != 0u && near_keys(last, b, near);
+  }
   const uint8_t* logits = (const uint8_t*)a.logits;
   float my_x = -INFINITY;
   if (my_id >= 0) my_x = clean_logit(RowVec<DT>::load_one(logits, t * E + my_id));
@@ -489,10 +498,10 @@ __device__ __forceinline__ void route_token(const RouterArgs& a, int64_t t, uint
     const float prev_x = __shfl_up(my_x, 1), prev_bias = __shfl_up(bias, 1);
     const bool unclear = lane > 0 && my_id >= 0 && near_keys(prev, my_key, near) &&
                          !(prev_x == my_x && prev_bias == bias);
-    if (__ballot(unclear) != 0) {
-      // (a lane is left for every expert that may be among the chosen unless
-      // 64 keys in a row are close)
-      if (n == 64) my_id = choose_exactly<VPL>(a, x, m, wkeys);
+    if (more || __ballot(unclear) != 0) {
+      // (where no key that is left is near the last one, every expert that may
+      // be among the chosen has a lane)
+      if (more) my_id = choose_exactly<VPL>(a, x, m, wkeys);
       else my_id = rank_exactly<VPL>(a, x, m, my_x, bias, my_id, n);
       my_x = -INFINITY;
       if (my_id >= 0) my_x = clean_logit(RowVec<DT>::load_one(logits, t * E + my_id));

@@ -287,6 +287,44 @@ def test_router_group_values_that_cancel(gpu, score, size):
     check_router(x, 4, bias, None, score=score, groups=8, topk_groups=4, group_top=2)
 
 
+@pytest.mark.parametrize("tokens", [None, 12001])
+@pytest.mark.parametrize("groups,group_top", [(1, 1), (1, 2), (4, 1), (4, 2)])
+@pytest.mark.parametrize("E", [128, 256, 1024])
+def test_router_more_equal_keys_than_lanes(gpu, E, groups, group_top, tokens):
+    """More experts with one and the same key of 32 bits than a wave has lanes:
+    the largest in 64 bits is chosen, wherever it stands."""
+    at = (E - 1, E // 2 + 40, 3 * E // 4)
+    kw = dict(groups=groups, topk_groups=max(1, groups - 1), group_top=group_top)
+    # 1 / (1 + e^-30) and e^-31 are both 1 in fp32, 6e-14 apart
+    x = torch.full((4, E), 30.0)
+    x[torch.arange(3), torch.tensor(at)] = 31.0
+    check_router(x, 8, torch.zeros(E), None, tokens=tokens, score="sigmoid", **kw)
+    # a bias of 2^20 has steps of 1 / 8, the scores differ by 1 / E at most
+    x = torch.zeros((4, E))
+    x[torch.arange(3), torch.tensor(at)] = 1.0
+    x[0, 5], x[1, 64:] = 0.5, -1.0
+    bias = torch.full((E,), 2.0 ** 20)
+    check_router(x, 8, bias, None, tokens=tokens, score="softmax", **kw)
+    check_router(x.bfloat16(), 3, bias, None, tokens=tokens, score="sigmoid", **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [128, 300])
+def test_router_last_of_64_places(gpu, E, score):
+    """The last of 64 places goes to the larger of two experts that only 64
+    bits tell apart; with one place less, to the lower of two equal ones."""
+    x = torch.zeros((3, E))
+    bias = torch.full((E,), -10.0)
+    bias[:63] = 5000.0 - 10.0 * torch.arange(63)
+    bias[100] = bias[E - 3] = 1024.0             # steps of 2^-13
+    x[0, 100], x[0, E - 3] = 30.0, 31.0
+    x[1, 100], x[1, E - 3] = 2.0 ** -20, 2.0 ** -19
+    if score == "softmax":
+        x *= 2.0 ** -8
+    check_router(x, 64, bias, None, score=score)
+    check_router(x, 63, bias, None, score=score)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups", [1, 4])
 def test_router_special_biases(gpu, score, groups):
