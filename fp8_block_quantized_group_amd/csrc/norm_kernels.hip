@@ -113,6 +113,18 @@ __device__ __forceinline__ float gate_value(float g, bool sigmoid) {
   return sigmoid ? 1.0f / (1.0f + expf(-g)) : g;
 }
 
+// What the gate's value g enters as, and its derivative by g.  1 - s taken from
+// a rounded s would cancel (the slope off by 5e-4 of itself at a gate of 10, 0
+// from 17 on); with e = exp(-|g|) both come from 1 / (1 + e).
+struct GateGrad {
+  float value, slope;
+};
+__device__ __forceinline__ GateGrad gate_grad(float g, bool sigmoid) {
+  if (!sigmoid) return GateGrad{g, 1.0f};
+  const float e = expf(-fabsf(g)), r = 1.0f / (1.0f + e);
+  return GateGrad{g >= 0.0f ? r : e * r, e * r * r};
+}
+
 // the row's inverse root mean square, its N * VPT values per lane given by f
 template <int BT, int VPT, int N, class F>
 __device__ __forceinline__ float row_inv_rms(F&& value, int H, float eps, float (*buf)[1][16]) {
@@ -235,7 +247,8 @@ __global__ __launch_bounds__(BT == 64 ? 256 : BT) void norm_kernel(const NormArg
 //   D  = dr'_in + xs (dh w_pre - xh mean(dh w_pre xh))       -> grad r
 //   dn = alpha gate D,  e = dn w_post
 //   dy = ys (e - yh mean(e yh))
-//   grad w_pre += dh xh,  grad w_post += dn yh,  grad gate += alpha D n gate'
+//   grad w_pre += dh xh,  grad w_post += dn yh,  grad gate += alpha D n, times
+//   the slope of a sigmoid
 // Each block walks rows with a stride of the grid and keeps the column sums
 // of its rows; they go to part[output][block][H] and are added up in block
 // order by grad_sum_kernel, so the result does not depend on timing.
@@ -247,7 +260,9 @@ struct GradRow {
 };
 
 // D, e and the addends of the column sums of one column vector, from its
-// weights (o + w, or 1) and its gate as it enters the product
+// weights (o + w, or 1) and its gate as it enters the product.  dg is the
+// gradient of that value; the sigmoid's slope multiplies it once per gate, after
+// the sum where columns or rows share one.
 template <int N, bool HAS_Y>
 __device__ __forceinline__ void grad_columns(const NormGradArgs& a, const GradRow& r,
                                              const float (&x)[N], const float (&dh)[N],
@@ -262,11 +277,13 @@ __device__ __forceinline__ void grad_columns(const NormGradArgs& a, const GradRo
     D[c] = fmaf(r.xs, fmaf(dh[c], wpre[c], -xh * r.xm), D[c]);
   }
   if (!HAS_Y) return;
+  // Each product once, as a value: fused into the two sums that dg goes to, its
+  // factors stay live, and the fullest shapes spill up to 17 registers.
 #pragma unroll
   for (int c = 0; c < N; ++c) {
+#pragma clang fp contract(off)
     const float yh = y[c] * r.ys, ad = a.alpha * D[c], adg = ad * g[c];
     dg[c] = ad * (yh * wpost[c]);
-    if (a.gate_sigmoid) dg[c] *= g[c] * (1.0f - g[c]);
     dpost[c] = adg * yh;
     e[c] = adg * wpost[c];
   }
@@ -280,12 +297,6 @@ __device__ __forceinline__ GradRow grad_row(const NormGradArgs& a, const float (
   r.xm = r.xs / fx * (s[1] / (float)a.H);
   r.ys = a.post ? inv_rms(s[2], a.H, a.eps, fy) : 1.0f;
   return r;
-}
-
-template <class RV>
-__device__ __forceinline__ float token_gate(const NormGradArgs& a, int64_t row) {
-  return a.y != nullptr && a.gate_kind == kGateToken
-             ? gate_value(RV::load_one(a.gate, row), a.gate_sigmoid) : 1.0f;
 }
 
 // Rows in registers: BT lanes per row, kGradThreads / BT rows side by side
@@ -362,6 +373,7 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
   constexpr int SUMS = FORM == kNoBlock ? 1 : FULL ? 2 : 3;   // column sums: pre, post, gate
   __shared__ float buf1[2][G][3][16], buf2[2][G][2][16], buf3[2][G][3][16];
   __shared__ float sums[G][BT * N];
+  __shared__ float slope_of[G];               // a token gate's, kept for the lane that writes it
   __shared__ __align__(16) float wlds[SUMS][N / P][NV][P];   // pre, post, gate
   const int sub = threadIdx.x / BT, first = threadIdx.x % BT;
   const int64_t stride = (int64_t)gridDim.x * G;
@@ -460,14 +472,18 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
       row_sums<BT, 3>(s, buf3[turn][sub]);
     }
     const GradRow r = grad_row(a, s, fx, fy);
-    const float gt = FORM == kBlock && a.gate_kind == kGateToken
-                         ? gate_value(cur.gt, a.gate_sigmoid) : 1.0f;
+    float gt = 1.0f;
+    if (FORM == kBlock && a.gate_kind == kGateToken) {
+      const GateGrad one = gate_grad(cur.gt, a.gate_sigmoid);
+      gt = one.value;
+      if (first == 0) slope_of[sub] = one.slope;
+    }
     float e[VPT][N], q[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       __builtin_amdgcn_sched_barrier(0);      // one vector after the other: registers
       const int col = (first + i * BT) * N;
-      float x[N], dh[N], D[N], y[N], wpre[N], wpost[N], g[N], dpre[N], dpost[N], dg[N];
+      float x[N], dh[N], D[N], y[N], wpre[N], wpost[N], g[N], dpre[N], dpost[N], dg[N], slope[N];
       RV::unpack(cur.x[i], x);
       RV::unpack(cur.dh[i], dh);
       RV::unpack(cur.dr[i], D);
@@ -478,7 +494,11 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
         if constexpr (FULL) {
           RV::unpack(cur.gate[i], g);
 #pragma unroll
-          for (int c = 0; c < N; ++c) g[c] = gate_value(g[c], a.gate_sigmoid);
+          for (int c = 0; c < N; ++c) {
+            const GateGrad one = gate_grad(g[c], a.gate_sigmoid);
+            g[c] = one.value;
+            slope[c] = one.slope;
+          }
         } else {
           read(2, i, g);
 #pragma unroll
@@ -496,6 +516,7 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
         agate[i % VG][c] += FULL ? 0.0f : dg[c];
         q[0] = fmaf(e[i][c], y[c] * r.ys, q[0]);
         q[1] += dg[c];
+        if (FULL) dg[c] *= slope[c];
       }
       if (FULL && a.d_gate != nullptr && col < h)
         RV::template store<true>((uint8_t*)a.d_gate + at, col, H, RV::pack(dg));
@@ -503,7 +524,7 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
     if constexpr (HAS_Y) {
       row_sums<BT, 2>(q, buf2[turn][sub]);
       if (live && a.gate_kind == kGateToken && a.d_gate != nullptr && first == 0)
-        ((float*)a.d_gate)[row] = q[1];
+        ((float*)a.d_gate)[row] = q[1] * slope_of[sub];
       const float ym = a.post ? q[0] / (float)H : 0.0f;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
@@ -609,24 +630,38 @@ __global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(const Norm
     }
     float e[N], dpre[N], dpost[N], dg[N], q[2] = {0.0f, 0.0f};
     const GradRow r = grad_row(a, s, fx, fy);
-    const float gt = token_gate<RV>(a, row);
+    const bool token = has_y && a.gate_kind == kGateToken;
+    const GateGrad gt = token ? gate_grad(RV::load_one(a.gate, row), a.gate_sigmoid)
+                              : GateGrad{1.0f, 1.0f};
     auto columns = [&](int col) {
-      float wpre[N], wpost[N], g[N];
+      float wpre[N], wpost[N], g[N], slope[N];
       load(col);
       load_weights<RV, W32>(a.w_pre, col, H, a.offset, wpre);
       load_weights<RV, W32>(a.post ? a.w_post : nullptr, col, H, a.offset, wpost);
 #pragma unroll
-      for (int c = 0; c < N; ++c) g[c] = gt;
+      for (int c = 0; c < N; ++c) {
+        g[c] = gt.value;
+        slope[c] = 1.0f;
+      }
       if (has_y && (a.gate_kind == kGateChannel || a.gate_kind == kGateFull)) {
         typename RV::Raw gv =
             RV::template load<false>(a.gate + (a.gate_kind == kGateFull ? at : 0), col, H);
         RV::settle(gv, col, H);
         RV::unpack(gv, g);
 #pragma unroll
-        for (int c = 0; c < N; ++c) g[c] = gate_value(g[c], a.gate_sigmoid);
+        for (int c = 0; c < N; ++c) {
+          const GateGrad one = gate_grad(g[c], a.gate_sigmoid);
+          g[c] = one.value;
+          if (a.gate_kind == kGateFull) slope[c] = one.slope;
+        }
       }
-      if (has_y) grad_columns<N, true>(a, r, x, dh, y, wpre, wpost, g, D, dpre, e, dpost, dg);
-      else grad_columns<N, false>(a, r, x, dh, y, wpre, wpost, g, D, dpre, e, dpost, dg);
+      if (has_y) {
+        grad_columns<N, true>(a, r, x, dh, y, wpre, wpost, g, D, dpre, e, dpost, dg);
+#pragma unroll
+        for (int c = 0; c < N; ++c) dg[c] *= slope[c];
+      } else {
+        grad_columns<N, false>(a, r, x, dh, y, wpre, wpost, g, D, dpre, e, dpost, dg);
+      }
     };
     if (has_y) {
       for (int col = threadIdx.x * N; col < H; col += kWideThreads * N) {
@@ -639,7 +674,7 @@ __global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(const Norm
       }
       row_sums<kWideThreads, 2>(q, buf2[turn]);
       if (a.gate_kind == kGateToken && a.d_gate != nullptr && threadIdx.x == 0)
-        ((float*)a.d_gate)[row] = q[1];
+        ((float*)a.d_gate)[row] = q[1] * gt.slope;
     }
     const float ym = a.post ? q[0] / (float)H : 0.0f;
     const bool begin = row == blockIdx.x;
@@ -672,10 +707,13 @@ __global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(const Norm
 constexpr int kSumCols = 64, kSumWays = 16, kSumBatch = 16;
 
 // Column c of output o: 16 interleaved runs of the blocks' parts side by
-// side, each with 16 loads in flight, then the runs in order.
+// side, each with 16 loads in flight, then the runs in order.  gate: the
+// channel gate behind a sigmoid (else nullptr), whose slope multiplies output 2.
+template <int DT>
 __global__ __launch_bounds__(kSumCols* kSumWays) void grad_sum_kernel(const float* part,
                                                                      int parts, int H, float* g0,
-                                                                     float* g1, float* g2) {
+                                                                     float* g1, float* g2,
+                                                                     const uint8_t* gate) {
   __shared__ float run[kSumWays][kSumCols];
   float* out = blockIdx.y == 0 ? g0 : blockIdx.y == 1 ? g1 : g2;
   if (out == nullptr) return;
@@ -697,6 +735,7 @@ __global__ __launch_bounds__(kSumCols* kSumWays) void grad_sum_kernel(const floa
   s = 0.0f;
 #pragma unroll
   for (int i = 0; i < kSumWays; ++i) s += run[i][x];
+  if (blockIdx.y == 2 && gate != nullptr) s *= gate_grad(RowVec<DT>::load_one(gate, c), true).slope;
   out[c] = s;
 }
 
@@ -824,9 +863,18 @@ hipError_t launch_norm_grad(const NormGradArgs& a, int dtype, bool w32, float* g
   }
   if (err != hipSuccess || (g_pre == nullptr && g_post == nullptr && g_gate == nullptr))
     return err;
-  grad_sum_kernel<<<dim3((a.H + kSumCols - 1) / kSumCols, 3), kSumCols * kSumWays, 0, stream>>>(
-      a.part, blocks, a.H, g_pre, g_post, g_gate);
-  return hipGetLastError();
+  const bool slope = blocks > 0 && a.gate_kind == kGateChannel && a.gate_sigmoid;
+  auto sum = [&](auto dt) {
+    grad_sum_kernel<decltype(dt)::value>
+        <<<dim3((a.H + kSumCols - 1) / kSumCols, 3), kSumCols * kSumWays, 0, stream>>>(
+            a.part, blocks, a.H, g_pre, g_post, g_gate, slope ? a.gate : nullptr);
+    return hipGetLastError();
+  };
+  switch (dtype) {
+    case kBf16: return sum(std::integral_constant<int, kBf16>());
+    case kF16: return sum(std::integral_constant<int, kF16>());
+    default: return sum(std::integral_constant<int, kF32>());
+  }
 }
 
 }  // namespace moe

@@ -783,6 +783,25 @@ def test_norm_optional_gradients(gpu, gate, skip):
     check_norm_grad(p, make_norm(rng, 40, 272, torch.bfloat16, torch.bfloat16, gate), rng, skip)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("H", [5, 200, 2056, 9000])
+@pytest.mark.parametrize("gate", ["token", "channel", "full"])
+def test_norm_saturated_gates(gpu, gate, H, dtype):
+    """Gates whose sigmoid is next to 0 or 1: their gradient is its slope s (1 -
+    s), 2e-9 at 20, where fp32 has no step between s and 1."""
+    rng = np.random.default_rng(H)
+    T = 17
+    p = moe.BlockNorm(T, H, dtype=dtype, weight_dtype=torch.float32, post_norm=True, gate=gate,
+                      gate_sigmoid=True, residual_scale=0.7)
+    t = make_norm(rng, T, H, dtype, torch.float32, gate)
+    at = torch.arange(t["gate"].numel()) % 7
+    t["gate"] = torch.tensor([12.0, -12.0, 20.0, -20.0, 0.0, 17.0, 3.5])[at].view(
+        t["gate"].shape).to(dtype)
+    check_norm(p, t)
+    check_norm_grad(p, t, rng)
+    check_norm_grad(p, t, rng, skip=("grad_normed", "grad_post_weight"))
+
+
 def test_norm_without_weights(gpu):
     rng = np.random.default_rng(6)
     p = moe.BlockNorm(9, 300, post_norm=True, weight_offset=1.0)
