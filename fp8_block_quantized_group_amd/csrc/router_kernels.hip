@@ -587,7 +587,11 @@ __device__ __forceinline__ void sort_descending(uint32_t (&key)[N]) {
 // carried, or two keys' errors, leave open sends a token to the whole wave, as
 // a router_topk_kernel wave takes it.  Keys that are 2-byte logits are exact
 // in the bits above.
-constexpr float kNearPlaces = 0x1p-17f;  // 16 steps of a group's two keys and of their sum
+//
+// A group's two keys and their sum lose less than 16 steps each: kNearPlaces of
+// their magnitudes, and of subnormal ones, whose step is 2^-149, kNearLeast.
+constexpr float kNearPlaces = 0x1p-17f;
+constexpr float kNearLeast = 0x1p-143f;  // 64 such steps
 
 template <int DT, int VPL, int WAVE_VPL>
 __global__ __launch_bounds__(64 * kRouterWaves) void router_rows_kernel(const RouterArgs a) {
@@ -678,7 +682,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_rows_kernel(const Ro
       const float fv = from_ordered(v);
       float mag = fabsf(from_ordered(b));
       if (a.group_top > 1 && s != 0u) mag += fabsf(from_ordered(s));
-      const float err = fminf(fmaf(kNearPlaces, mag, near), FLT_MAX);
+      const float err = fminf(fmaf(kNearPlaces, mag, near + kNearLeast), FLT_MAX);
       const uint32_t dropped = row_max(keep || !some ? 0u : ordered_bits(fv + err));
       const uint32_t kept = ~row_max(keep && some ? ~ordered_bits(fv - err) : 0u);
       unclear = kept <= dropped;

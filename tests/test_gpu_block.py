@@ -235,6 +235,22 @@ def test_router_many_tokens_hard_to_tell(gpu, score, groups, group_top):
     check_router(x.bfloat16(), 8, None, None, tokens=many, **kw)
 
 
+@pytest.mark.parametrize("tokens", [None, 20003])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(64, 16), (128, 8), (256, 8), (256, 16)])
+def test_router_groups_of_subnormal_logits(gpu, E, groups, score, tokens):
+    """Logits a few steps of 2^-149 apart, or zero: groups are told apart by
+    them, in batches of any size."""
+    rng = np.random.default_rng(21)
+    steps = rng.integers(-40, 41, (200, E))
+    steps[0::5] *= 1 << 10
+    steps[1::5] //= 16
+    x = torch.from_numpy((steps * 2.0 ** -149).astype(np.float32))
+    assert (x.double() * 2.0 ** 149 == torch.from_numpy(steps)).all()
+    check_router(x, 5, None, None, tokens=tokens, score=score, groups=groups,
+                 topk_groups=groups // 4 + 1)
+
+
 def test_router_ties_go_to_the_lower_index(gpu):
     """bf16 logits from a few values and a zero bias: most keys are equal."""
     rng = np.random.default_rng(6)
