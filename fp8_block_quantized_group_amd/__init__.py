@@ -760,6 +760,8 @@ class MoeBlock:
         """residual_out (new unless given; may be residual).  ``normed``: the
         residual's pre norm where the block before this one left it; with
         ``next_normed`` the next block's is written there, by next_weight."""
+        p = self.layer.p
+        _arg(normed, "normed", self.norm.dtype, (p.num_tokens, p.hidden), residual.device)
         with torch.cuda.device(_device(residual, "residual")):
             if normed is None:
                 normed = self.hidden

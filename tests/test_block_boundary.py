@@ -208,3 +208,25 @@ def test_argument_checks():
                     (x.to("meta"), "meta")]:
         with pytest.raises(ValueError, match=word):
             moe._arg(t, "x", torch.float32, (4, 8), d)
+
+
+def small_block(experts=8):
+    """A block on the host: what it refuses, it refuses before anything runs."""
+    from types import SimpleNamespace
+    layer = SimpleNamespace(p=moe.Problem(4, 128, 128, 8, 2))
+    return moe.MoeBlock(layer, moe.Router(4, experts, 2), torch.zeros((experts, 128)),
+                        moe.BlockNorm(4, 128))
+
+
+def test_block_refuses_a_pre_norm_its_layer_would_misread():
+    """One of another type or shape: the layer would read its bytes as bfloat16."""
+    x, block = torch.zeros((4, 128), dtype=torch.bfloat16), small_block()
+    for bad, word in [(x.half(), "normed must be torch.bfloat16"),
+                      (x.float(), "normed must be torch.bfloat16"),
+                      (x[:, :64].contiguous(), "normed must be"),
+                      (x.t().contiguous().t(), "normed must be contiguous"),
+                      (x.to("meta"), "normed is on meta")]:
+        with pytest.raises(ValueError, match=word):
+            block(x, normed=bad)
+    with pytest.raises(ValueError, match="GPU"):
+        block(x, normed=x)
