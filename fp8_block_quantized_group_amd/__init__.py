@@ -759,8 +759,13 @@ class MoeBlock:
                  residual_out=None, next_normed=None, next_weight=None):
         """residual_out (new unless given; may be residual).  ``normed``: the
         residual's pre norm where the block before this one left it; with
-        ``next_normed`` the next block's is written there, by next_weight."""
-        p = self.layer.p
+        ``next_normed`` the next block's is written there, by next_weight.  With
+        ``eplb`` the router's experts are its logical ones."""
+        p, r = self.layer.p, self.router
+        experts = p.num_experts if eplb is None else eplb["l2p"].shape[0]
+        if r.num_experts != experts:
+            raise ValueError(f"the router chooses from {r.num_experts} experts, the layer has "
+                             f"{experts}{'' if eplb is None else ' logical ones'}")
         _arg(normed, "normed", self.norm.dtype, (p.num_tokens, p.hidden), residual.device)
         with torch.cuda.device(_device(residual, "residual")):
             if normed is None:

@@ -230,3 +230,17 @@ def test_block_refuses_a_pre_norm_its_layer_would_misread():
             block(x, normed=bad)
     with pytest.raises(ValueError, match="GPU"):
         block(x, normed=x)
+
+
+def test_block_refuses_a_router_of_other_experts():
+    """The layer would drop the ids past its own experts."""
+    x = torch.zeros((4, 128), dtype=torch.bfloat16)
+    maps = [dict(l2p=torch.zeros((n, 2), dtype=torch.int64)) for n in (7, 8, 9)]
+    for n in (7, 9):
+        with pytest.raises(ValueError, match=f"{n} experts, the layer has 8$"):
+            small_block(n)(x)
+    with pytest.raises(ValueError, match="8 experts, the layer has 7 logical ones"):
+        small_block(8)(x, eplb=maps[0])
+    for n, eplb in ((8, None), (9, maps[2]), (7, maps[0])):
+        with pytest.raises(ValueError, match="GPU"):
+            small_block(n)(x, eplb=eplb)
