@@ -446,8 +446,13 @@ class _Descriptor:
     """A frozen dataclass whose C struct is made once."""
 
     def __post_init__(self):
-        object.__setattr__(self, "_c", self._struct())
-        object.__setattr__(self, "_ref", ctypes.byref(self._c))
+        c = self._struct()
+        for name, kind in c._fields_:
+            value = getattr(self, name)
+            if kind is ctypes.c_int32 and isinstance(value, int) and getattr(c, name) != value:
+                raise ValueError(f"{name} = {value} does not fit 32 bits")
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ref", ctypes.byref(c))
 
 
 @dataclass(frozen=True)

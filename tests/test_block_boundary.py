@@ -244,3 +244,14 @@ def test_block_refuses_a_router_of_other_experts():
     for n, eplb in ((8, None), (9, maps[2]), (7, maps[0])):
         with pytest.raises(ValueError, match="GPU"):
             small_block(n)(x, eplb=eplb)
+
+
+def test_descriptors_refuse_sizes_past_32_bits():
+    """ctypes would keep their low 32 bits: 2^32 + 3 tokens would run as 3."""
+    for make in (lambda n: moe.Router(n, 8, 2), lambda n: moe.Router(4, n, 2),
+                 lambda n: moe.ExpertRows(n, 8, 8, 2), lambda n: moe.ExpertRows(4, n, 8, 2),
+                 lambda n: moe.BlockNorm(n, 8), lambda n: moe.BlockNorm(4, n)):
+        for n in (2 ** 31, 2 ** 32 + 3, -2 ** 31 - 1):
+            with pytest.raises(ValueError, match="32 bits"):
+                make(n)
+        make(2 ** 31 - 1)
