@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass, replace
+from dataclasses import dataclass, fields, replace
 from typing import Optional
 
 import torch
@@ -453,6 +453,9 @@ class _Descriptor:
                 raise ValueError(f"{name} = {value} does not fit 32 bits")
         object.__setattr__(self, "_c", c)
         object.__setattr__(self, "_ref", ctypes.byref(c))
+
+    def __reduce__(self):                   # a reference to a C struct has no copy
+        return type(self), tuple(getattr(self, f.name) for f in fields(self))
 
 
 @dataclass(frozen=True)

@@ -255,3 +255,14 @@ def test_descriptors_refuse_sizes_past_32_bits():
             with pytest.raises(ValueError, match="32 bits"):
                 make(n)
         make(2 ** 31 - 1)
+
+
+def test_descriptors_can_be_copied_and_pickled():
+    """As part of a model or of a worker's arguments."""
+    import copy
+    import pickle
+    for p in (moe.Router(4, 8, 2, score="sigmoid", dtype=torch.float16),
+              moe.ExpertRows(4, 8, 8, 2), moe.BlockNorm(4, 8, gate="token", post_norm=True)):
+        for other in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p))):
+            assert other == p and bytes(other._c) == bytes(p._c)
+            assert getattr(other, "gate_shape", None) == getattr(p, "gate_shape", None)
