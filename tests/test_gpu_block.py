@@ -840,6 +840,30 @@ def test_norm_zero_rows_and_large_values(gpu):
     check_norm_grad(p, t, rng)
 
 
+@pytest.mark.parametrize("block", [True, False])
+@pytest.mark.parametrize("dtype,T,H", [
+    (torch.float32, 2100, 128), (torch.float32, 2100, 400), (torch.float32, 700, 900),
+    (torch.float32, 530, 2000), (torch.float32, 530, 4000), (torch.float32, 270, 8000),
+    (torch.float32, 270, 9000), (torch.float32, 40, 1500), (torch.bfloat16, 1100, 1030),
+    (torch.bfloat16, 530, 7168), (torch.bfloat16, 270, 12001), (torch.bfloat16, 40, 32768)])
+def test_norm_large_rows_among_others(gpu, dtype, T, H, block):
+    """Rows whose squares pass fp32's range beside rows that a block, or lanes
+    side by side in one, take with them or next: in every shape a row can have,
+    with several rows per block."""
+    rng = np.random.default_rng(H)
+    gate = "channel" if block else "none"
+    p = moe.BlockNorm(T, H, dtype=dtype, weight_dtype=torch.float32, post_norm=True, gate=gate)
+    t = make_norm(rng, T, H, dtype, torch.float32, gate, y=block)
+    size = torch.ones((2, T, 1))
+    size[0, T // 2::53], size[0, 3::37] = 3e30, 1e22
+    size[1, 5::41], size[1, 3::74] = 1e25, 1e20
+    t["residual"] = (t["residual"] * size[0]).to(dtype)
+    if block:
+        t["y"] = (t["y"] * size[1]).to(dtype)
+    check_norm(p, t)
+    check_norm_grad(p, t, rng)
+
+
 def test_norm_in_place_and_unaligned(gpu):
     rng = np.random.default_rng(8)
     p = moe.BlockNorm(70, 2056, post_norm=True, gate="full")
