@@ -1166,6 +1166,41 @@ def test_block_in_a_graph(gpu):
         assert torch.equal(got, out)
 
 
+@pytest.mark.parametrize("layout", [moe.LAYOUT_CONTIGUOUS, moe.LAYOUT_INDEXED])
+def test_block_captured_whole(gpu, layout):
+    """One call, the logits' product in it: every replay gives the eager bits, of
+    other inputs, with eager work and cleared buffers in between."""
+    block, layer, norm, w, x, g, pad = make_block(T=200, layout=layout)
+    got, nxt = torch.empty_like(x), torch.empty_like(x)
+
+    def run():
+        block(x, gate=g, is_padding=pad, residual_out=got, next_normed=nxt,
+              next_weight=w["next"])
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    rng = np.random.default_rng(23)
+    bufs = (got, nxt, block.hidden, block.y, block.topk_ids, block.topk_weights)
+    for _ in range(4):
+        x.copy_(rand(rng, tuple(x.shape), torch.bfloat16, 2.0))
+        run()
+        want = [t.clone() for t in bufs]
+        for t in bufs:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(bufs, want):
+            assert torch.equal(a, b)
+
+
+def test_block_of_no_tokens(gpu):
+    block, layer, norm, w, x, g, pad = make_block(T=0)
+    assert block(x, gate=g, is_padding=pad).shape == (0, 256)
+
+
 def test_block_refusals(gpu):
     block, layer, norm, w, x, g, pad = make_block()
     r, rw = block.router, block.router_weight
