@@ -449,7 +449,8 @@ class _Descriptor:
         c = self._struct()
         for name, kind in c._fields_:
             value = getattr(self, name)
-            if kind is ctypes.c_int32 and isinstance(value, int) and getattr(c, name) != value:
+            whole = kind is ctypes.c_int32 and hasattr(value, "__index__")
+            if whole and getattr(c, name) != value:
                 raise ValueError(f"{name} = {value} does not fit 32 bits")
         object.__setattr__(self, "_c", c)
         object.__setattr__(self, "_ref", ctypes.byref(c))

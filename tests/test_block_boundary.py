@@ -257,6 +257,14 @@ def test_descriptors_refuse_sizes_past_32_bits():
         make(2 ** 31 - 1)
 
 
+def test_descriptors_refuse_numpy_sizes_past_32_bits():
+    import numpy as np
+    for n in (np.int64(2 ** 32 + 3), np.uint32(2 ** 31), torch.tensor(2 ** 32 + 3)):
+        with pytest.raises(ValueError, match="32 bits"):
+            moe.BlockNorm(n, 8)
+    assert moe.BlockNorm(np.int64(4), 8)._c.num_tokens == 4
+
+
 def test_descriptors_can_be_copied_and_pickled():
     """As part of a model or of a worker's arguments."""
     import copy
