@@ -731,7 +731,8 @@ class MoeBlock:
 
     ``norm`` describes both norms (dtype bfloat16, the layer's); ``router_weight``
     is [num_experts, hidden] and makes the logits, router.dtype, by a product of
-    torch's.  The batched layout has no place here: its slabs come from a
+    torch's: a float32 router copies the normed rows to float32 for it on every
+    call (16384 x 7168 by 256 experts: 550 us, 71 with a bfloat16 one).  The batched layout has no place here: its slabs come from a
     dispatch that already routed.
     """
 

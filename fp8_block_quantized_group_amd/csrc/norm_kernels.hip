@@ -6,13 +6,13 @@
 //   h  = r' * rsqrt(mean(r'^2) + eps) * (o + w_pre)
 //
 // A row stays in registers from its first load to its last store: BT lanes
-// hold VPT vectors each, the row sums cross the lanes of a wave by shuffles
+// hold VPT vectors each, the row sums cross the lanes of a wave in registers
 // and, for BT over 64, the waves through LDS.  Everything is fp32; h is made
 // from r' before r' is rounded.
 //
 // Bound by HBM: every stream is read or written once, non-temporal.  MI355X,
-// where a 2 GiB copy moves 5.1 TB/s: forward 16381 x 4096 bf16 91 us (537 MB,
-// 5.9 TB/s); gradients 4095 x 7168 bf16 77-84 us (352 MB, 4.2-4.6 TB/s: the
+// where a 2 GiB copy moves 5.1 TB/s: forward 16381 x 4096 bf16 92 us (537 MB,
+// 5.8 TB/s); gradients 4095 x 7168 bf16 75-80 us (352 MB, 4.4-4.7 TB/s: the
 // row sums' barriers leave gaps, and the column sums of 256 blocks cost 22 MB
 // each way).
 #include <type_traits>
@@ -578,8 +578,8 @@ __global__ __launch_bounds__(BT < kGradThreads ? kGradThreads : BT) void norm_gr
 // Rows too wide for registers (2-byte types past 8192 columns, fp32 past
 // 8192): one block per row, which is read three times (from the caches after
 // the first): for its first sums, for its second, and to write.  The block's
-// column sums are kept in its part itself.  2048 x 16384 bf16: 423 us, 0.95
-// TB/s of what the call has to move; 63 us without a block, in registers.
+// column sums are kept in its part itself.  2048 x 16384 bf16: 440 us, 0.9
+// TB/s of what the call has to move; 62 us without a block, in registers.
 constexpr int kWideThreads = 1024;
 
 template <class RV, bool W32>

@@ -22,7 +22,8 @@
 // The choice runs on 32-bit keys as ordered integers, k rounds of a wave
 // maximum; 64-bit keys are computed only for a token where two keys that
 // decide something lie within the 32-bit keys' error (kNear*: some tokens in
-// a thousand).
+// a thousand), those of all its experts where more keys than a wave has lanes
+// do (saturated scores, or scores that drown in a bias).
 #include <float.h>
 #include <limits.h>
 

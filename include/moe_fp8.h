@@ -476,9 +476,12 @@ moe_status_t moe_forward_static(const moe_problem_t* p, const void* hidden,
  * (moe_dtype_t); data pointers need their element's alignment only, index
  * arrays 4 bytes.  Sums, softmax statistics and norms are held in fp32 and
  * rounded once on the way out.  Results do not depend on timing: no sum's
- * order does.  Outputs must not overlap inputs or each other except where a
- * call says so (then as the same pointer).  An empty batch (num_tokens 0) is
- * a no-op except where a call below says what it still writes. */
+ * order does.  Between batch sizes a token's experts are the same; its
+ * weights, norms and gradients may differ by roundings (more or fewer lanes
+ * share a row's sums).  Outputs must not overlap inputs or each other except
+ * where a call says so (then as the same pointer).  An empty batch
+ * (num_tokens 0) is a no-op except where a call below says what it still
+ * writes. */
 
 /* Element types of the calls below. */
 typedef enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1, MOE_DT_F32 = 2 } moe_dtype_t;
