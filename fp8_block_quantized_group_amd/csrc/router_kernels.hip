@@ -220,6 +220,7 @@ __device__ bool keep_exactly(const RouterArgs& a, const uint64_t (&key)[VPL], ui
     }
     group = lane >> a.group_lanes_log;
   } else {
+    wave_lds_order();                       // what lay there has been read
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (lane * VPL + i < a.E) wkeys[lane * VPL + i] = key[i];
@@ -268,6 +269,7 @@ __device__ __forceinline__ void keep_groups(const RouterArgs& a, uint32_t (&key)
     group = lane >> a.group_lanes_log;
     pitch = lanes;
   } else {
+    wave_lds_order();                     // what lay there, of the token before, has been read
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (lane * VPL + i < a.E) wkeys[lane * VPL + i] = key[i];
@@ -292,7 +294,6 @@ __device__ __forceinline__ void keep_groups(const RouterArgs& a, uint32_t (&key)
     if (kept <= dropped) {
       uint64_t exact[VPL];
       exact_keys<VPL>(a, x, m, exact);
-      wave_lds_order();
       keep = keep_exactly<VPL>(a, exact, lds);
     }
   }
@@ -325,10 +326,7 @@ __device__ int choose_exactly(const RouterArgs& a, const float (&x)[VPL], float 
   const int lane = threadIdx.x & 63;
   uint64_t key[VPL];
   exact_keys<VPL>(a, x, m, key);
-  if (a.groups > 1) {
-    wave_lds_order();                     // the 32-bit keys there have been read
-    drop_groups<VPL>(a, keep_exactly<VPL>(a, key, wkeys), key);
-  }
+  if (a.groups > 1) drop_groups<VPL>(a, keep_exactly<VPL>(a, key, wkeys), key);
   int my_id = -1;
   for (int j = 0; j < a.k; ++j) {
     uint64_t b = key[0];

@@ -251,6 +251,18 @@ def test_router_groups_of_subnormal_logits(gpu, E, groups, score, tokens):
                  topk_groups=groups // 4 + 1)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(256, 2), (128, 2), (64, 2)])
+def test_router_open_tokens_of_one_wave(gpu, E, groups, score):
+    """All four tokens of a wave need the choice of 64 bits, one after the other
+    through the same LDS, groups and experts alike."""
+    rng = np.random.default_rng(25)
+    x = rand(rng, (701, E), torch.float32, 2.0 ** -21)
+    for top in (1, 2):
+        check_router(x, 8, torch.zeros(E), None, tokens=12007, score=score, groups=groups,
+                     topk_groups=1, group_top=top)
+
+
 def test_router_ties_go_to_the_lower_index(gpu):
     """bf16 logits from a few values and a zero bias: most keys are equal."""
     rng = np.random.default_rng(6)
