@@ -61,6 +61,12 @@ class _BlockNorm(ctypes.Structure):
             "eps", "residual_scale", "weight_offset")]
 
 
+class _ExpertLinear(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_rows", "in_features", "out_features", "num_experts", "dtype", "activation")] + [
+        ("act_limit", ctypes.c_float)]
+
+
 class _Eplb(ctypes.Structure):
     _fields_ = [("logical_to_physical", ctypes.c_void_p), ("map_stride", ctypes.c_int32),
                 ("replica_count", ctypes.c_void_p), ("num_logical", ctypes.c_int32),
@@ -92,7 +98,9 @@ EXPORTS = ("moe_routing_sizes", "moe_stage_workspace_size", "moe_workspace_size"
            "moe_forward_static", "moe_last_error",
            "moe_router_topk", "moe_router_topk_backward", "moe_permute_workspace_size",
            "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
-           "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward")
+           "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward",
+           "moe_expert_linear", "moe_expert_linear_workspace_size",
+           "moe_expert_linear_backward")
 
 _lib = None
 
@@ -139,6 +147,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_block_norm.argtypes = [P(_BlockNorm)] + [V] * 8
     lib.moe_block_norm_workspace_size.argtypes = [P(_BlockNorm), P(S)]
     lib.moe_block_norm_backward.argtypes = [P(_BlockNorm)] + [V] * 13 + [S, V]
+    lib.moe_expert_linear.argtypes = [P(_ExpertLinear)] + [V] * 6
+    lib.moe_expert_linear_workspace_size.argtypes = [P(_ExpertLinear), P(S)]
+    lib.moe_expert_linear_backward.argtypes = [P(_ExpertLinear)] + [V] * 8 + [S, V]
     lib.moe_last_error.argtypes = []
     for name in EXPORTS:
         fn = getattr(lib, name)
@@ -721,6 +732,81 @@ def block_norm_backward(p: BlockNorm, residual_out, grad_normed, grad_residual, 
          _arg(grad_post_weight, "grad_post_weight", torch.float32, (H,), d),
          _arg(grad_gate, "grad_gate", p.dtype if p.gate == "full" else torch.float32,
               p.gate_shape, d), wp, wn)
+
+
+# ---- the experts' own products --------------------------------------------------
+
+_LINEAR_ACTS = {"none": -1, **{name: i for i, name in enumerate(ACTIVATIONS)}}
+_SINGLE_ACTS = ("none", "silu_no_mul", "gelu_no_mul", "gelu_tanh_no_mul", "relu2_no_mul")
+
+
+@dataclass(frozen=True)
+class ExpertLinear(_Descriptor):
+    """moe_expert_linear_t: a linear layer of rows sorted by expert, with the
+    activation that follows it."""
+    num_rows: int
+    in_features: int
+    out_features: int
+    num_experts: int = 1
+    dtype: torch.dtype = torch.bfloat16
+    activation: str = "none"                # "none" or one of ACTIVATIONS
+    act_limit: float = 0.0
+
+    def _struct(self):
+        return _ExpertLinear(self.num_rows, self.in_features, self.out_features,
+                             self.num_experts, _choice(self.dtype, _DTYPES, "dtype"),
+                             _choice(self.activation, _LINEAR_ACTS, "activation"),
+                             self.act_limit)
+
+    def __post_init__(self):
+        super().__post_init__()
+        wide = self.out_features * (1 if self.activation in _SINGLE_ACTS else 2)
+        object.__setattr__(self, "wide", wide)      # weight rows of an expert
+
+
+def _offsets(p, expert_offsets, d):
+    return _arg(expert_offsets, "expert_offsets", torch.int32, (p.num_experts + 1,), d)
+
+
+def expert_linear(p: ExpertLinear, x, weight, out, expert_offsets=None, pre_act=None):
+    """moe_expert_linear: out = F(x W_e^T) for every expert's rows (expert_offsets
+    None: the one expert has all); pre_act: the product before F, for the gradient."""
+    d = _device(x, "x")
+    R, K, N, dt = p.num_rows, p.in_features, p.out_features, p.dtype
+    _run(load_library().moe_expert_linear, d, p._ref, _arg(x, "x", dt, (R, K), d),
+         _offsets(p, expert_offsets, d),
+         _arg(weight, "weight", dt, (p.num_experts, p.wide, K), d),
+         _arg(out, "out", dt, (R, N), d), _arg(pre_act, "pre_act", dt, (R, p.wide), d))
+
+
+def expert_linear_workspace_size(p: ExpertLinear) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().moe_expert_linear_workspace_size(p._ref, ctypes.byref(n)))
+    return n.value
+
+
+def alloc_expert_linear_workspace(p: ExpertLinear, device="cuda") -> Optional[torch.Tensor]:
+    """Scratch of expert_linear_backward; None without an activation."""
+    n = expert_linear_workspace_size(p)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n > 0 else None
+
+
+def expert_linear_backward(p: ExpertLinear, x, weight, grad_out, grad_x=None, grad_weight=None,
+                           expert_offsets=None, pre_act=None, ws="auto"):
+    """moe_expert_linear_backward: grad_x and grad_weight (either may be None;
+    x is needed for grad_weight, weight for grad_x); ws: "auto" allocates it
+    where it is needed."""
+    d = _device(grad_out, "grad_out")
+    R, K, N, dt = p.num_rows, p.in_features, p.out_features, p.dtype
+    shape = (p.num_experts, p.wide, K)
+    if isinstance(ws, str):
+        ws = alloc_expert_linear_workspace(p, d)
+    wp, wn = _scratch(ws, d)
+    _run(load_library().moe_expert_linear_backward, d, p._ref, _arg(x, "x", dt, (R, K), d),
+         _offsets(p, expert_offsets, d), _arg(weight, "weight", dt, shape, d),
+         _arg(pre_act, "pre_act", dt, (R, p.wide), d),
+         _arg(grad_out, "grad_out", dt, (R, N), d), _arg(grad_x, "grad_x", dt, (R, K), d),
+         _arg(grad_weight, "grad_weight", dt, shape, d), wp, wn)
 
 
 class MoeBlock:

@@ -1,0 +1,189 @@
+// Host side of the experts' own products: argument validation and launches.
+#include <algorithm>
+
+#include "api_common.h"
+#include "kernels.h"
+
+using moe::check_ptr;
+using moe::fail;
+using moe::launch_status;
+using moe::ok;
+
+namespace {
+
+constexpr float kSwigluDefaultLimit = 7.0f;
+
+size_t elem(int dt) { return dt == MOE_DT_F32 ? 4 : 2; }
+
+moe_status_t check_opt(const void* ptr, const char* name, size_t align) {
+  return ptr == nullptr ? MOE_OK : check_ptr(ptr, name, align);
+}
+
+bool gated(int act) {
+  return act != MOE_ACT_NONE && (act < MOE_ACT_SILU_NO_MUL || act > MOE_ACT_RELU2_NO_MUL);
+}
+int wide_of(int out_features, int act) { return out_features * (gated(act) ? 2 : 1); }
+float limit_of(int act, float limit) {
+  const bool clamps = act == MOE_ACT_SWIGLUOAI || act == MOE_ACT_SWIGLUSTEP;
+  return clamps && limit == 0.0f ? kSwigluDefaultLimit : limit;
+}
+
+// what every linear layer of rows sorted by expert has
+moe_status_t check_sizes(int rows, int in, int out, int experts, int dtype, int act,
+                         float limit) {
+  if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "num_rows < 0 (%d)", rows);
+  if (in < 1 || in > 32768)
+    return fail(MOE_ERR_UNSUPPORTED, "in_features must be in [1, 32768], got %d", in);
+  if (out < 1 || out > 32768)
+    return fail(MOE_ERR_UNSUPPORTED, "out_features must be in [1, 32768], got %d", out);
+  if (experts < 1 || experts > 1024)
+    return fail(MOE_ERR_UNSUPPORTED, "num_experts must be in [1, 1024], got %d", experts);
+  if (dtype < MOE_DT_BF16 || dtype > MOE_DT_F32)
+    return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLUSTEP)
+    return fail(MOE_ERR_INVALID_ARG, "unknown activation %d", act);
+  if (!(limit >= 0.0f) || limit > 3.0e38f)
+    return fail(MOE_ERR_INVALID_ARG, "act_limit must be finite and >= 0, got %g", (double)limit);
+  if (limit > 0.0f && act != MOE_ACT_SILU && act != MOE_ACT_SWIGLUOAI &&
+      act != MOE_ACT_SWIGLUSTEP)
+    return fail(MOE_ERR_UNSUPPORTED, "activation %d takes no clamp limit", act);
+  // launches count their tiles in 31 bits
+  const int64_t m = (int64_t)rows / 64 + std::min(rows, experts);
+  const int64_t n = (std::max(in, wide_of(out, act)) + 63) / 64;
+  if (m * n >= (int64_t)1 << 31)
+    return fail(MOE_ERR_UNSUPPORTED, "%d rows of %d columns are more than 2^31 tiles", rows,
+                std::max(in, out));
+  return MOE_OK;
+}
+
+moe_status_t check_offsets(const int32_t* offsets, int experts) {
+  if (offsets == nullptr && experts != 1)
+    return fail(MOE_ERR_INVALID_ARG, "expert_offsets is NULL with %d experts", experts);
+  return check_opt(offsets, "expert_offsets", 4);
+}
+
+moe_status_t check_linear(const moe_expert_linear_t* p) {
+  if (p == nullptr) return fail(MOE_ERR_INVALID_ARG, "expert linear is NULL");
+  CHECK(check_sizes(p->num_rows, p->in_features, p->out_features, p->num_experts, p->dtype,
+                    p->activation, p->act_limit));
+  // an expert's weights are addressed with 32-bit buffer offsets
+  const int64_t wide = wide_of(p->out_features, p->activation);
+  if (wide * p->in_features * (int64_t)elem(p->dtype) >= (int64_t)0xF0000000u)
+    return fail(MOE_ERR_UNSUPPORTED, "one expert's weights must be under 3.75 GiB");
+  // and the weights' gradient is tiled expert by expert
+  if ((wide + 63) / 64 * ((p->in_features + 63) / 64) * p->num_experts >= (int64_t)1 << 31)
+    return fail(MOE_ERR_UNSUPPORTED, "the experts' weights are more than 2^31 tiles");
+  return MOE_OK;
+}
+
+size_t linear_ws_bytes(const moe_expert_linear_t* p) {
+  if (p->activation == MOE_ACT_NONE) return 0;
+  return moe::round_up((size_t)p->num_rows * wide_of(p->out_features, p->activation) *
+                       elem(p->dtype));
+}
+
+moe::ExpertGemmArgs gemm_args(const moe_expert_linear_t* p, const int32_t* offsets) {
+  moe::ExpertGemmArgs a{};
+  a.offsets = offsets;
+  a.R = p->num_rows;
+  a.K = p->in_features;
+  a.N = p->out_features;
+  a.wide = wide_of(p->out_features, p->activation);
+  a.E = p->num_experts;
+  a.act = p->activation;
+  a.limit = limit_of(p->activation, p->act_limit);
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_expert_linear(const moe_expert_linear_t* p, const void* x,
+                               const int32_t* expert_offsets, const void* weight, void* out,
+                               void* pre_act, void* stream) {
+  CHECK(check_linear(p));
+  if (p->num_rows == 0) return ok();
+  const size_t es = elem(p->dtype);
+  CHECK(check_ptr(x, "x", es));
+  CHECK(check_offsets(expert_offsets, p->num_experts));
+  CHECK(check_ptr(weight, "weight", es));
+  CHECK(check_ptr(out, "out", es));
+  CHECK(check_opt(pre_act, "pre_act", es));
+  moe::ExpertGemmArgs a = gemm_args(p, expert_offsets);
+  a.a = (const uint8_t*)x;
+  a.b = (const uint8_t*)weight;
+  a.out = (uint8_t*)out;
+  a.pre = (uint8_t*)pre_act;
+  return launch_status(moe::launch_expert_out(a, p->dtype, (hipStream_t)stream),
+                       "moe_expert_linear");
+}
+
+moe_status_t moe_expert_linear_workspace_size(const moe_expert_linear_t* p, size_t* bytes) {
+  CHECK(check_linear(p));
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = linear_ws_bytes(p);
+  return ok();
+}
+
+moe_status_t moe_expert_linear_backward(const moe_expert_linear_t* p, const void* x,
+                                        const int32_t* expert_offsets, const void* weight,
+                                        const void* pre_act, const void* grad_out, void* grad_x,
+                                        void* grad_weight, void* ws, size_t ws_bytes,
+                                        void* stream) {
+  CHECK(check_linear(p));
+  const size_t es = elem(p->dtype);
+  const bool act = p->activation != MOE_ACT_NONE;
+  CHECK(check_opt(grad_weight, "grad_weight", es));
+  if (p->num_rows > 0) {
+    CHECK(check_offsets(expert_offsets, p->num_experts));
+    CHECK(check_ptr(grad_out, "grad_out", es));
+    CHECK(check_opt(grad_x, "grad_x", es));
+    if (grad_weight != nullptr) CHECK(check_ptr(x, "x", es));
+    if (grad_x != nullptr) CHECK(check_ptr(weight, "weight", es));
+    if (act) {
+      CHECK(check_ptr(pre_act, "pre_act", es));
+      CHECK(check_ptr(ws, "ws", 16));
+      if (ws_bytes < linear_ws_bytes(p))
+        return fail(MOE_ERR_WORKSPACE, "expert linear workspace too small: %zu < %zu bytes",
+                    ws_bytes, linear_ws_bytes(p));
+    } else if (pre_act != nullptr) {
+      return fail(MOE_ERR_INVALID_ARG, "pre_act given without an activation");
+    }
+  }
+  const hipStream_t s = (hipStream_t)stream;
+  moe::ExpertGemmArgs a = gemm_args(p, expert_offsets);
+  a.a = (const uint8_t*)grad_out;
+  a.act = MOE_ACT_NONE;
+  if (act && p->num_rows > 0 && (grad_x != nullptr || grad_weight != nullptr)) {
+    moe::ExpertActGradArgs g{};
+    g.pre = (const uint8_t*)pre_act;
+    g.grad_out = (const uint8_t*)grad_out;
+    g.d = (uint8_t*)ws;
+    g.offsets = expert_offsets;
+    g.R = p->num_rows;
+    g.N = p->out_features;
+    g.E = p->num_experts;
+    g.act = p->activation;
+    g.limit = a.limit;
+    CHECK(launch_status(moe::launch_expert_act_grad(g, p->dtype, s),
+                        "moe_expert_linear_backward"));
+    a.a = (const uint8_t*)ws;
+  }
+  if (grad_x != nullptr && p->num_rows > 0) {
+    a.b = (const uint8_t*)weight;
+    a.out = (uint8_t*)grad_x;
+    CHECK(launch_status(moe::launch_expert_grad_x(a, p->dtype, s),
+                        "moe_expert_linear_backward"));
+  }
+  if (grad_weight != nullptr) {
+    if (p->num_rows == 0) a.offsets = nullptr;      // R = 0: every expert's range is empty
+    a.b = (const uint8_t*)x;
+    a.out = (uint8_t*)grad_weight;
+    CHECK(launch_status(moe::launch_expert_grad_w(a, p->dtype, s),
+                        "moe_expert_linear_backward"));
+  }
+  return ok();
+}
+
+}  // extern "C"

@@ -1,0 +1,583 @@
+// Products of rows sorted by expert with the experts' own bf16, fp16 or fp32
+// weights, and their gradients:
+//
+//   out[r, :]  = F(x[r, :] W_e^T)                 e the expert of row r
+//   grad_x     = d W_e                            d = F' grad_out (act_grad_kernel)
+//   grad_W_e   = sum over the expert's rows of d[r, :]^T x[r, :]
+//
+// F is the identity or one of the layer's activations; a gated one takes the
+// first half of W's rows as gate and the second as up, and a block computes 16
+// (or 32) of each side by side, so that a wave holds both when it stores.
+//
+// One kernel, three forms: a block makes BM x BN of the result in registers
+// from LDS tiles of 128 bytes of the reduction, two of them in turn.  The MFMA's
+// A operand is the side of the result's columns and its B operand that of its
+// rows, so a lane holds four consecutive columns of one row.  An operand whose
+// memory runs along the reduction (x and W in out, d in grad_x) lies in LDS as
+// rows of 128 bytes and is read 16 bytes per lane; one whose memory runs along
+// the result (W in grad_x, both in grad_W) lies there as it comes and is read
+// transposed by ds_read_b64_tr_b16 (fp32: word by word).  Every product of the
+// 16-bit types is exact and sums are fp32; fp32 goes through the fp32 MFMA.
+#include <type_traits>
+
+#include "expert_act.h"
+#include "kernels.h"
+#include "lds_copy.h"
+#include "row_vec.h"
+
+namespace moe {
+
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
+constexpr uint32_t kOutOfRange = 0xF0000000u;   // past every buffer: reads as zeros
+constexpr int kRowB = 128;                      // bytes of the reduction per step
+
+enum Product { kOut, kGradX, kGradW };
+
+template <int BM_, int BN_, int WM_, int WN_, int PER_CU>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int NW = WM * WN, THREADS = 64 * NW;
+  static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;   // 16 x 16 tiles of a wave
+  static constexpr int WAVES_PER_EU = PER_CU * NW / 4 > 0 ? PER_CU * NW / 4 : 1;
+  static constexpr int STAGE = (BM + BN) * kRowB;
+  static_assert(TN % 2 == 0, "gate and up in one wave");
+};
+
+// 16-byte chunk c of LDS row r of an operand that runs along the reduction is
+// at chunk c ^ key_row(r): a fragment read's 16 rows hit distinct 16-byte bank
+// groups in each pass of 8 lanes (32 banks) and of 16 (64 banks).
+__device__ __forceinline__ int key_row(int r) { return (r & 6) | ((r ^ (r >> 3)) & 1); }
+// The same for one that runs along the result: row r is a step of the
+// reduction.  A transposed read's 16 lanes take 32 bytes of 4 rows, its four
+// groups rows 8 apart; fp32 reads 64 bytes of rows 4 apart.
+template <int DT>
+__device__ __forceinline__ int key_col(int r) {
+  return DT == kF32 ? ((r >> 2) & 3) << 2 : ((r & 3) | ((r >> 1) & 4)) << 1;
+}
+
+// Four registers of a fragment: 8 16-bit or 4 fp32 values along the reduction.
+template <int DT>
+__device__ __forceinline__ v4f mma(u32x4_t a, u32x4_t b, v4f c) {
+  if constexpr (DT == kBf16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a),
+                                                   __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+  } else if constexpr (DT == kF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a),
+                                                  __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  } else {
+    // lane group g holds values 4g .. 4g+3: each MFMA takes one of every group
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c,
+                                               0, 0, 0);
+    return c;
+  }
+}
+
+// The fragment of 16 rows (or columns) from `first` for step s of a stage:
+// lane l holds row first + l % 16, chunk 4s + l / 16 of the reduction.
+template <int DT, bool RED, int COLS>
+__device__ __forceinline__ u32x4_t fragment(const uint8_t* tile, int first, int s, int lane) {
+  const int i = lane & 15, g = lane >> 4;
+  if constexpr (!RED) {
+    const int r = first + i;
+    return *reinterpret_cast<const u32x4_t*>(tile + r * kRowB +
+                                             (((4 * s + g) ^ key_row(r)) << 4));
+  } else if constexpr (DT == kF32) {
+    u32x4_t v;
+    const int c = (first + i) >> 2, sub = ((first + i) & 3) << 2;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = 16 * s + 4 * g + j;
+      v[j] = *reinterpret_cast<const uint32_t*>(tile + r * (COLS * 4) +
+                                                ((c ^ key_col<DT>(r)) << 4) + sub);
+    }
+    return v;
+  } else {
+    // 16 lanes read 4 rows of 16 columns, 4 columns each, and get back 4 rows of
+    // one column; rows r and r + 4 have the same key
+    const int r = 32 * s + 8 * g + (i >> 2), c = (first >> 3) + ((i & 3) >> 1);
+    const uint8_t* p = tile + r * (COLS * 2) + ((c ^ key_col<DT>(r)) << 4) + ((i & 1) << 3);
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)p);
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * (COLS * 2)));
+    u32x4_t v;
+    v[0] = __builtin_bit_cast(uint2, lo).x;
+    v[1] = __builtin_bit_cast(uint2, lo).y;
+    v[2] = __builtin_bit_cast(uint2, hi).x;
+    v[3] = __builtin_bit_cast(uint2, hi).y;
+    return v;
+  }
+}
+
+// Rows [r0, r0 + n) of expert e.  Offsets that are not what the sort writes
+// give wrong rows, never rows outside [0, R).
+struct ExpertRange {
+  int r0, n;
+};
+__device__ __forceinline__ ExpertRange expert_range(const int32_t* off, int R, int e) {
+  if (off == nullptr) return ExpertRange{0, R};
+  const int a = min(max(off[e], 0), R), b = min(max(off[e + 1], a), R);
+  return ExpertRange{a, b - a};
+}
+
+// Block b's tile of `live` ones.  Consecutive blocks run on the 8 XCDs in turn;
+// each takes a run of consecutive tiles, whose operands its L2 then shares.
+// -1: none.
+__device__ __forceinline__ int64_t tile_of_block(int64_t b, int64_t live) {
+  const int64_t run = (live + 7) / 8, t = (b & 7) * run + (b >> 3);
+  return (b >> 3) < run && t < live ? t : -1;
+}
+
+// Tile t of mts x nts, walked in bands of 8 rows of tiles, down each band first.
+struct TileAt {
+  int m, n;
+};
+constexpr int kBand = 8;
+__device__ __forceinline__ TileAt tile_at(int64_t t, int mts, int nts) {
+  const int64_t per = (int64_t)kBand * nts;
+  const int band = (int)(t / per), rest = (int)(t - band * per);
+  const int h = min(kBand, mts - band * kBand);
+  return TileAt{band * kBand + rest % h, rest / h};
+}
+
+// The rows' tile for this block: the tiles of all experts with rows, in their
+// order, are the tile rows.  Every wave finds it for itself: a lane adds up the
+// tiles of E / 64 experts, a scan over the lanes gives the total and the lane
+// that holds the tile.
+struct RowTile {
+  int e, r0, n, m, nt;      // expert, its first row and rows, tile row in it, tile column
+  bool live;
+};
+template <int BM>
+__device__ __forceinline__ RowTile find_row_tile(const int32_t* off, int R, int E, int nts,
+                                                 int64_t block) {
+  RowTile t{0, 0, R, 0, 0, true};
+  if (off == nullptr) {
+    const int mts = (R + BM - 1) / BM;
+    const int64_t at = tile_of_block(block, (int64_t)mts * nts);
+    t.live = at >= 0;
+    if (!t.live) return t;
+    const TileAt w = tile_at(at, mts, nts);
+    t.m = w.m;
+    t.nt = w.n;
+    return t;
+  }
+  const int lane = threadIdx.x & 63, per = (E + 63) / 64;
+  const int e0 = min(lane * per, E), e1 = min(e0 + per, E);
+  int mine = 0;
+  for (int e = e0; e < e1; ++e) mine += (expert_range(off, R, e).n + BM - 1) / BM;
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(upto, d);
+    if (lane >= d) upto += v;
+  }
+  const int mts = __builtin_amdgcn_readlane(upto, 63);
+  const int64_t at = tile_of_block(block, (int64_t)mts * nts);
+  t.live = at >= 0;
+  if (!t.live) return t;
+  const TileAt w = tile_at(at, mts, nts);
+  t.nt = w.n;
+  // the lane whose tiles hold row w.m, then the expert among its own
+  const int owner = __builtin_ctzll(__ballot(w.m < upto));
+  int left = w.m - (upto - mine), he = 0, hr = 0, hn = 0;
+  for (int e = e0; e < e1; ++e) {
+    const ExpertRange r = expert_range(off, R, e);
+    const int tiles = (r.n + BM - 1) / BM;
+    if (left >= 0 && left < tiles) {
+      he = e;
+      hr = r.r0;
+      hn = r.n;
+      break;
+    }
+    left -= tiles;
+  }
+  t.e = __builtin_amdgcn_readlane(he, owner);
+  t.r0 = __builtin_amdgcn_readlane(hr, owner);
+  t.n = __builtin_amdgcn_readlane(hn, owner);
+  t.m = __builtin_amdgcn_readlane(left, owner);
+  return t;
+}
+
+// Where an operand's 16-byte chunks come from.  RED: LDS rows are steps of the
+// reduction and chunks run along the result's columns.
+template <int DT, bool RED, int ROWS, int THREADS>
+struct Slots {
+  static constexpr int ES = dtype_size(DT), CE = 16 / ES, BK = kRowB / ES;
+  static constexpr int CHUNKS = RED ? ROWS * ES / 16 : 8;     // of an LDS row
+  static constexpr int COUNT = ROWS * 8 / THREADS;            // per lane
+  static_assert(ROWS * 8 % THREADS == 0 && (!RED || CHUNKS >= 16), "whole instructions");
+  static __device__ __forceinline__ int row(int i) {
+    return (i * THREADS + (int)threadIdx.x) / CHUNKS;
+  }
+  static __device__ __forceinline__ int chunk(int i) {
+    const int r = row(i), pos = (int)threadIdx.x % CHUNKS;
+    return pos ^ (RED ? key_col<DT>(r) : key_row(r));
+  }
+};
+
+// A chunk at column col of a row of `limit` columns, at any address, zeros past
+// the end; in two steps, so that the load is in flight in between.
+template <int DT>
+__device__ __forceinline__ u32x4_t load_chunk(const uint8_t* row, int col, int limit) {
+  constexpr int CE = RowVec<DT>::N;
+  if (limit >= CE) return RowVec<DT>::template load<false>(row, col, limit);
+  float f[CE];
+#pragma unroll
+  for (int i = 0; i < CE; ++i) f[i] = col + i < limit ? RowVec<DT>::load_one(row, col + i) : 0.0f;
+  return RowVec<DT>::pack(f);
+}
+template <int DT>
+__device__ __forceinline__ void settle_chunk(u32x4_t& v, int col, int limit, bool live) {
+  if (!live || col >= limit) v = u32x4_t{0u, 0u, 0u, 0u};
+  else if (limit >= RowVec<DT>::N) RowVec<DT>::settle(v, col, limit);
+}
+
+template <int DT, Product P, class S, bool DIRECT, bool GATED>
+__global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kernel(
+    const ExpertGemmArgs p) {
+  constexpr int ES = dtype_size(DT), CE = 16 / ES, BK = kRowB / ES;
+  constexpr bool AR = P == kGradW, BR = P != kOut;
+  constexpr int BM = S::BM, BN = S::BN, TM = S::TM, TN = S::TN;
+  constexpr int WNC = TN * 16, OUTC = GATED ? BN / 2 : BN;     // result columns of a block
+  constexpr int PITCH = WNC + 4;                               // floats of an epilogue row
+  constexpr int EPI = S::NW * 16 * PITCH * 4;
+  constexpr int LDS = 2 * S::STAGE > EPI ? 2 * S::STAGE : EPI;
+  static_assert(LDS <= 160 * 1024, "LDS of a CU");
+  __shared__ __align__(1024) uint8_t lds[LDS];
+  typedef Slots<DT, AR, BM, S::THREADS> SA;
+  typedef Slots<DT, BR, BN, S::THREADS> SB;
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int ncols = P == kOut ? p.N : p.K;
+  const int nts = (ncols + OUTC - 1) / OUTC;
+
+  // this block's tile: result rows [m0, m0 + mrows) of the operand's, columns from n0
+  int e, L, mrows;
+  int64_t row0;                 // first result row in out (and of x or d where they are rows)
+  int n0;
+  const uint8_t *a, *b;         // the operands' first elements of the tile
+  int a_pitch, b_pitch;         // bytes
+  int64_t a_step, b_step;       // bytes per BK of the reduction
+  if constexpr (P == kGradW) {
+    const int mts = (p.wide + BM - 1) / BM;
+    const int64_t per = (int64_t)mts * nts;
+    const int64_t t = tile_of_block(block_index(), per * p.E);
+    if (t < 0) return;
+    e = (int)(t / per);
+    const TileAt at = tile_at(t - e * per, mts, nts);
+    const ExpertRange r = expert_range(p.offsets, p.R, e);
+    L = r.n;
+    n0 = at.n * OUTC;
+    row0 = at.m * BM;
+    mrows = min(BM, p.wide - at.m * BM);
+    a_pitch = p.wide * ES;
+    b_pitch = p.K * ES;
+    a = p.a + (int64_t)r.r0 * a_pitch + row0 * ES;
+    b = p.b + (int64_t)r.r0 * b_pitch + (int64_t)n0 * ES;
+    a_step = (int64_t)BK * a_pitch;
+    b_step = (int64_t)BK * b_pitch;
+  } else {
+    const RowTile t = find_row_tile<BM>(p.offsets, p.R, p.E, nts, block_index());
+    if (!t.live) return;
+    e = t.e;
+    n0 = t.nt * OUTC;
+    row0 = (int64_t)t.r0 + t.m * BM;
+    mrows = min(BM, t.n - t.m * BM);
+    L = P == kOut ? p.K : p.wide;
+    a_pitch = L * ES;
+    b_pitch = p.K * ES;
+    a = p.a + row0 * a_pitch;
+    b = p.b + (int64_t)e * p.wide * b_pitch +
+        (P == kOut ? (int64_t)n0 * b_pitch : (int64_t)n0 * ES);
+    a_step = kRowB;
+    b_step = P == kOut ? kRowB : (int64_t)BK * b_pitch;
+  }
+  // tile row j of W in out: its distance from the first one, or -1
+  auto weight_row = [&](int j) {
+    if (!GATED) return n0 + j < p.N ? j : -1;
+    const int w = j / WNC, q = j % WNC, c = w * (WNC / 2) + q % (WNC / 2);
+    return n0 + c < p.N ? (q < WNC / 2 ? c : p.N + c) : -1;
+  };
+  const int steps = (L + BK - 1) / BK;
+
+  uint32_t a_off[SA::COUNT], b_off[SB::COUNT];    // DIRECT: from the step's first element
+  if constexpr (DIRECT) {
+#pragma unroll
+    for (int i = 0; i < SA::COUNT; ++i) {
+      const int r = SA::row(i), c = SA::chunk(i);
+      const bool in = AR ? c * CE < mrows : r < mrows;
+      a_off[i] = in ? (uint32_t)r * a_pitch + c * 16 : kOutOfRange;
+    }
+#pragma unroll
+    for (int i = 0; i < SB::COUNT; ++i) {
+      const int r = SB::row(i), c = SB::chunk(i);
+      if (BR) {
+        b_off[i] = n0 + c * CE < ncols ? (uint32_t)r * b_pitch + c * 16 : kOutOfRange;
+      } else {
+        const int w = weight_row(r);
+        b_off[i] = w >= 0 ? (uint32_t)w * b_pitch + c * 16 : kOutOfRange;
+      }
+    }
+  }
+  u32x4_t a_reg[DIRECT ? 1 : SA::COUNT], b_reg[DIRECT ? 1 : SB::COUNT];
+  const uint32_t lds0 = lds_addr(lds);
+
+  // the step's tiles on their way: into LDS, or into registers
+  auto fetch = [&](int t) {
+    const uint8_t* at = a + t * a_step;
+    const uint8_t* bt = b + t * b_step;
+    const int left = L - t * BK;
+    if constexpr (DIRECT) {
+      const v4i ra = buffer_rsrc(at, kOutOfRange), rb = buffer_rsrc(bt, kOutOfRange);
+      const uint32_t to = lds0 + (t & 1) * S::STAGE + wave * 1024;
+#pragma unroll
+      for (int i = 0; i < SA::COUNT; ++i) {
+        const int k = AR ? SA::row(i) : SA::chunk(i) * CE;
+        dma16(ra, to + i * S::THREADS * 16, k < left ? a_off[i] : kOutOfRange);
+      }
+#pragma unroll
+      for (int i = 0; i < SB::COUNT; ++i) {
+        const int k = BR ? SB::row(i) : SB::chunk(i) * CE;
+        dma16(rb, to + BM * kRowB + i * S::THREADS * 16, k < left ? b_off[i] : kOutOfRange);
+      }
+    } else {
+      // rows that are not there load the first one's, which is, and are dropped
+#pragma unroll
+      for (int i = 0; i < SA::COUNT; ++i) {
+        const int r = SA::row(i), c = SA::chunk(i) * CE;
+        a_reg[i] = load_chunk<DT>(at + (int64_t)(r < (AR ? left : mrows) ? r : 0) * a_pitch, c,
+                                  AR ? mrows : left);
+      }
+#pragma unroll
+      for (int i = 0; i < SB::COUNT; ++i) {
+        const int r = SB::row(i), c = SB::chunk(i) * CE;
+        const int w = BR ? (r < left ? r : 0) : max(weight_row(r), 0);
+        b_reg[i] = load_chunk<DT>(bt + (int64_t)w * b_pitch, c, BR ? ncols - n0 : left);
+      }
+    }
+  };
+  auto settle = [&](int t) {
+    if constexpr (!DIRECT) {
+      const int left = L - t * BK;
+      uint8_t* to = lds + (t & 1) * S::STAGE + threadIdx.x * 16;
+#pragma unroll
+      for (int i = 0; i < SA::COUNT; ++i) {
+        const int r = SA::row(i), c = SA::chunk(i) * CE;
+        settle_chunk<DT>(a_reg[i], c, AR ? mrows : left, r < (AR ? left : mrows));
+        *reinterpret_cast<u32x4_t*>(to + i * S::THREADS * 16) = a_reg[i];
+      }
+#pragma unroll
+      for (int i = 0; i < SB::COUNT; ++i) {
+        const int r = SB::row(i), c = SB::chunk(i) * CE;
+        settle_chunk<DT>(b_reg[i], c, BR ? ncols - n0 : left,
+                         BR ? r < left : weight_row(r) >= 0);
+        *reinterpret_cast<u32x4_t*>(to + BM * kRowB + i * S::THREADS * 16) = b_reg[i];
+      }
+    }
+  };
+
+  v4f acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // One barrier per step: behind it this step's tiles are in LDS and the other
+  // pair, read in the step before, is free.
+  if (steps > 0) fetch(0);
+  for (int t = 0; t < steps; ++t) {
+    settle(t);
+    wait_then_barrier<0>();
+    if (t + 1 < steps) fetch(t + 1);
+    const uint8_t* ta = lds + (t & 1) * S::STAGE;
+    const uint8_t* tb = ta + BM * kRowB;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      u32x4_t fa[TM], fb[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        fb[j] = fragment<DT, BR, BN>(tb, wn * WNC + 16 * j, s, lane);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+        fa[i] = fragment<DT, AR, BM>(ta, (wm * TM + i) * 16, s, lane);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[j], fa[i], acc[i][j]);
+    }
+  }
+
+  // 16 rows at a time through the wave's own LDS, so that a lane stores 8
+  // consecutive columns and the activation's code is there once.
+  __syncthreads();
+  float* mine = reinterpret_cast<float*>(lds) + wave * 16 * PITCH;
+  const int64_t out_pitch = (int64_t)ncols * ES;
+  uint8_t* out = p.out + row0 * out_pitch;
+  if (P == kGradW) out += (int64_t)e * p.wide * out_pitch;
+  auto store8 = [&](uint8_t* row, int col, int limit, const float (&f)[8]) {
+#pragma unroll
+    for (int c = 0; c < 8; c += CE)
+      if (col + c < limit)
+        RowVec<DT>::template store<false>(row, col + c, limit, RowVec<DT>::pack(f + c));
+  };
+  for (int i = 0; i < TM; ++i) {
+    const int first = (wm * TM + i) * 16;
+    if (first >= mrows) break;
+    wave_lds_order();
+    with_constant<TM - 1>(i, [&](auto at) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        *reinterpret_cast<v4f*>(mine + (lane & 15) * PITCH + 16 * j + (lane >> 4) * 4) =
+            acc[decltype(at)::value][j];
+    });
+    wave_lds_order();
+    constexpr int LANES = WNC / (GATED ? 2 : 1) / 8;      // that share a row
+    for (int at = lane; at < 16 * LANES; at += 64) {
+      const int r = at / LANES, q = (at % LANES) * 8;
+      if (first + r >= mrows) continue;
+      float g[8], u[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        g[c] = mine[r * PITCH + q + c];
+        u[c] = GATED ? mine[r * PITCH + WNC / 2 + q + c] : 0.0f;
+      }
+      const int col = n0 + wn * (WNC / (GATED ? 2 : 1)) + q;
+      if (P == kOut && p.pre != nullptr) {
+        uint8_t* row = p.pre + (row0 + first + r) * (int64_t)p.wide * ES;
+        store8(row, col, p.N, g);
+        if (GATED) store8(row + (int64_t)p.N * ES, col, p.N, u);
+      }
+      if (P == kOut && p.act != kActNone) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) g[c] = apply_act(p.act, g[c], u[c], p.limit);
+      }
+      store8(out + (first + r) * out_pitch, col, ncols, g);
+    }
+  }
+}
+
+// d = F'(pre) grad_out for the rows of all experts; bound by HBM.
+constexpr int kActThreads = 256;
+
+template <class RV>
+__global__ __launch_bounds__(kActThreads) void act_grad_kernel(const ExpertActGradArgs p) {
+  constexpr int N = RV::N;
+  const int per = (p.N + N - 1) / N;
+  const int64_t at = (int64_t)block_index() * kActThreads + threadIdx.x;
+  const int64_t row = at / per;
+  const int rows = p.offsets == nullptr ? p.R : min(max(p.offsets[p.E], 0), p.R);
+  if (row >= rows) return;
+  const int col = (int)(at - row * per) * N;
+  const int wide = p.N * act_width(p.act);
+  const uint8_t* pre = p.pre + row * wide * RV::kSize;
+  uint8_t* d = p.d + row * wide * RV::kSize;
+  const bool gated = act_width(p.act) == 2;
+  typename RV::Raw gv = RV::template load<true>(pre, col, p.N), uv = {};
+  if (gated) uv = RV::template load<true>(pre + (int64_t)p.N * RV::kSize, col, p.N);
+  typename RV::Raw hv = RV::template load<true>(p.grad_out + row * p.N * RV::kSize, col, p.N);
+  RV::settle(gv, col, p.N);
+  RV::settle(uv, col, p.N);
+  RV::settle(hv, col, p.N);
+  float g[N], u[N], h[N];
+  RV::unpack(gv, g);
+  RV::unpack(uv, u);
+  RV::unpack(hv, h);
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const ActGrad r = act_grad(p.act, g[c], u[c], p.limit, h[c]);
+    g[c] = r.gate;
+    u[c] = r.up;
+  }
+  RV::template store<false>(d, col, p.N, RV::pack(g));
+  if (gated) RV::template store<false>(d + (int64_t)p.N * RV::kSize, col, p.N, RV::pack(u));
+}
+
+template <int DT, Product P, class S, bool GATED>
+hipError_t launch_shape(const ExpertGemmArgs& a, bool direct, hipStream_t stream) {
+  constexpr int OUTC = GATED ? S::BN / 2 : S::BN;
+  const int ncols = P == kOut ? a.N : a.K;
+  const int64_t nts = (ncols + OUTC - 1) / OUTC;
+  const int64_t mts = P == kGradW ? (int64_t)((a.wide + S::BM - 1) / S::BM) * a.E
+                      : a.offsets == nullptr ? (a.R + S::BM - 1) / S::BM
+                                             : a.R / S::BM + (a.E < a.R ? a.E : a.R);
+  const dim3 grid = grid_of((mts * nts + 7) / 8 * 8);
+  if (direct)
+    expert_gemm_kernel<DT, P, S, true, GATED><<<grid, S::THREADS, 0, stream>>>(a);
+  else
+    expert_gemm_kernel<DT, P, S, false, GATED><<<grid, S::THREADS, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int DT, Product P, bool GATED>
+hipError_t launch_gemm(const ExpertGemmArgs& a, bool direct, hipStream_t stream) {
+  if constexpr (P != kGradW) {
+    if (a.R <= 32 * (int64_t)a.E)
+      return launch_shape<DT, P, Tile<64, 128, 1, 4, 2>, GATED>(a, direct, stream);
+  }
+  return launch_shape<DT, P, Tile<128, 128, 2, 2, 2>, GATED>(a, direct, stream);
+}
+
+template <class F>
+hipError_t with_dtype(int dtype, F&& f) {
+  switch (dtype) {
+    case kBf16: return f(std::integral_constant<int, kBf16>());
+    case kF16: return f(std::integral_constant<int, kF16>());
+    default: return f(std::integral_constant<int, kF32>());
+  }
+}
+
+bool aligned16(const void* p, int64_t pitch) { return (((uintptr_t)p | pitch) & 15) == 0; }
+
+}  // namespace
+
+hipError_t launch_expert_out(const ExpertGemmArgs& a, int dtype, hipStream_t stream) {
+  const int64_t pitch = (int64_t)a.K * dtype_size(dtype);
+  const bool direct = aligned16(a.a, pitch) && aligned16(a.b, pitch);
+  return with_dtype(dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    return act_width(a.act) == 2 ? launch_gemm<DT, kOut, true>(a, direct, stream)
+                                 : launch_gemm<DT, kOut, false>(a, direct, stream);
+  });
+}
+
+hipError_t launch_expert_grad_x(const ExpertGemmArgs& a, int dtype, hipStream_t stream) {
+  const bool direct = aligned16(a.a, (int64_t)a.wide * dtype_size(dtype)) &&
+                      aligned16(a.b, (int64_t)a.K * dtype_size(dtype));
+  return with_dtype(dtype, [&](auto dt) {
+    return launch_gemm<decltype(dt)::value, kGradX, false>(a, direct, stream);
+  });
+}
+
+hipError_t launch_expert_grad_w(const ExpertGemmArgs& a, int dtype, hipStream_t stream) {
+  const bool direct = aligned16(a.a, (int64_t)a.wide * dtype_size(dtype)) &&
+                      aligned16(a.b, (int64_t)a.K * dtype_size(dtype));
+  return with_dtype(dtype, [&](auto dt) {
+    return launch_gemm<decltype(dt)::value, kGradW, false>(a, direct, stream);
+  });
+}
+
+hipError_t launch_expert_act_grad(const ExpertActGradArgs& a, int dtype, hipStream_t stream) {
+  return with_dtype(dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    auto go = [&](auto rv) {
+      typedef decltype(rv) RV;
+      const int64_t lanes = (int64_t)a.R * ((a.N + RV::N - 1) / RV::N);
+      act_grad_kernel<RV><<<grid_of((lanes + kActThreads - 1) / kActThreads), kActThreads, 0,
+                            stream>>>(a);
+      return hipGetLastError();
+    };
+    return a.N < RowVec<DT>::N ? go(RowOne<DT>()) : go(RowVec<DT>());
+  });
+}
+
+}  // namespace moe

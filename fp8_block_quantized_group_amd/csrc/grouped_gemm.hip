@@ -51,13 +51,13 @@
 
 #include "device_common.h"
 #include "kernels.h"
+#include "lds_copy.h"
 
 namespace moe {
 
 namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -65,7 +65,6 @@ typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int kRowBytes = 128;      // one k-step of a row: 128 fp8 values
 constexpr uint32_t kOutOfRange = 0xF0000000u;
-constexpr uint32_t kRsrcWord3 = 0x00020000u;   // raw buffer, 32-bit data format
 constexpr int kMaxGroups = 256;                // reduction length <= 32768
 #ifndef MOE_ZIP
 #define MOE_ZIP 16
@@ -143,16 +142,6 @@ __device__ __forceinline__ int key_w4(int r) {
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 
-// Wait until at most N of this wave's LDS-bound loads are in flight and its
-// own LDS reads have completed, then barrier.
-template <int N>
-__device__ __forceinline__ void wait_then_barrier() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(N) : "memory");
-#endif
-}
-
 // `after` = how many later k-steps (L loads each) may still be in flight.
 // L is per wave and per block (waves skip the loads of rows an expert does
 // not have), so it is dispatched to a compile-time immediate here.
@@ -191,22 +180,6 @@ __device__ __forceinline__ void stage_landed(int loads_per_stage, int after) {
   wait_stages_l<L>(after);
 }
 
-// Raw buffer resource over [base, base + num_records): offsets at or past
-// num_records read zeros.  Kept in SGPRs.
-__device__ __forceinline__ v4i buffer_rsrc(const void* base, uint32_t num_records) {
-  const uint64_t b = (uint64_t)base;
-  return v4i{__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
-             __builtin_amdgcn_readfirstlane((int)((b >> 32) & 0xFFFFu)),
-             __builtin_amdgcn_readfirstlane((int)num_records), (int)kRsrcWord3};
-}
-
-// HBM -> LDS: lane l's 16 (4) bytes at rsrc + voffset land at lds + 16*l (4*l).
-__device__ __forceinline__ void dma16(v4i rsrc, uint32_t lds, uint32_t voffset) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               ::"s"(lds), "v"(voffset), "s"(rsrc) : "memory", "m0");
-#endif
-}
 // Weight tiles.  stream (wave-uniform): no other block reads this tile, so
 // the copy carries the non-temporal hint and leaves L2 to the tiles that
 // are shared (activation rows, the weight tiles of multi-tile groups).
@@ -230,20 +203,6 @@ __device__ __forceinline__ void dma4(v4i rsrc, uint32_t lds, uint32_t voffset) {
 #endif
 }
 #pragma clang diagnostic pop
-
-// f(integral_constant<int, v>) for a wave-uniform v in [0, N].
-template <int N, class F>
-__device__ __forceinline__ void with_constant(int v, F&& f) {
-  if constexpr (N > 0) {
-    if (v == N) {
-      f(std::integral_constant<int, N>{});
-      return;
-    }
-    with_constant<N - 1>(v, f);
-  } else {
-    f(std::integral_constant<int, 0>{});
-  }
-}
 
 // bf16 activation rows (256 bytes per k-step): the row is stored as two
 // 128-byte virtual rows v = 2r + bit 2 of the chunk, chunk
@@ -276,10 +235,6 @@ __device__ __forceinline__ int wsc_rot(int n) {
 }
 __device__ __forceinline__ int wsc_unrot(int pos) {
   return (pos & ~15) | ((pos - 4 * ((pos >> 4) & 3)) & 15);
-}
-
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
 }
 
 // ACT (w13 only): the block's 256 weight rows are the gate rows j0 + [0, 128)

@@ -304,4 +304,29 @@ int norm_grad_parts(int64_t T, int H, int dtype);
 hipError_t launch_norm_grad(const NormGradArgs& a, int dtype, bool w32, float* g_pre,
                             float* g_post, float* g_gate, hipStream_t stream);
 
+// The experts' own products (expert_gemm.hip).
+struct ExpertGemmArgs {
+  const uint8_t* a;            // out: x [R, K]; gradients: d [R, wide]
+  const uint8_t* b;            // out, grad_x: W [E, wide, K]; grad_w: x
+  uint8_t* out;                // [R, N], [R, K] or [E, wide, K]
+  uint8_t* pre;                // out: [R, wide] or nullptr
+  const int32_t* offsets;      // [E + 1], or nullptr: one expert has all rows
+  int R, K, N, wide, E;        // wide: columns before the activation, N or 2N
+  int act;                     // moe_act_t or kActNone; out only
+  float limit;
+};
+hipError_t launch_expert_out(const ExpertGemmArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_expert_grad_x(const ExpertGemmArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_expert_grad_w(const ExpertGemmArgs& a, int dtype, hipStream_t stream);
+
+struct ExpertActGradArgs {
+  const uint8_t* pre;          // [R, wide]
+  const uint8_t* grad_out;     // [R, N]
+  uint8_t* d;                  // [R, wide]
+  const int32_t* offsets;
+  int R, N, E, act;
+  float limit;
+};
+hipError_t launch_expert_act_grad(const ExpertActGradArgs& a, int dtype, hipStream_t stream);
+
 }  // namespace moe

@@ -115,6 +115,7 @@ typedef enum {
  * SWIGLUOAI: (clamp(up, -L, L) + 1) * g' * sigmoid(1.702 g'), g' = min(g, L);
  * for the last two act_limit 0 means L = 7. */
 typedef enum {
+  MOE_ACT_NONE = -1,       /* moe_expert_linear* only: the product itself    */
   MOE_ACT_SILU = 0,
   MOE_ACT_GELU = 1,
   MOE_ACT_GELU_TANH = 2,
@@ -652,6 +653,61 @@ moe_status_t moe_block_norm_backward(const moe_block_norm_t* p, const void* resi
                                      void* grad_y, float* grad_pre_weight,
                                      float* grad_post_weight, void* grad_gate, void* ws,
                                      size_t ws_bytes, void* stream);
+
+/* ---- The experts' own products ---------------------------------------------
+ * Linear layers of rows sorted by expert (moe_permute's rows and
+ * expert_offsets) with weights of the rows' own type: what stands between
+ * moe_permute and moe_unpermute in training, or serves a dense or shared
+ * expert (one expert, no offsets).  The conventions of the calls around the
+ * layer hold: any width, any element's address, fp32 sums, one rounding on
+ * the way out, results that do not depend on timing.  A row's bits may change
+ * with the batch's size (another tile adds in another order). */
+
+/* One linear layer (host struct).  Requirements: num_rows >= 0; 1 <=
+ * in_features, out_features <= 32768; 1 <= num_experts <= 1024; one expert's
+ * weights under 3.75 GiB; fewer than 2^31 tiles of 64 x 64 results. */
+typedef struct {
+  int32_t num_rows;
+  int32_t in_features;
+  int32_t out_features; /* columns of out                                    */
+  int32_t num_experts;
+  int32_t dtype;        /* moe_dtype_t of rows, weights and gradients        */
+  int32_t activation;   /* moe_act_t; MOE_ACT_NONE: the product itself       */
+  float act_limit;      /* as in moe_problem_t                               */
+} moe_expert_linear_t;
+
+/* out[r, :] = F(x[r, :] W_e^T) for the rows r of every expert e,
+ * [expert_offsets[e], expert_offsets[e+1]).  x [R, in], weight [E, wide, in],
+ * out [R, out]; wide is 2 * out_features for a gated activation (gate rows
+ * first) and out_features otherwise.  pre_act [R, wide] or NULL: the product
+ * before F, rounded to dtype, which the gradient takes (F itself is applied
+ * before that rounding).  expert_offsets int32 [E+1], ascending from 0 (what
+ * is not, is cut to [0, R]; such calls give wrong rows, never an access out
+ * of bounds), or NULL with one expert: it has all rows.  Rows from
+ * expert_offsets[E] on stay as they were. */
+moe_status_t moe_expert_linear(const moe_expert_linear_t* p, const void* x,
+                               const int32_t* expert_offsets, const void* weight, void* out,
+                               void* pre_act, void* stream);
+
+/* Device scratch bytes of moe_expert_linear_backward (host only; 0 without an
+ * activation): the pre-activations' gradient, [R, wide] in dtype. */
+moe_status_t moe_expert_linear_workspace_size(const moe_expert_linear_t* p, size_t* bytes);
+
+/* With d = grad_out F'(pre_act), rounded to dtype (grad_out itself without an
+ * activation; the products take their operands in that type):
+ *   grad_x[r, :]    = d[r, :] W_e                     [R, in]
+ *   grad_weight[e]  = sum over e's rows of d[r, :]^T x[r, :]   [E, wide, in]
+ * Either may be NULL.  Experts without rows get a grad_weight of zeros, also
+ * with R = 0.  A clamp passes its gradient up to and at the limit.  pre_act
+ * must be NULL exactly when there is no activation; x is needed for
+ * grad_weight, weight for grad_x.  ws: device scratch of
+ * moe_expert_linear_workspace_size bytes, 16-byte aligned (NULL when that is
+ * 0); calls sharing one must not overlap. */
+moe_status_t moe_expert_linear_backward(const moe_expert_linear_t* p, const void* x,
+                                        const int32_t* expert_offsets, const void* weight,
+                                        const void* pre_act, const void* grad_out, void* grad_x,
+                                        void* grad_weight, void* ws, size_t ws_bytes,
+                                        void* stream);
 
 /* Message of the last failed call on this thread ("" if none).  The
  * argument errors it describes follow the ValueError conditions of

@@ -1,0 +1,117 @@
+"""Refusals of the experts' own products, without a GPU: the C ABI checks
+every argument before anything is enqueued (the pointers here are not
+addresses of anything), the Python binding the shapes, types and devices."""
+import copy
+import ctypes
+import os
+import pickle
+
+import pytest
+import torch
+
+import fp8_block_quantized_group_amd as moe
+
+V = ctypes.c_void_p(1 << 20)
+ODD = ctypes.c_void_p((1 << 20) + 1)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(moe.LIB_PATH):
+        from fp8_block_quantized_group_amd import build
+        build.build()
+    return moe.load_library()
+
+
+def refused(lib, status, want, word):
+    assert status == want, (status, lib.moe_last_error())
+    assert word in lib.moe_last_error().decode(), lib.moe_last_error()
+
+
+SIZES = [
+    (dict(num_rows=-1), -1, "num_rows"), (dict(in_features=0), -2, "in_features"),
+    (dict(in_features=32769), -2, "in_features"), (dict(out_features=0), -2, "out_features"),
+    (dict(out_features=32769), -2, "out_features"), (dict(num_experts=0), -2, "num_experts"),
+    (dict(num_experts=1025), -2, "num_experts"), (dict(act_limit=-1.0), -1, "act_limit"),
+    (dict(act_limit=float("nan")), -1, "act_limit"),
+    (dict(act_limit=float("inf")), -1, "act_limit"),
+    (dict(activation="none", act_limit=1.0), -2, "clamp"),
+    (dict(activation="gelu", act_limit=1.0), -2, "clamp"),
+    (dict(num_rows=(1 << 31) - 1, in_features=32768), -2, "tiles")]
+
+
+@pytest.mark.parametrize("kw,status,word", SIZES + [
+    (dict(in_features=32768, out_features=32768, dtype=torch.float32), -2, "3.75 GiB"),
+    (dict(in_features=32768, out_features=32768, activation="silu"), -2, "3.75 GiB")])
+def test_linear_problems(lib, kw, status, word):
+    p = moe.ExpertLinear(**{**dict(num_rows=4, in_features=64, out_features=32, num_experts=2,
+                                   activation="silu"), **kw})
+    refused(lib, lib.moe_expert_linear(p._ref, V, V, V, V, V, None), status, word)
+    refused(lib, lib.moe_expert_linear_backward(p._ref, *[V] * 8, 1 << 40, None), status, word)
+    n = ctypes.c_size_t()
+    refused(lib, lib.moe_expert_linear_workspace_size(p._ref, ctypes.byref(n)), status, word)
+
+
+def test_linear_arguments(lib):
+    p = moe.ExpertLinear(4, 64, 32, 2, activation="silu")
+    fwd, bwd = lib.moe_expert_linear, lib.moe_expert_linear_backward
+    refused(lib, fwd(None, V, V, V, V, V, None), -1, "expert linear")
+    for i, word in enumerate(("x", "expert_offsets", "weight", "out")):
+        args = [V] * 5
+        args[i] = None
+        refused(lib, fwd(p._ref, *args, None), -1, word + " is NULL")
+        args[i] = ODD
+        refused(lib, fwd(p._ref, *args, None), -1, word)
+    refused(lib, fwd(p._ref, V, V, V, V, ODD, None), -1, "pre_act")
+    n = moe.expert_linear_workspace_size(p)
+    assert n >= 4 * 64 * 2
+    refused(lib, bwd(None, *[V] * 8, n, None), -1, "expert linear")
+    # x, offsets, weight, pre_act, grad_out, grad_x, grad_weight, ws
+    for i, word in ((0, "x"), (1, "expert_offsets"), (2, "weight"), (3, "pre_act"),
+                    (4, "grad_out"), (7, "ws")):
+        args = [V] * 8
+        args[i] = None
+        refused(lib, bwd(p._ref, *args, n, None), -1, word + " is NULL")
+    for i, word in ((5, "grad_x"), (6, "grad_weight"), (7, "ws")):
+        args = [V] * 8
+        args[i] = ODD
+        refused(lib, bwd(p._ref, *args, n, None), -1, word)
+    refused(lib, bwd(p._ref, *[V] * 8, n - 1, None), -3, "workspace")
+    plain = moe.ExpertLinear(4, 64, 32, 2)
+    assert moe.expert_linear_workspace_size(plain) == 0
+    refused(lib, bwd(plain._ref, *[V] * 8, 0, None), -1, "pre_act")
+    refused(lib, lib.moe_expert_linear_workspace_size(p._ref, None), -1, "bytes")
+    empty = moe.ExpertLinear(0, 64, 32, 2, activation="silu")
+    assert fwd(empty._ref, *[None] * 6) == 0
+    assert bwd(empty._ref, *[None] * 8, 0, None) == 0
+    refused(lib, bwd(empty._ref, *[None] * 6, ODD, None, 0, None), -1, "grad_weight")
+    bad = moe._ExpertLinear(4, 64, 32, 2, 3, 0, 0.0)
+    refused(lib, fwd(ctypes.byref(bad), V, V, V, V, V, None), -1, "dtype")
+    for act in (-2, 9):
+        bad = moe._ExpertLinear(4, 64, 32, 2, 0, act, 0.0)
+        refused(lib, fwd(ctypes.byref(bad), V, V, V, V, V, None), -1, "activation")
+
+
+def test_the_layer_still_needs_an_activation(lib):
+    """MOE_ACT_NONE belongs to the linear layers alone."""
+    p = moe.Problem(16, 256, 512, 4, 2, activation=-1)
+    with pytest.raises(moe.MoeError, match="activation"):
+        moe.workspace_size(p)
+
+
+def test_linear_binding():
+    with pytest.raises(ValueError, match="activation"):
+        moe.ExpertLinear(4, 64, 32, activation="relu")
+    with pytest.raises(ValueError, match="dtype"):
+        moe.ExpertLinear(4, 64, 32, dtype=torch.float64)
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.ExpertLinear(1 << 32, 64, 32)
+    p = moe.ExpertLinear(4, 64, 32, 2, activation="swiglustep", act_limit=2.0)
+    assert p.wide == 64 and moe.ExpertLinear(4, 64, 32, activation="gelu_no_mul").wide == 32
+    for q in (copy.deepcopy(p), pickle.loads(pickle.dumps(p))):
+        assert q == p and q.wide == 64
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        moe.expert_linear(p, x, x, x)
+    with pytest.raises(ValueError, match="GPU"):
+        moe.expert_linear_backward(p, x, x, x)
