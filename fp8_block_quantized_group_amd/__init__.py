@@ -67,6 +67,11 @@ class _ExpertLinear(ctypes.Structure):
         ("act_limit", ctypes.c_float)]
 
 
+class _ExpertLinearW4(ctypes.Structure):
+    _fields_ = _ExpertLinear._fields_ + [(n, ctypes.c_int32) for n in (
+        "format", "group_size", "scale_dtype")]
+
+
 class _Eplb(ctypes.Structure):
     _fields_ = [("logical_to_physical", ctypes.c_void_p), ("map_stride", ctypes.c_int32),
                 ("replica_count", ctypes.c_void_p), ("num_logical", ctypes.c_int32),
@@ -100,7 +105,7 @@ EXPORTS = ("moe_routing_sizes", "moe_stage_workspace_size", "moe_workspace_size"
            "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
            "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward",
            "moe_expert_linear", "moe_expert_linear_workspace_size",
-           "moe_expert_linear_backward")
+           "moe_expert_linear_backward", "moe_expert_linear_w4")
 
 _lib = None
 
@@ -150,6 +155,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_expert_linear.argtypes = [P(_ExpertLinear)] + [V] * 6
     lib.moe_expert_linear_workspace_size.argtypes = [P(_ExpertLinear), P(S)]
     lib.moe_expert_linear_backward.argtypes = [P(_ExpertLinear)] + [V] * 8 + [S, V]
+    lib.moe_expert_linear_w4.argtypes = [P(_ExpertLinearW4)] + [V] * 7
     lib.moe_last_error.argtypes = []
     for name in EXPORTS:
         fn = getattr(lib, name)
@@ -807,6 +813,56 @@ def expert_linear_backward(p: ExpertLinear, x, weight, grad_out, grad_x=None, gr
          _arg(pre_act, "pre_act", dt, (R, p.wide), d),
          _arg(grad_out, "grad_out", dt, (R, N), d), _arg(grad_x, "grad_x", dt, (R, K), d),
          _arg(grad_weight, "grad_weight", dt, shape, d), wp, wn)
+
+
+W4_FORMATS = ("int4", "int4_zero", "mxfp4")                            # moe_w4_t
+
+
+@dataclass(frozen=True)
+class ExpertLinearW4(_Descriptor):
+    """moe_expert_linear_w4_t: the same with 4-bit weights and group scales."""
+    num_rows: int
+    in_features: int
+    out_features: int
+    num_experts: int = 1
+    dtype: torch.dtype = torch.bfloat16
+    activation: str = "none"
+    act_limit: float = 0.0
+    format: str = "int4"                            # "int4" | "int4_zero" | "mxfp4"
+    group_size: int = 128
+    scale_dtype: Optional[torch.dtype] = None       # None: dtype; mxfp4: uint8
+
+    def _struct(self):
+        mx = self.format == "mxfp4"
+        if mx and self.scale_dtype not in (None, torch.uint8):
+            raise ValueError(f"mxfp4 scales are torch.uint8, got {self.scale_dtype}")
+        scale = self.dtype if mx or self.scale_dtype is None else self.scale_dtype
+        return _ExpertLinearW4(self.num_rows, self.in_features, self.out_features,
+                               self.num_experts, _choice(self.dtype, _DTYPES, "dtype"),
+                               _choice(self.activation, _LINEAR_ACTS, "activation"),
+                               self.act_limit, _choice(self.format, W4_FORMATS, "format"),
+                               self.group_size, _choice(scale, _DTYPES, "scale_dtype"))
+
+    def __post_init__(self):
+        super().__post_init__()
+        wide = self.out_features * (1 if self.activation in _SINGLE_ACTS else 2)
+        scales = torch.uint8 if self.format == "mxfp4" else self.scale_dtype or self.dtype
+        object.__setattr__(self, "wide", wide)
+        object.__setattr__(self, "scales", scales)  # the scales' type
+
+
+def expert_linear_w4(p: ExpertLinearW4, x, codes, scales, out, expert_offsets=None, zeros=None):
+    """moe_expert_linear_w4: out = F(x W_e^T) with W_e from 4-bit codes uint8
+    [E, wide, in / 2] and scales (and zeros uint8) [E, wide, in / group_size]."""
+    d = _device(x, "x")
+    R, K, E, dt = p.num_rows, p.in_features, p.num_experts, p.dtype
+    groups = (E, p.wide, K // p.group_size if p.group_size > 0 else 0)
+    _run(load_library().moe_expert_linear_w4, d, p._ref, _arg(x, "x", dt, (R, K), d),
+         _offsets(p, expert_offsets, d),
+         _arg(codes, "codes", torch.uint8, (E, p.wide, K // 2), d),
+         _arg(scales, "scales", p.scales, groups, d),
+         _arg(zeros, "zeros", torch.uint8, groups, d),
+         _arg(out, "out", dt, (R, p.out_features), d))
 
 
 class MoeBlock:

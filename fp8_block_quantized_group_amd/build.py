@@ -3,7 +3,7 @@
     python -m fp8_block_quantized_group_amd.build
 
 Each source compiles to its own object (the grouped GEMM once per scale
-scheme), in parallel, and the objects link into one shared library.
+scheme, the 4-bit products once per row type), in parallel, and the objects link into one shared library.
 """
 import os
 import subprocess
@@ -21,6 +21,8 @@ SOURCES = ["moe_api.hip", "quant_kernels.hip", "route_kernels.hip", "reduce_kern
 # the grouped GEMM's scale schemes (kQuantUe8m0, kQuantF32, kQuantBf16,
 # kQuantMxfp8, kSchemeMxfp8W4)
 GEMM_SCHEMES = [0, 1, 2, 3, 4]
+# the 4-bit products' row types (moe_dtype_t)
+W4_DTYPES = [0, 1, 2]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -50,6 +52,10 @@ def build(verbose: bool = False, extra_flags=(), lib: str = LIB) -> str:
         obj = os.path.join(OBJ_DIR, f"grouped_gemm_s{sc}.o")
         jobs.append([HIPCC, *FLAGS, *extra_flags, f"-DMOE_GEMM_SCHEME={sc}", "-c",
                      os.path.join(CSRC, "grouped_gemm.hip"), "-o", obj])
+    for dt in W4_DTYPES:
+        obj = os.path.join(OBJ_DIR, f"expert_w4_d{dt}.o")
+        jobs.append([HIPCC, *FLAGS, *extra_flags, f"-DMOE_W4_DTYPE={dt}", "-c",
+                     os.path.join(CSRC, "expert_w4.hip"), "-o", obj])
     workers = max(1, min(len(jobs), os.cpu_count() or 1, 16))
     with ThreadPoolExecutor(workers) as ex:
         results = list(ex.map(_run, jobs))

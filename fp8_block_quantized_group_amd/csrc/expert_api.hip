@@ -47,9 +47,9 @@ moe_status_t check_sizes(int rows, int in, int out, int experts, int dtype, int 
   if (limit > 0.0f && act != MOE_ACT_SILU && act != MOE_ACT_SWIGLUOAI &&
       act != MOE_ACT_SWIGLUSTEP)
     return fail(MOE_ERR_UNSUPPORTED, "activation %d takes no clamp limit", act);
-  // launches count their tiles in 31 bits
-  const int64_t m = (int64_t)rows / 64 + std::min(rows, experts);
-  const int64_t n = (std::max(in, wide_of(out, act)) + 63) / 64;
+  // launches count their tiles, of at least 16 x 16 results, in 31 bits
+  const int64_t m = (int64_t)rows / 16 + std::min(rows, experts);
+  const int64_t n = (std::max(in, wide_of(out, act)) + 15) / 16;
   if (m * n >= (int64_t)1 << 31)
     return fail(MOE_ERR_UNSUPPORTED, "%d rows of %d columns are more than 2^31 tiles", rows,
                 std::max(in, out));
@@ -93,6 +93,25 @@ moe::ExpertGemmArgs gemm_args(const moe_expert_linear_t* p, const int32_t* offse
   a.act = p->activation;
   a.limit = limit_of(p->activation, p->act_limit);
   return a;
+}
+
+moe_status_t check_w4(const moe_expert_linear_w4_t* p) {
+  if (p == nullptr) return fail(MOE_ERR_INVALID_ARG, "expert linear is NULL");
+  CHECK(check_sizes(p->num_rows, p->in_features, p->out_features, p->num_experts, p->dtype,
+                    p->activation, p->act_limit));
+  if (p->format < MOE_W4_INT4 || p->format > MOE_W4_MXFP4)
+    return fail(MOE_ERR_INVALID_ARG, "unknown 4-bit format %d", p->format);
+  if (p->group_size != 32 && p->group_size != 64 && p->group_size != 128)
+    return fail(MOE_ERR_UNSUPPORTED, "group_size must be 32, 64 or 128, got %d", p->group_size);
+  if (p->format == MOE_W4_MXFP4 && p->group_size != 32)
+    return fail(MOE_ERR_UNSUPPORTED, "MXFP4 groups are 32 columns, got %d", p->group_size);
+  if (p->in_features % p->group_size != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "group_size %d does not divide in_features %d",
+                p->group_size, p->in_features);
+  if (p->format != MOE_W4_MXFP4 && p->scale_dtype != p->dtype && p->scale_dtype != MOE_DT_F32)
+    return fail(MOE_ERR_UNSUPPORTED, "scale_dtype must be dtype or fp32, got %d",
+                p->scale_dtype);
+  return MOE_OK;
 }
 
 }  // namespace
@@ -184,6 +203,47 @@ moe_status_t moe_expert_linear_backward(const moe_expert_linear_t* p, const void
                         "moe_expert_linear_backward"));
   }
   return ok();
+}
+
+moe_status_t moe_expert_linear_w4(const moe_expert_linear_w4_t* p, const void* x,
+                                  const int32_t* expert_offsets, const void* codes,
+                                  const void* scales, const void* zeros, void* out,
+                                  void* stream) {
+  CHECK(check_w4(p));
+  if (p->num_rows == 0) return ok();
+  const bool mx = p->format == MOE_W4_MXFP4;
+  CHECK(check_ptr(x, "x", elem(p->dtype)));
+  CHECK(check_offsets(expert_offsets, p->num_experts));
+  CHECK(check_ptr(codes, "codes", 1));
+  CHECK(check_ptr(scales, "scales", mx ? 1 : elem(p->scale_dtype)));
+  if (p->format == MOE_W4_INT4_ZERO) {
+    CHECK(check_ptr(zeros, "zeros", 1));
+  } else if (zeros != nullptr) {
+    return fail(MOE_ERR_INVALID_ARG, "zeros given for a format without them");
+  }
+  CHECK(check_ptr(out, "out", elem(p->dtype)));
+  moe::ExpertW4Args a{};
+  a.x = (const uint8_t*)x;
+  a.codes = (const uint8_t*)codes;
+  a.scales = (const uint8_t*)scales;
+  a.zeros = (const uint8_t*)zeros;
+  a.out = (uint8_t*)out;
+  a.offsets = expert_offsets;
+  a.R = p->num_rows;
+  a.K = p->in_features;
+  a.N = p->out_features;
+  a.wide = wide_of(p->out_features, p->activation);
+  a.E = p->num_experts;
+  a.act = p->activation;
+  a.format = p->format;
+  a.group = p->group_size;
+  a.limit = limit_of(p->activation, p->act_limit);
+  const hipStream_t s = (hipStream_t)stream;
+  const bool s32 = p->scale_dtype == MOE_DT_F32;
+  const hipError_t err = p->dtype == MOE_DT_BF16  ? moe::launch_expert_w4_dt<0>(a, s32, s)
+                         : p->dtype == MOE_DT_F16 ? moe::launch_expert_w4_dt<1>(a, s32, s)
+                                                  : moe::launch_expert_w4_dt<2>(a, s32, s);
+  return launch_status(err, "moe_expert_linear_w4");
 }
 
 }  // extern "C"

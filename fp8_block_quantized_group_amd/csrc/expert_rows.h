@@ -1,0 +1,107 @@
+// Which expert and which of its rows a block works on, for the kernels over rows
+// sorted by expert.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+// Rows [r0, r0 + n) of expert e.  Offsets that are not what the sort writes
+// give wrong rows, never rows outside [0, R).
+struct ExpertRange {
+  int r0, n;
+};
+__device__ __forceinline__ ExpertRange expert_range(const int32_t* off, int R, int e) {
+  if (off == nullptr) return ExpertRange{0, R};
+  const int a = min(max(off[e], 0), R), b = min(max(off[e + 1], a), R);
+  return ExpertRange{a, b - a};
+}
+
+// Block b's tile of `live` ones.  Consecutive blocks run on the 8 XCDs in turn;
+// each takes a run of consecutive tiles, whose operands its L2 then shares.
+// -1: none.
+__device__ __forceinline__ int64_t tile_of_block(int64_t b, int64_t live) {
+  const int64_t run = (live + 7) / 8, t = (b & 7) * run + (b >> 3);
+  return (b >> 3) < run && t < live ? t : -1;
+}
+
+// Tile t of mts x nts, walked in bands of 8 rows of tiles, down each band first.
+struct TileAt {
+  int m, n;
+};
+constexpr int kBand = 8;
+__device__ __forceinline__ TileAt tile_at(int64_t t, int mts, int nts) {
+  const int64_t per = (int64_t)kBand * nts;
+  const int band = (int)(t / per), rest = (int)(t - band * per);
+  const int h = min(kBand, mts - band * kBand);
+  return TileAt{band * kBand + rest % h, rest / h};
+}
+
+// The rows' tile for this block: the tiles of all experts with rows, in their
+// order, are the tile rows.  Every wave finds it for itself: a lane adds up the
+// tiles of E / 64 experts, a scan over the lanes gives the total and the lane
+// that holds the tile.
+struct RowTile {
+  int e, r0, n, m, nt;      // expert, its first row and rows, tile row in it, tile column
+  bool live;
+};
+template <int BM>
+__device__ __forceinline__ RowTile find_row_tile(const int32_t* off, int R, int E, int nts,
+                                                 int64_t block) {
+  RowTile t{0, 0, R, 0, 0, true};
+  if (off == nullptr) {
+    const int mts = (R + BM - 1) / BM;
+    const int64_t at = tile_of_block(block, (int64_t)mts * nts);
+    t.live = at >= 0;
+    if (!t.live) return t;
+    const TileAt w = tile_at(at, mts, nts);
+    t.m = w.m;
+    t.nt = w.n;
+    return t;
+  }
+  const int lane = threadIdx.x & 63, per = (E + 63) / 64;
+  const int e0 = min(lane * per, E), e1 = min(e0 + per, E);
+  int mine = 0;
+  for (int e = e0; e < e1; ++e) mine += (expert_range(off, R, e).n + BM - 1) / BM;
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(upto, d);
+    if (lane >= d) upto += v;
+  }
+  const int mts = __builtin_amdgcn_readlane(upto, 63);
+  const int64_t at = tile_of_block(block, (int64_t)mts * nts);
+  t.live = at >= 0;
+  if (!t.live) return t;
+  const TileAt w = tile_at(at, mts, nts);
+  t.nt = w.n;
+  // the lane whose tiles hold row w.m, then the expert among its own
+  const int owner = __builtin_ctzll(__ballot(w.m < upto));
+  int left = w.m - (upto - mine), he = 0, hr = 0, hn = 0;
+  for (int e = e0; e < e1; ++e) {
+    const ExpertRange r = expert_range(off, R, e);
+    const int tiles = (r.n + BM - 1) / BM;
+    if (left >= 0 && left < tiles) {
+      he = e;
+      hr = r.r0;
+      hn = r.n;
+      break;
+    }
+    left -= tiles;
+  }
+  t.e = __builtin_amdgcn_readlane(he, owner);
+  t.r0 = __builtin_amdgcn_readlane(hr, owner);
+  t.n = __builtin_amdgcn_readlane(hn, owner);
+  t.m = __builtin_amdgcn_readlane(left, owner);
+  return t;
+}
+
+// Tile rows of BM that `rows` rows of `experts` experts can have at most.
+template <int BM>
+inline int64_t most_row_tiles(const int32_t* offsets, int rows, int experts) {
+  if (offsets == nullptr) return (rows + BM - 1) / BM;
+  return rows / BM + (experts < rows ? experts : rows);
+}
+
+}  // namespace moe

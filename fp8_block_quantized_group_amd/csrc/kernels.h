@@ -329,4 +329,22 @@ struct ExpertActGradArgs {
 };
 hipError_t launch_expert_act_grad(const ExpertActGradArgs& a, int dtype, hipStream_t stream);
 
+// Rows sorted by expert times 4-bit weights (expert_w4.hip).
+constexpr int kW4Int4 = 0, kW4Int4Zero = 1, kW4Mxfp4 = 2;     // match moe_w4_t
+struct ExpertW4Args {
+  const uint8_t* x;            // [R, K]
+  const uint8_t* codes;        // [E, wide, K / 2]
+  const uint8_t* scales;       // [E, wide, K / group]
+  const uint8_t* zeros;        // the same, or nullptr
+  uint8_t* out;                // [R, N]
+  const int32_t* offsets;
+  int R, K, N, wide, E, act, format, group;
+  float limit;
+};
+template <int DT>
+hipError_t launch_expert_w4_dt(const ExpertW4Args& a, bool s32, hipStream_t stream);
+extern template hipError_t launch_expert_w4_dt<0>(const ExpertW4Args&, bool, hipStream_t);
+extern template hipError_t launch_expert_w4_dt<1>(const ExpertW4Args&, bool, hipStream_t);
+extern template hipError_t launch_expert_w4_dt<2>(const ExpertW4Args&, bool, hipStream_t);
+
 }  // namespace moe

@@ -665,7 +665,7 @@ moe_status_t moe_block_norm_backward(const moe_block_norm_t* p, const void* resi
 
 /* One linear layer (host struct).  Requirements: num_rows >= 0; 1 <=
  * in_features, out_features <= 32768; 1 <= num_experts <= 1024; one expert's
- * weights under 3.75 GiB; fewer than 2^31 tiles of 64 x 64 results. */
+ * weights under 3.75 GiB; fewer than 2^31 tiles of 16 x 16 results. */
 typedef struct {
   int32_t num_rows;
   int32_t in_features;
@@ -708,6 +708,41 @@ moe_status_t moe_expert_linear_backward(const moe_expert_linear_t* p, const void
                                         const void* pre_act, const void* grad_out, void* grad_x,
                                         void* grad_weight, void* ws, size_t ws_bytes,
                                         void* stream);
+
+/* 4-bit weights, two codes per byte, column 2j in the low nibble. */
+typedef enum {
+  MOE_W4_INT4 = 0,      /* s (q - 8), q in [0, 15]                           */
+  MOE_W4_INT4_ZERO = 1, /* s (q - z), a zero point z per group               */
+  MOE_W4_MXFP4 = 2      /* 2^(s - 127) e2m1(q): MOE_W_MXFP4's weights        */
+} moe_w4_t;
+
+/* One linear layer with 4-bit weights (host struct).  Requirements: those of
+ * moe_expert_linear_t, for weights of half a byte; group_size 32, 64 or 128
+ * (MXFP4: 32) divides in_features; scale_dtype is dtype or fp32 (MXFP4:
+ * ignored, the scales are E8M0 bytes, 255 NaN). */
+typedef struct {
+  int32_t num_rows;
+  int32_t in_features;
+  int32_t out_features;
+  int32_t num_experts;
+  int32_t dtype;       /* moe_dtype_t of x and out                           */
+  int32_t activation;  /* as in moe_expert_linear_t                          */
+  float act_limit;
+  int32_t format;      /* moe_w4_t                                           */
+  int32_t group_size;  /* columns that share a scale                         */
+  int32_t scale_dtype; /* moe_dtype_t                                        */
+} moe_expert_linear_w4_t;
+
+/* out[r, :] = F(x[r, :] W_e^T) as moe_expert_linear, W_e from codes uint8
+ * [E, wide, in / 2], scales [E, wide, in / group_size] and, MOE_W4_INT4_ZERO
+ * alone, zeros uint8 of the scales' shape (any value counts as it is).  The
+ * weights are used as the exact products of scale and code; sums are fp32.
+ * Made for decode batches: every 64 rows of an expert (32 of fp32) read its
+ * weights once.  A row with an infinity or a NaN gives infinities or NaN. */
+moe_status_t moe_expert_linear_w4(const moe_expert_linear_w4_t* p, const void* x,
+                                  const int32_t* expert_offsets, const void* codes,
+                                  const void* scales, const void* zeros, void* out,
+                                  void* stream);
 
 /* Message of the last failed call on this thread ("" if none).  The
  * argument errors it describes follow the ValueError conditions of

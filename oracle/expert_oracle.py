@@ -88,6 +88,19 @@ def activate(kind, pre, limit=0.0):
     return f * u, df * live_g * u, f * live_u
 
 
+def activated(kind, pre, err, limit=0.0):
+    """(values, err) of F at pre, which is off by at most err."""
+    f, dg, du = activate(kind, pre, limit)
+    if kind == "none":
+        return f, err
+    if du is None:
+        return f, err * (np.abs(dg) + 4.0 * err) + act_rel(pre) * (np.abs(f) + np.abs(pre))
+    n = f.shape[1]
+    eg, eu, up = err[:, :n], err[:, n:], 2.0 * (1.0 + np.abs(pre[:, n:]))
+    return f, eg * (np.abs(dg) + eg * up) + eu * (np.abs(du) + eu) \
+        + act_rel(pre[:, :n]) * (np.abs(f) + np.abs(du))
+
+
 def ranges(offsets, R, E):
     if offsets is None:
         return [(0, 0, R)]
@@ -102,17 +115,7 @@ def linear(x, w, offsets, kind="none", limit=0.0):
         pre[a:b] = x[a:b] @ w[e].T
         mag[a:b] = np.abs(x[a:b]) @ np.abs(w[e]).T
     err = sum_rel(K) * mag
-    f, dg, du = activate(kind, pre, limit)
-    if kind == "none":
-        return {"out": (f, err), "pre_act": (pre, err)}
-    if du is None:
-        ferr = err * (np.abs(dg) + 4.0 * err) + act_rel(pre) * (np.abs(f) + np.abs(pre))
-    else:
-        n = f.shape[1]
-        eg, eu, up = err[:, :n], err[:, n:], 2.0 * (1.0 + np.abs(pre[:, n:]))
-        ferr = eg * (np.abs(dg) + eg * up) + eu * (np.abs(du) + eu) \
-            + act_rel(pre[:, :n]) * (np.abs(f) + np.abs(du))
-    return {"out": (f, ferr), "pre_act": (pre, err)}
+    return {"out": activated(kind, pre, err, limit), "pre_act": (pre, err)}
 
 
 def linear_grad(x, w, offsets, grad_out, pre=None, kind="none", limit=0.0, step=0.0):
@@ -141,3 +144,34 @@ def linear_grad(x, w, offsets, grad_out, pre=None, kind="none", limit=0.0, step=
         gw[e] = d[a:b].T @ x[a:b]
         gwe[e] = sum_rel(b - a) * (ad.T @ ax) + derr[a:b].T @ ax
     return {"grad_x": (gx, gxe), "grad_weight": (gw, gwe)}
+
+
+E2M1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6])
+
+
+def dequant_w4(codes, scales, form, zeros=None):
+    """(weights [E, wide, K], magnitudes that a product with x may pass through):
+    int4 codes may be carried as 128 + q of the group's own scale."""
+    E, wide, half = codes.shape
+    q = np.empty((E, wide, 2 * half), dtype=np.int64)
+    q[..., 0::2], q[..., 1::2] = codes & 15, codes >> 4
+    group = 2 * half // scales.shape[2]
+    if form == "mxfp4":
+        s = np.where(scales == 255, np.nan, 2.0 ** (scales.astype(float) - 127.0))
+        v = E2M1[q] * np.repeat(s, group, axis=2)
+        return v, np.abs(v)
+    z = np.full(scales.shape, 8) if zeros is None else zeros.astype(np.int64)
+    s = np.repeat(scales, group, axis=2)
+    z = np.repeat(z, group, axis=2)
+    return s * (q - z), np.abs(s) * (144.0 + np.abs(z))
+
+
+def linear_w4(x, w, mag, offsets, kind="none", limit=0.0):
+    """(values, err) of out; w, mag: from dequant_w4."""
+    R, K = x.shape
+    wide = w.shape[1]
+    pre, err = np.full((R, wide), np.nan), np.full((R, wide), np.nan)
+    for e, a, b in ranges(offsets, R, w.shape[0]):
+        pre[a:b] = x[a:b] @ w[e].T
+        err[a:b] = sum_rel(K) * (np.abs(x[a:b]) @ mag[e].T)
+    return activated(kind, pre, err, limit)

@@ -115,3 +115,48 @@ def test_linear_binding():
         moe.expert_linear(p, x, x, x)
     with pytest.raises(ValueError, match="GPU"):
         moe.expert_linear_backward(p, x, x, x)
+
+
+@pytest.mark.parametrize("kw,status,word", SIZES + [
+    (dict(group_size=16), -2, "group_size"), (dict(group_size=0), -2, "group_size"),
+    (dict(format="mxfp4", group_size=64), -2, "MXFP4"),
+    (dict(in_features=96, group_size=64), -2, "does not divide"),
+    (dict(scale_dtype=torch.float16), -2, "scale_dtype")])
+def test_w4_problems(lib, kw, status, word):
+    p = moe.ExpertLinearW4(**{**dict(num_rows=4, in_features=64, out_features=32, num_experts=2,
+                                     activation="silu", group_size=32), **kw})
+    refused(lib, lib.moe_expert_linear_w4(p._ref, V, V, V, V, None, V, None), status, word)
+
+
+def test_w4_arguments(lib):
+    p = moe.ExpertLinearW4(4, 64, 32, 2, format="int4_zero", group_size=32)
+    call = lib.moe_expert_linear_w4
+    refused(lib, call(None, V, V, V, V, V, V, None), -1, "expert linear")
+    for i, word in enumerate(("x", "expert_offsets", "codes", "scales", "zeros", "out")):
+        args = [V] * 6
+        args[i] = None
+        refused(lib, call(p._ref, *args, None), -1, word + " is NULL")
+        if word not in ("codes", "zeros"):              # bytes lie at any address
+            args[i] = ODD
+            refused(lib, call(p._ref, *args, None), -1, word)
+    plain = moe.ExpertLinearW4(4, 64, 32, 2, group_size=32)
+    refused(lib, call(plain._ref, V, V, V, V, V, V, None), -1, "zeros")
+    empty = moe.ExpertLinearW4(0, 64, 32, 2, group_size=32)
+    assert call(empty._ref, *[None] * 7) == 0
+    bad = moe._ExpertLinearW4(4, 64, 32, 2, 0, -1, 0.0, 3, 32, 0)
+    refused(lib, call(ctypes.byref(bad), V, V, V, V, None, V, None), -1, "format")
+
+
+def test_w4_binding():
+    with pytest.raises(ValueError, match="format"):
+        moe.ExpertLinearW4(4, 64, 32, format="nf4")
+    with pytest.raises(ValueError, match="uint8"):
+        moe.ExpertLinearW4(4, 64, 32, format="mxfp4", group_size=32, scale_dtype=torch.float32)
+    with pytest.raises(ValueError, match="scale_dtype"):
+        moe.ExpertLinearW4(4, 64, 32, scale_dtype=torch.uint8)
+    p = moe.ExpertLinearW4(4, 64, 32, 2, activation="silu", format="mxfp4", group_size=32)
+    assert p.wide == 64 and p.scales == torch.uint8
+    assert pickle.loads(pickle.dumps(p)) == p
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        moe.expert_linear_w4(p, x, x, x, x)
