@@ -105,7 +105,8 @@ EXPORTS = ("moe_routing_sizes", "moe_stage_workspace_size", "moe_workspace_size"
            "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
            "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward",
            "moe_expert_linear", "moe_expert_linear_workspace_size",
-           "moe_expert_linear_backward", "moe_expert_linear_w4")
+           "moe_expert_linear_backward", "moe_expert_linear_w4",
+           "moe_block_norm_quant", "moe_stage_routing", "moe_forward_quantized")
 
 _lib = None
 
@@ -156,6 +157,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_expert_linear_workspace_size.argtypes = [P(_ExpertLinear), P(S)]
     lib.moe_expert_linear_backward.argtypes = [P(_ExpertLinear)] + [V] * 8 + [S, V]
     lib.moe_expert_linear_w4.argtypes = [P(_ExpertLinearW4)] + [V] * 7
+    lib.moe_block_norm_quant.argtypes = [P(_BlockNorm), I32] + [V] * 10
+    lib.moe_stage_routing.argtypes = [P(_Problem)] + [V] * 4 + [P(_Eplb), V, V, P(_Routing), V, S,
+                                                               V]
+    lib.moe_forward_quantized.argtypes = [P(_Problem)] + [V] * 6 + [P(_Eplb)] + [V] * 6 + [S, V]
     lib.moe_last_error.argtypes = []
     for name in EXPORTS:
         fn = getattr(lib, name)
@@ -314,6 +319,17 @@ def stage(p: Problem, hidden, topk_ids, topk_weights, bufs: dict, is_padding=Non
                          _ptr(bufs["ws"]), bufs["ws"].numel(), _stream()))
 
 
+def stage_routing(p: Problem, topk_ids, topk_weights, bufs: dict, is_padding=None,
+                  expert_num_tokens=None, eplb=None):
+    """moe_stage_routing: stage without its rows, for x_q and x_sf made elsewhere."""
+    e = _eplb(eplb)
+    r = _routing(bufs)
+    _check(load_library().moe_stage_routing(
+        ctypes.byref(p.c()), _ptr(expert_num_tokens), _ptr(topk_ids), _ptr(topk_weights),
+        _ptr(is_padding), e[0] if e else None, _ptr(bufs["topk_idx"]), _ptr(bufs["topk_w"]),
+        ctypes.byref(r), _ptr(bufs["ws"]), bufs["ws"].numel(), _stream()))
+
+
 def grouped_gemm_w13(p: Problem, a_q, a_sf, routing: dict, w13, w13_sf, gate_up):
     r = _routing(routing)
     _check(load_library().moe_grouped_gemm_w13(ctypes.byref(p.c()), _ptr(a_q), _ptr(a_sf),
@@ -412,6 +428,16 @@ def forward(p: Problem, hidden, topk_ids, topk_weights, w13, w13_sf, w2, w2_sf, 
         _ptr(w2), _ptr(w2_sf), _ptr(out), _ptr(ws), ws.numel(), _stream()))
 
 
+def forward_quantized(p: Problem, x_q, x_sf, topk_ids, topk_weights, w13, w13_sf, w2, w2_sf, out,
+                      ws, is_padding=None, expert_num_tokens=None, eplb=None):
+    """moe_forward_quantized: the layer on staged rows (block_norm_quant, stage)."""
+    e = _eplb(eplb)
+    _check(load_library().moe_forward_quantized(
+        ctypes.byref(p.c()), _ptr(x_q), _ptr(x_sf), _ptr(expert_num_tokens), _ptr(topk_ids),
+        _ptr(topk_weights), _ptr(is_padding), e[0] if e else None, _ptr(w13), _ptr(w13_sf),
+        _ptr(w2), _ptr(w2_sf), _ptr(out), _ptr(ws), ws.numel(), _stream()))
+
+
 STATIC_SCRATCH_BYTES = 64 << 20      # MOE_STATIC_SCRATCH_BYTES
 
 
@@ -444,12 +470,24 @@ class MoeLayer:
         return out
 
 
+    def quantized(self, x_q, x_sf, topk_ids, topk_weights, out=None, is_padding=None,
+                  expert_num_tokens=None, eplb=None):
+        """The layer on rows that are staged already."""
+        if out is None:
+            out = torch.empty((self.p.num_tokens, self.p.hidden), dtype=torch.bfloat16,
+                              device=x_q.device)
+        forward_quantized(self.p, x_q, x_sf, topk_ids, topk_weights, self.w13, self.w13_sf,
+                          self.w2, self.w2_sf, out, self.ws, is_padding, expert_num_tokens, eplb)
+        return out
+
+
 # ---- around the layer: router, sorted rows, block norms ----------------------
 # Unlike the layer's calls these check shapes, types and devices here, and run
 # on the tensors' device, on its current stream, whatever device is current.
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}     # moe_dtype_t
 SCORES = ("softmax", "sigmoid")                                        # moe_score_t
+_EIGHT_BITS = {k: v for k, v in _ACT_QUANT.items() if v != Q_BF16}
 GATES = ("none", "token", "channel", "full")                           # moe_gate_t
 
 
@@ -714,6 +752,37 @@ def block_norm(p: BlockNorm, residual, normed=None, y=None, residual_out=None,
          _arg(normed, "normed", p.dtype, shape, d))
 
 
+def quant_shape(rows: int, hidden: int, quant: str):
+    """(dtype, shape) of the scales of ``rows`` staged rows."""
+    if quant == "fp32":
+        return torch.float32, (rows, hidden // 128)
+    return torch.uint8, (rows, hidden // 32 if quant == "mxfp8" else
+                         (hidden // 128 + 3) // 4 * 4)
+
+
+def alloc_quant_outputs(p: BlockNorm, quant: str = "ue8m0", device="cuda") -> dict:
+    """The 8-bit outputs of block_norm_quant, by its parameters' names."""
+    dtype, shape = quant_shape(p.num_tokens, p.hidden, quant)
+    return {"x_q": torch.empty((p.num_tokens, p.hidden), dtype=torch.uint8, device=device),
+            "x_sf": torch.empty(shape, dtype=dtype, device=device)}
+
+
+def block_norm_quant(p: BlockNorm, residual, x_q, x_sf, quant: str = "ue8m0", normed=None, y=None,
+                     residual_out=None, pre_weight=None, post_weight=None, gate=None):
+    """moe_block_norm_quant: block_norm whose normed rows leave as the layer's
+    staged input, x_q and x_sf (quant: "ue8m0" | "fp32" | "mxfp8"), and as they
+    are too where normed is given."""
+    d = _device(residual, "residual")
+    shape = (p.num_tokens, p.hidden)
+    kind = _choice(quant, _EIGHT_BITS, "quant")
+    _run(load_library().moe_block_norm_quant, d, p._ref, kind,
+         _arg(residual, "residual", p.dtype, shape, d),
+         *_block_args(p, y, post_weight, gate, pre_weight, d),
+         _arg(residual_out, "residual_out", p.dtype, shape, d),
+         _arg(normed, "normed", p.dtype, shape, d), _arg(x_q, "x_q", torch.uint8, shape, d),
+         _arg(x_sf, "x_sf", *quant_shape(*shape, quant), d))
+
+
 def block_norm_backward(p: BlockNorm, residual_out, grad_normed, grad_residual, y=None,
                         grad_residual_out=None, pre_weight=None, post_weight=None, gate=None,
                         grad_y=None, grad_pre_weight=None, grad_post_weight=None,
@@ -876,11 +945,17 @@ class MoeBlock:
     torch's: a float32 router copies the normed rows to float32 for it on every
     call (16384 x 7168 by 256 experts: 550 us, 71 with a bfloat16 one).  The batched layout has no place here: its slabs come from a
     dispatch that already routed.
+
+    ``staged``: the pre norm's rows leave it in the layer's 8 bits too, beside the 16
+    that the router reads, and the layer does not stage them again.  The codes then come
+    from the norm before its rounding: the block's bits are not those without it.
     """
 
     def __init__(self, layer: MoeLayer, router: Router, router_weight, norm: BlockNorm,
-                 pre_weight=None, post_weight=None, bias=None):
+                 pre_weight=None, post_weight=None, bias=None, staged: bool = False):
         p = layer.p
+        if staged and p.act_quant == Q_BF16:
+            raise ValueError("bf16 activations are not quantized: staged has no place")
         if p.layout == LAYOUT_BATCHED:
             raise ValueError("MoeBlock needs the contiguous or the indexed layout")
         if norm.dtype != torch.bfloat16:
@@ -906,30 +981,54 @@ class MoeBlock:
         k = (p.num_tokens, p.top_k)
         self.topk_ids = torch.empty(k, dtype=torch.int32, device=dev)
         self.topk_weights = torch.empty(k, dtype=torch.float32, device=dev)
+        self.quant = {v: n for n, v in _ACT_QUANT.items()}[p.act_quant]
+        self.staged = alloc_quant_outputs(norm, self.quant, dev) if staged else None
 
     def __call__(self, residual, normed=None, gate=None, is_padding=None, eplb=None,
-                 residual_out=None, next_normed=None, next_weight=None):
+                 residual_out=None, next_normed=None, next_weight=None, staged=None,
+                 next_staged=None):
         """residual_out (new unless given; may be residual).  ``normed``: the
-        residual's pre norm where the block before this one left it; with
-        ``next_normed`` the next block's is written there, by next_weight.  With
-        ``eplb`` the router's experts are its logical ones."""
+        residual's pre norm where the block before this one left it, and
+        ``staged``, a dict of x_q and x_sf, the same in the layer's 8 bits where
+        it left that too; with ``next_normed`` (and ``next_staged``) the next
+        block's are written there, by next_weight.  With ``eplb`` the router's
+        experts are its logical ones."""
         p, r = self.layer.p, self.router
         experts = p.num_experts if eplb is None else eplb["l2p"].shape[0]
         if r.num_experts != experts:
             raise ValueError(f"the router chooses from {r.num_experts} experts, the layer has "
                              f"{experts}{'' if eplb is None else ' logical ones'}")
         _arg(normed, "normed", self.norm.dtype, (p.num_tokens, p.hidden), residual.device)
+        if staged is not None:
+            if normed is None:
+                raise ValueError("staged rows come with the normed ones the router reads")
+            if p.act_quant == Q_BF16:
+                raise ValueError("bf16 activations are not quantized: staged has no place")
+            _arg(staged["x_q"], "x_q", torch.uint8, (p.num_tokens, p.hidden), residual.device)
+            _arg(staged["x_sf"], "x_sf", *quant_shape(p.num_tokens, p.hidden, self.quant),
+                 residual.device)
         with torch.cuda.device(_device(residual, "residual")):
             if normed is None:
-                normed = self.hidden
-                block_norm(self.pre, residual, normed, pre_weight=self.pre_weight)
+                normed, staged = self.hidden, self.staged
+                if staged is None:
+                    block_norm(self.pre, residual, normed, pre_weight=self.pre_weight)
+                else:
+                    block_norm_quant(self.pre, residual, **staged, quant=self.quant,
+                                     normed=normed, pre_weight=self.pre_weight)
             logits = torch.matmul(normed.to(self.router.dtype), self.router_weight.t())
             router_topk(self.router, logits, self.topk_ids, self.topk_weights, bias=self.bias,
                         is_padding=is_padding)
-            self.layer(normed, self.topk_ids, self.topk_weights, out=self.y,
-                       is_padding=is_padding, eplb=eplb)
+            run = self.layer if staged is None else self.layer.quantized
+            rows = (normed,) if staged is None else (staged["x_q"], staged["x_sf"])
+            run(*rows, self.topk_ids, self.topk_weights, out=self.y, is_padding=is_padding,
+                eplb=eplb)
             if residual_out is None:
                 residual_out = torch.empty_like(residual)
-            block_norm(self.norm, residual, next_normed, y=self.y, residual_out=residual_out,
-                       pre_weight=next_weight, post_weight=self.post_weight, gate=gate)
+            after = dict(y=self.y, residual_out=residual_out, pre_weight=next_weight,
+                         post_weight=self.post_weight, gate=gate)
+            if next_staged is None:
+                block_norm(self.norm, residual, next_normed, **after)
+            else:
+                block_norm_quant(self.norm, residual, **next_staged, quant=self.quant,
+                                 normed=next_normed, **after)
         return residual_out

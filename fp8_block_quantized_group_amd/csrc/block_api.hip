@@ -135,6 +135,40 @@ moe_status_t check_block(const moe_block_norm_t* p, const void* y, const void* p
   return MOE_OK;
 }
 
+// the streams of a norm: y comes with the residual_out that it makes
+moe_status_t check_norm_streams(const moe_block_norm_t* p, const void* residual, const void* y,
+                                const void* post_weight, const void* gate,
+                                const void* pre_weight, const void* residual_out) {
+  CHECK(check_ptr(residual, "residual", elem(p->dtype)));
+  CHECK(check_block(p, y, post_weight, gate, pre_weight));
+  if (y != nullptr) return check_ptr(residual_out, "residual_out", elem(p->dtype));
+  if (residual_out != nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "residual_out given without y");
+  return MOE_OK;
+}
+
+moe::NormArgs norm_args(const moe_block_norm_t* p, const void* residual, const void* y,
+                        const void* post_weight, const void* gate, const void* pre_weight,
+                        void* residual_out, void* normed) {
+  moe::NormArgs a{};
+  a.r = (const uint8_t*)residual;
+  a.y = (const uint8_t*)y;
+  a.r_out = (uint8_t*)residual_out;
+  a.h = (uint8_t*)normed;
+  a.w_post = post_weight;
+  a.w_pre = pre_weight;
+  a.gate = (const uint8_t*)gate;
+  a.T = p->num_tokens;
+  a.H = p->hidden;
+  a.gate_kind = gate != nullptr ? p->gate : moe::kGateNone;
+  a.post = p->post_norm != 0;
+  a.gate_sigmoid = p->gate_sigmoid != 0;
+  a.eps = p->eps;
+  a.alpha = p->residual_scale;
+  a.offset = p->weight_offset;
+  return a;
+}
+
 size_t norm_ws_bytes(const moe_block_norm_t* p) {
   const size_t parts = moe::norm_grad_parts(p->num_tokens, p->hidden, p->dtype);
   return moe::round_up(std::max<size_t>(parts, 1) * 3 * p->hidden * sizeof(float));
@@ -266,36 +300,38 @@ moe_status_t moe_block_norm(const moe_block_norm_t* p, const void* residual, con
                             void* residual_out, void* normed, void* stream) {
   CHECK(check_norm(p));
   if (p->num_tokens == 0) return ok();
-  const size_t es = elem(p->dtype);
-  CHECK(check_ptr(residual, "residual", es));
-  CHECK(check_block(p, y, post_weight, gate, pre_weight));
-  if (y != nullptr) {
-    CHECK(check_ptr(residual_out, "residual_out", es));
-    CHECK(check_opt(normed, "normed", es));
-  } else {
-    if (residual_out != nullptr)
-      return fail(MOE_ERR_INVALID_ARG, "residual_out given without y");
-    CHECK(check_ptr(normed, "normed", es));
-  }
-  moe::NormArgs a{};
-  a.r = (const uint8_t*)residual;
-  a.y = (const uint8_t*)y;
-  a.r_out = (uint8_t*)residual_out;
-  a.h = (uint8_t*)normed;
-  a.w_post = post_weight;
-  a.w_pre = pre_weight;
-  a.gate = (const uint8_t*)gate;
-  a.T = p->num_tokens;
-  a.H = p->hidden;
-  a.gate_kind = gate != nullptr ? p->gate : moe::kGateNone;
-  a.post = p->post_norm != 0;
-  a.gate_sigmoid = p->gate_sigmoid != 0;
-  a.eps = p->eps;
-  a.alpha = p->residual_scale;
-  a.offset = p->weight_offset;
+  CHECK(check_norm_streams(p, residual, y, post_weight, gate, pre_weight, residual_out));
+  if (y != nullptr) CHECK(check_opt(normed, "normed", elem(p->dtype)));
+  else CHECK(check_ptr(normed, "normed", elem(p->dtype)));
+  const moe::NormArgs a =
+      norm_args(p, residual, y, post_weight, gate, pre_weight, residual_out, normed);
   return launch_status(
       moe::launch_norm(a, p->dtype, p->weight_dtype == MOE_DT_F32, (hipStream_t)stream),
       "moe_block_norm");
+}
+
+moe_status_t moe_block_norm_quant(const moe_block_norm_t* p, int32_t act_quant,
+                                  const void* residual, const void* y, const void* post_weight,
+                                  const void* gate, const void* pre_weight, void* residual_out,
+                                  void* normed, void* x_q, void* x_sf, void* stream) {
+  CHECK(check_norm(p));
+  if (act_quant != MOE_Q_FP8_UE8M0 && act_quant != MOE_Q_FP8_F32 && act_quant != MOE_Q_MXFP8)
+    return fail(MOE_ERR_INVALID_ARG, "unknown 8-bit quantization %d", act_quant);
+  if (p->hidden % 128 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "hidden must be a multiple of 128, got %d", p->hidden);
+  if (p->num_tokens == 0) return ok();
+  CHECK(check_norm_streams(p, residual, y, post_weight, gate, pre_weight, residual_out));
+  CHECK(check_opt(normed, "normed", elem(p->dtype)));
+  CHECK(check_ptr(x_q, "x_q", 16));
+  CHECK(check_ptr(x_sf, "x_sf", 4));
+  moe::NormArgs a =
+      norm_args(p, residual, y, post_weight, gate, pre_weight, residual_out, normed);
+  a.quant = act_quant;
+  a.q = (uint8_t*)x_q;
+  a.q_sf = (uint8_t*)x_sf;
+  return launch_status(
+      moe::launch_norm_quant(a, p->dtype, p->weight_dtype == MOE_DT_F32, (hipStream_t)stream),
+      "moe_block_norm_quant");
 }
 
 moe_status_t moe_block_norm_workspace_size(const moe_block_norm_t* p, size_t* bytes) {

@@ -277,7 +277,11 @@ struct NormArgs {
   int H, gate_kind;
   bool post, gate_sigmoid;
   float eps, alpha, offset;
+  int quant;                   // launch_norm_quant: kQuantUe8m0, kQuantF32 or kQuantMxfp8
+  uint8_t* q;                  // [T, H] codes
+  uint8_t* q_sf;               // [T, padded groups] bytes or [T, groups] fp32
 };
+hipError_t launch_norm_quant(const NormArgs& a, int dtype, bool w32, hipStream_t stream);
 hipError_t launch_norm(const NormArgs& a, int dtype, bool w32, hipStream_t stream);
 
 // blocks of the norm gradient at most (one per CU), each walking its rows

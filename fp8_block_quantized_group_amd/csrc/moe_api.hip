@@ -427,8 +427,9 @@ moe::EplbArgs eplb_args(const moe_eplb_t* eplb) {
 
 moe_status_t check_stage_args(const moe_problem_t* p, const void* hidden,
                               const int32_t* counts_in, const int32_t* topk_ids,
-                              const float* topk_weights, const moe_eplb_t* eplb) {
-  CHECK(check_ptr(hidden, "hidden", 16));
+                              const float* topk_weights, const moe_eplb_t* eplb,
+                              bool staged = false) {
+  if (!staged) CHECK(check_ptr(hidden, "hidden", 16));
   CHECK(check_ptr(topk_ids, "topk_ids", 4));
   CHECK(check_ptr(topk_weights, "topk_weights", 4));
   if (batched(p)) CHECK(check_ptr(counts_in, "expert_num_tokens (batched layout)", 4));
@@ -442,6 +443,7 @@ moe_status_t check_stage_args(const moe_problem_t* p, const void* hidden,
   return MOE_OK;
 }
 
+// hidden NULL: the rows are staged already, the routing alone
 moe_status_t run_stage(const moe_problem_t* p, const Plan& pl, const void* hidden,
                        const int32_t* counts_in, const int32_t* topk_ids,
                        const float* topk_weights, const uint8_t* is_padding,
@@ -451,11 +453,11 @@ moe_status_t run_stage(const moe_problem_t* p, const Plan& pl, const void* hidde
   const int32_t* cin = batched(p) ? counts_in : nullptr;
   // fp8 quantization runs inside the routing scan's launch; the bf16 copy
   // launches on its own
-  const bool fused = p->act_quant != MOE_Q_BF16;
+  const bool fused = hidden != nullptr && p->act_quant != MOE_Q_BF16;
   const moe::StageQuant sq{hidden, x_q, x_sf, pl.s.stage_rows, p->hidden,
                            p->act_quant == MOE_Q_MXFP8 ? 32 : 128,
                            p->act_quant != MOE_Q_FP8_F32};
-  if (!fused) {
+  if (hidden != nullptr && !fused) {
     const hipError_t err =
         moe::launch_stage_quant(hidden, x_q, x_sf, pl.s.stage_rows, p->hidden, p->act_quant,
                                 cin, p->max_tokens_per_expert, stream);
@@ -820,6 +822,28 @@ moe_status_t moe_stage(const moe_problem_t* p, const void* hidden,
                    (hipStream_t)stream);
 }
 
+moe_status_t moe_stage_routing(const moe_problem_t* p, const int32_t* expert_num_tokens_in,
+                               const int32_t* topk_ids, const float* topk_weights,
+                               const uint8_t* is_padding, const moe_eplb_t* eplb,
+                               int64_t* topk_idx_out, float* topk_w_out,
+                               const moe_routing_t* routing, void* ws, size_t ws_bytes,
+                               void* stream) {
+  CHECK(validate_problem(p));
+  if (p->num_tokens == 0) return ok();
+  CHECK(check_stage_args(p, nullptr, expert_num_tokens_in, topk_ids, topk_weights, eplb, true));
+  CHECK(check_ptr(topk_idx_out, "topk_idx_out", 8));
+  CHECK(check_ptr(topk_w_out, "topk_w_out", 4));
+  CHECK(check_routing(routing));
+  CHECK(check_ptr(ws, "ws", 4));
+  const Plan pl = make_plan(p);
+  if (ws_bytes < pl.stage_ws_bytes)
+    return fail(MOE_ERR_WORKSPACE, "stage workspace too small: %zu < %zu bytes", ws_bytes,
+                pl.stage_ws_bytes);
+  return run_stage(p, pl, nullptr, expert_num_tokens_in, topk_ids, topk_weights, is_padding, eplb,
+                   nullptr, nullptr, topk_idx_out, topk_w_out, routing, (int32_t*)ws,
+                   (hipStream_t)stream);
+}
+
 moe_status_t moe_grouped_gemm_w13(const moe_problem_t* p, const void* a_q, const void* a_sf,
                                   const moe_routing_t* routing, const void* w13,
                                   const void* w13_sf, void* gate_up, void* stream) {
@@ -989,14 +1013,19 @@ moe_status_t moe_fused_mul_sum(const moe_problem_t* p, const void* down, const i
 
 namespace {
 // side: the two-list GEMM steps may use the second stream (moe_forward);
-// otherwise their launches stay on the caller's stream (moe_forward_static)
+// otherwise their launches stay on the caller's stream (moe_forward_static).
+// staged: hidden is x_q and staged_sf its scales
 moe_status_t forward_impl(const moe_problem_t* p, const void* hidden,
                           const int32_t* expert_num_tokens_in, const int32_t* topk_ids,
                           const float* topk_weights, const uint8_t* is_padding,
                           const moe_eplb_t* eplb, const void* w13, const void* w13_sf,
                           const void* w2, const void* w2_sf, void* out, void* ws,
-                          size_t ws_bytes, void* stream, bool side) {
+                          size_t ws_bytes, void* stream, bool side, bool staged = false,
+                          const void* staged_sf = nullptr) {
   CHECK(validate_problem(p));
+  if (staged && p->act_quant == MOE_Q_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "staged rows are quantized: bf16 activations go to "
+                                     "moe_forward");
   if (p->num_tokens == 0) return ok();
   CHECK(check_stage_args(p, hidden, expert_num_tokens_in, topk_ids, topk_weights, eplb));
   CHECK(check_ptr(w13, "w13", 16));
@@ -1006,12 +1035,17 @@ moe_status_t forward_impl(const moe_problem_t* p, const void* hidden,
   CHECK(check_ptr(out, "out", 16));
   CHECK(check_ptr(ws, "ws", kAlign));
   const Plan pl = make_plan(p);
-  const Workspace w = carve(pl, p, (uint8_t*)ws);
+  Workspace w = carve(pl, p, (uint8_t*)ws);
   if (ws_bytes < w.total)
     return fail(MOE_ERR_WORKSPACE, "forward workspace too small: %zu < %zu bytes", ws_bytes,
                 w.total);
   const hipStream_t s = (hipStream_t)stream;
-  CHECK(run_stage(p, pl, hidden, expert_num_tokens_in, topk_ids, topk_weights, is_padding, eplb,
+  if (staged) {
+    CHECK(check_ptr(staged_sf, "x_sf", 4));
+    w.x_q = (decltype(w.x_q))const_cast<void*>(hidden);        // read only from here on
+    w.x_sf = (decltype(w.x_sf))const_cast<void*>(staged_sf);
+  }
+  CHECK(run_stage(p, pl, staged ? nullptr : hidden, expert_num_tokens_in, topk_ids, topk_weights, is_padding, eplb,
                   w.x_q, w.x_sf, w.idx, w.w, &w.routing, w.stage_ws, s));
   // gated activations: w13 with the activation fused; _no_mul ones: the w13
   // GEMM into gate_up, then the activation kernel
@@ -1078,6 +1112,18 @@ moe_status_t moe_forward(const moe_problem_t* p, const void* hidden,
                          size_t ws_bytes, void* stream) {
   return forward_impl(p, hidden, expert_num_tokens_in, topk_ids, topk_weights, is_padding, eplb,
                       w13, w13_sf, w2, w2_sf, out, ws, ws_bytes, stream, true);
+}
+
+moe_status_t moe_forward_quantized(const moe_problem_t* p, const void* x_q, const void* x_sf,
+                                   const int32_t* expert_num_tokens_in, const int32_t* topk_ids,
+                                   const float* topk_weights, const uint8_t* is_padding,
+                                   const moe_eplb_t* eplb, const void* w13, const void* w13_sf,
+                                   const void* w2, const void* w2_sf, void* out, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  CHECK(validate_problem(p));
+  if (p->num_tokens > 0) CHECK(check_ptr(x_q, "x_q", 16));
+  return forward_impl(p, x_q, expert_num_tokens_in, topk_ids, topk_weights, is_padding, eplb,
+                      w13, w13_sf, w2, w2_sf, out, ws, ws_bytes, stream, true, true, x_sf);
 }
 
 moe_status_t moe_forward_static(const moe_problem_t* p, const void* hidden,

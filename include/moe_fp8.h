@@ -301,6 +301,15 @@ moe_status_t moe_stage(const moe_problem_t* p, const void* hidden,
                        float* topk_w_out, const moe_routing_t* routing, void* ws,
                        size_t ws_bytes, void* stream);
 
+/* Step 2 alone, for rows that are staged already (moe_block_norm_quant):
+ * moe_stage without hidden, x_q and x_sf. */
+moe_status_t moe_stage_routing(const moe_problem_t* p, const int32_t* expert_num_tokens_in,
+                               const int32_t* topk_ids, const float* topk_weights,
+                               const uint8_t* is_padding, const moe_eplb_t* eplb,
+                               int64_t* topk_idx_out, float* topk_w_out,
+                               const moe_routing_t* routing, void* ws, size_t ws_bytes,
+                               void* stream);
+
 /* Step 3 ("...experts.fused_humming_moe", HummingGroupedExperts.apply and
  * BatchedHummingGroupedExperts.apply: humming_forward on the "w13" sublayer,
  * with the weight / activation pair of HummingExpertsBase.
@@ -446,6 +455,18 @@ moe_status_t moe_forward(const moe_problem_t* p, const void* hidden,
                          const moe_eplb_t* eplb, const void* w13, const void* w13_sf,
                          const void* w2, const void* w2_sf, void* out, void* ws,
                          size_t ws_bytes, void* stream);
+
+/* moe_forward of rows that are staged already: x_q and x_sf as moe_stage
+ * writes them for the problem's act_quant (not MOE_Q_BF16), for instance by
+ * moe_block_norm_quant; they are not written.  The other arguments, the
+ * workspace and the results are moe_forward's: of moe_stage's x_q and x_sf the
+ * same bits. */
+moe_status_t moe_forward_quantized(const moe_problem_t* p, const void* x_q, const void* x_sf,
+                                   const int32_t* expert_num_tokens_in, const int32_t* topk_ids,
+                                   const float* topk_weights, const uint8_t* is_padding,
+                                   const moe_eplb_t* eplb, const void* w13, const void* w13_sf,
+                                   const void* w2, const void* w2_sf, void* out, void* ws,
+                                   size_t ws_bytes, void* stream);
 
 /* moe_forward for callers that cannot allocate device memory: code under
  * HIP graph capture, tight serving loops, harnesses that forbid hipMalloc.
@@ -627,6 +648,17 @@ typedef struct {
 moe_status_t moe_block_norm(const moe_block_norm_t* p, const void* residual, const void* y,
                             const void* post_weight, const void* gate, const void* pre_weight,
                             void* residual_out, void* normed, void* stream);
+
+/* moe_block_norm whose normed rows leave in 8 bits, staged as the layer's
+ * calls take them: act_quant MOE_Q_FP8_UE8M0, MOE_Q_FP8_F32 or MOE_Q_MXFP8,
+ * x_q [T, hidden] and x_sf in the layout of moe_stage (16- and 4-byte
+ * aligned), by its quantizer, from the normed values before they are rounded
+ * (staging the stored normed rounds twice; its codes may differ by a step).
+ * normed may be NULL with or without y.  hidden must be a multiple of 128. */
+moe_status_t moe_block_norm_quant(const moe_block_norm_t* p, int32_t act_quant,
+                                  const void* residual, const void* y, const void* post_weight,
+                                  const void* gate, const void* pre_weight, void* residual_out,
+                                  void* normed, void* x_q, void* x_sf, void* stream);
 
 /* Device scratch bytes of moe_block_norm_backward when it returns a weight's
  * or a per-channel gate's gradient (host only). */

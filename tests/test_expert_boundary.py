@@ -1,4 +1,5 @@
-"""Refusals of the experts' own products, without a GPU: the C ABI checks
+"""Refusals of the experts' own products, of the norm that leaves in 8 bits and
+of the layer on staged rows, without a GPU: the C ABI checks
 every argument before anything is enqueued (the pointers here are not
 addresses of anything), the Python binding the shapes, types and devices."""
 import copy
@@ -160,3 +161,65 @@ def test_w4_binding():
     x = torch.zeros((4, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="GPU"):
         moe.expert_linear_w4(p, x, x, x, x)
+
+
+# ---- the norm in 8 bits and the layer on staged rows --------------------------------
+
+@pytest.mark.parametrize("kw,status,word", [
+    (dict(num_tokens=-1), -1, "num_tokens"), (dict(hidden=0), -2, "hidden"),
+    (dict(hidden=32896), -2, "hidden"), (dict(hidden=200), -2, "multiple of 128"),
+    (dict(eps=0.0), -1, "eps")])
+def test_norm_quant_problems(lib, kw, status, word):
+    p = moe.BlockNorm(**{**dict(num_tokens=4, hidden=256), **kw})
+    refused(lib, lib.moe_block_norm_quant(p._ref, 0, V, V, None, None, V, V, V, V, V, None),
+            status, word)
+
+
+def test_norm_quant_arguments(lib):
+    p = moe.BlockNorm(4, 256, post_norm=True, gate="token")
+    call = lib.moe_block_norm_quant
+    # residual, y, post_weight, gate, pre_weight, residual_out, normed, x_q, x_sf
+    for i, word in ((0, "residual"), (3, "gate"), (5, "residual_out"), (7, "x_q"), (8, "x_sf")):
+        args = [V] * 9
+        args[i] = None
+        refused(lib, call(p._ref, 0, *args, None), -1, word + " is NULL")
+        args[i] = ODD
+        refused(lib, call(p._ref, 0, *args, None), -1, word)
+    refused(lib, call(p._ref, 0, *[V] * 7, ctypes.c_void_p((1 << 20) + 8), V, None), -1, "x_q")
+    for kind in (-1, 2, 4):
+        refused(lib, call(p._ref, kind, *[V] * 9, None), -1, "quantization")
+    refused(lib, call(p._ref, 0, V, None, None, None, V, V, V, V, V, None), -1, "residual_out")
+    refused(lib, call(None, 0, *[V] * 9, None), -1, "block norm")
+    empty = moe.BlockNorm(0, 256)
+    assert call(empty._ref, 0, *[None] * 10) == 0
+
+
+def test_staged_rows_arguments(lib):
+    p = moe.Problem(16, 256, 256, 4, 2)
+    ref = ctypes.byref(p.c())
+    call = lib.moe_forward_quantized
+    # x_q, x_sf, counts, ids, weights, padding | eplb | w13, w13_sf, w2, w2_sf, out, ws
+    good = [V, V, None, V, V, None, None, V, V, V, V, V, V]
+    n = moe.workspace_size(p)
+    for i, word in ((0, "x_q"), (1, "x_sf"), (3, "topk_ids"), (4, "topk_weights"), (7, "w13"),
+                    (8, "w13_sf"), (9, "w2"), (10, "w2_sf"), (11, "out"), (12, "ws")):
+        args = list(good)
+        args[i] = None
+        refused(lib, call(ref, *args, n, None), -1, word + " is NULL")
+    refused(lib, call(ref, ODD, *good[1:], n, None), -1, "x_q")
+    refused(lib, call(ref, *good, n - 1, None), -3, "workspace")
+    half = moe.Problem(16, 256, 256, 4, 2, act_quant=moe.Q_BF16)
+    refused(lib, call(ctypes.byref(half.c()), *good, 1 << 40, None), -2, "staged")
+    call = lib.moe_stage_routing
+    r = moe._Routing(*[V] * 5)
+    good = [None, V, V, None, None, V, V, ctypes.byref(r), V]
+    n = moe.stage_workspace_size(p)
+    for i, word in ((1, "topk_ids"), (2, "topk_weights"), (5, "topk_idx_out"), (6, "topk_w_out"),
+                    (7, "routing"), (8, "ws")):
+        args = list(good)
+        args[i] = None
+        refused(lib, call(ref, *args, n, None), -1, word)
+    refused(lib, call(ref, *good, n - 1, None), -3, "workspace")
+    empty = moe.Problem(0, 256, 256, 4, 2)
+    assert call(ctypes.byref(empty.c()), *[None] * 9, 0, None) == 0
+    assert lib.moe_forward_quantized(ctypes.byref(empty.c()), *[None] * 13, 0, None) == 0
