@@ -55,6 +55,11 @@ __device__ __forceinline__ v4f mma(u32x4_t a, u32x4_t b, v4f c) {
                                                    __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
+// 2^(e - 127); 255 is NaN
+__device__ __forceinline__ float e8m0(uint32_t e) {
+  return e == 255u ? __builtin_nanf("") : __builtin_ldexpf(1.0f, (int)e - 127);
+}
+
 // The codes' dwords so that MFMA j takes one group only (GROUP 32, 64), and
 // the first of the 8 columns that lane quarter g has in it.
 template <int GROUP>
@@ -196,8 +201,7 @@ __global__ __launch_bounds__(64 * kWaves) void expert_w4_kernel(const ExpertW4Ar
         const int gi = k0 / GROUP + b;
         const int64_t i = sp[n] + (gi < groups ? gi : 0);
         if constexpr (MX) {
-          const uint32_t e = p.scales[i];                      // 2^(e - 127); 255: NaN
-          s[n][b] = e == 0 ? 0x1p-127f : e == 255 ? __builtin_nanf("") : __uint_as_float(e << 23);
+          s[n][b] = e8m0(p.scales[i]);
         } else {
           s[n][b] = RowVec<S32 ? kF32 : DT>::load_one(p.scales, i);
           z[n][b] = p.zeros != nullptr ? (float)p.zeros[i] : 8.0f;
@@ -301,10 +305,217 @@ hipError_t launch_tile(const ExpertW4Args& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int DT, bool MX, int GROUP, bool S32>
+// ---- few rows per expert -------------------------------------------------------
+// Up to 16 rows of x stay in registers, a wave's RW runs of 128 columns each,
+// while the block walks over tiles of weight rows: x is read once per block, and
+// the next tile's codes and scales are on their way while this one is worked on.
+
+// The raw codes, scales and zero points of one weight row's run.
+template <int FMT, int GROUP, int SB>
+struct RawRun {
+  static constexpr int GR = kRun / GROUP;
+  static constexpr int SW = GR * SB >= 4 ? GR * SB / 4 : 1;    // words of scales
+  u32x4_t w;
+  uint32_t s[SW], z;
+
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales,
+                                       const uint8_t* zeros) {
+    w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(codes));
+    typedef uint32_t __attribute__((aligned(1))) word;
+    typedef uint16_t __attribute__((aligned(1))) half;
+    if constexpr (GR * SB == 2) {
+      s[0] = *reinterpret_cast<const half*>(scales);
+    } else {
+#pragma unroll
+      for (int i = 0; i < SW; ++i) s[i] = reinterpret_cast<const word*>(scales)[i];
+    }
+    if constexpr (FMT == kW4Int4Zero)
+      z = GR == 1   ? *zeros
+          : GR == 2 ? *reinterpret_cast<const half*>(zeros)
+                    : *reinterpret_cast<const word*>(zeros);
+    else
+      z = 0x08080808u;
+  }
+  template <int DT>
+  __device__ __forceinline__ float scale(int b) const {
+    if constexpr (FMT == kW4Mxfp4) return e8m0((s[0] >> (8 * b)) & 255u);
+    else if constexpr (SB == 4) return __uint_as_float(s[b]);
+    else if constexpr (DT == kBf16) return __uint_as_float((s[b / 2] >> (16 * (b & 1))) << 16);
+    else return (float)__builtin_bit_cast(_Float16, (uint16_t)(s[b / 2] >> (16 * (b & 1))));
+  }
+  __device__ __forceinline__ uint32_t zero(int b) const { return (z >> (8 * b)) & 255u; }
+};
+
+// waves of a SIMD: registers for four where they hold everything (two blocks per CU)
+constexpr int few_waves(int fmt, int rw) { return rw <= 2 || (rw == 4 && fmt == kW4Mxfp4) ? 4 : 2; }
+
+template <int DT, int FMT, int GROUP, bool S32, int RW, bool GATED>
+__global__ __launch_bounds__(64 * kWaves, few_waves(FMT, RW)) void expert_w4_few_kernel(const ExpertW4Args p,
+                                                                    int per_block) {
+  constexpr bool MX = FMT == kW4Mxfp4;
+  constexpr int GR = kRun / GROUP, SB = MX ? 1 : S32 ? 4 : 2;
+  constexpr bool SUMS = DT == kBf16 && !MX;
+  constexpr int NT = GATED ? 2 : 1;
+  typedef RawRun<FMT, GROUP, SB> Raw;
+  __shared__ __align__(16) v4f red[2][kWaves][NT][64];
+
+  const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int tiles = (p.N + 15) / 16;
+  const RowTile t = find_row_tile<16>(p.offsets, p.R, p.E, (tiles + per_block - 1) / per_block,
+                                      block_index());
+  if (!t.live) return;
+  const int rows = min(16, t.n - t.m * 16);
+  const int64_t row0 = (int64_t)t.r0 + t.m * 16;
+  const int K = p.K, groups = K / GROUP, runs = K / kRun;
+
+  u32x4_t xa[RW][4];
+  const uint8_t* xp = p.x + (row0 + min(i16, rows - 1)) * K * 2;
+#pragma unroll
+  for (int j = 0; j < RW; ++j) {
+    const int c = wave * RW + j;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      xa[j][q] = *reinterpret_cast<const u32x4_any*>(
+          xp + (int64_t)((c < runs ? c : 0) * kRun + column_of<GROUP>(q, g)) * 2);
+  }
+  const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+  const v4f none = {0.0f, 0.0f, 0.0f, 0.0f};
+
+  // 16 weight rows, of the gate's half or the up one's; runs that are not there
+  // load the first one's, against zeros of x
+  auto fetch = [&](int tile, int half, Raw (&r)[RW]) {
+    const int64_t at = (int64_t)t.e * p.wide + half * p.N + min(tile * 16 + i16, p.N - 1);
+    const uint8_t* codes = p.codes + at * (K / 2) + 16 * g;
+    const int64_t sp = at * groups;
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+      const int c = wave * RW + j, k = c < runs ? c : 0;
+      const int64_t s = sp + k * GR;
+      r[j].load(codes + k * (kRun / 2), p.scales + s * SB, p.zeros + s);
+    }
+  };
+  auto product = [&](Raw (&r)[RW]) {
+    v4f acc = none;
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+      gather_groups<GROUP>(r[j].w);
+      v4f sum, ssum;
+      // The sums of x are the same for every tile, and kept: but 7 runs leave no
+      // registers for them.
+      u32x4_t one = ones;
+      if (RW > 4) asm volatile("" : "+v"(one));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int b = q * GR / 4;
+        const bool begin = q % (4 / GR) == 0, last = (q + 1) % (4 / GR) == 0;
+        const uint32_t z = r[j].zero(b);
+        if (SUMS) ssum = mma<DT>(xa[j][q], one, begin ? none : ssum);
+        const u32x4_t v =
+            codes_as_values<DT, MX>(r[j].w[q], 0x64006400u + z * 0x00010001u, 0.0f);
+        sum = mma<DT>(xa[j][q], v, begin ? none : sum);
+        if (last) {
+          const float s = r[j].template scale<DT>(b), zf = -128.0f - (float)z;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float f = SUMS ? fmaf(zf, ssum[i], sum[i]) : sum[i];
+            acc[i] = fmaf(s, f, acc[i]);
+          }
+        }
+      }
+    }
+    return acc;
+  };
+  // The waves' sums of a tile.  Two buffers in turn: what is written was read two
+  // tiles ago.  The barrier is for LDS alone, the next loads stay in flight.
+  auto finish = [&](int tile, int buf, v4f a, v4f u) {
+    red[buf][wave][0][lane] = a;
+    if constexpr (GATED) red[buf][wave][NT - 1][lane] = u;
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (threadIdx.x >= 256) return;
+    const float* flat = reinterpret_cast<const float*>(red[buf]);
+    const int r16 = threadIdx.x >> 4, c = threadIdx.x & 15;
+    const int at = ((r16 / 4) * 16 + c) * 4 + r16 % 4;
+    float f = 0.0f, h = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      f += flat[w * NT * 256 + at];
+      if (GATED) h += flat[w * NT * 256 + 256 + at];
+    }
+    if (r16 < rows && tile * 16 + c < p.N) {
+      if (p.act != kActNone) f = apply_act(p.act, f, h, p.limit);
+      RowVec<DT>::store_one(p.out, (row0 + r16) * p.N + tile * 16 + c, f);
+    }
+  };
+
+  Raw ra[RW], rb[RW];
+  int tile = t.nt * per_block;
+  const int end = min(tile + per_block, tiles);
+  fetch(tile, 0, ra);
+#pragma unroll
+  for (int j = 0; j < RW; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (wave * RW + j >= runs) xa[j][q] = u32x4_t{0u, 0u, 0u, 0u};
+      if (!MX) xa[j][q] = paired(xa[j][q]);
+    }
+  if constexpr (GATED) {
+    int buf = 0;
+    for (; tile + 1 < end; ++tile, buf ^= 1) {
+      fetch(tile, 1, rb);
+      const v4f a = product(ra);
+      fetch(tile + 1, 0, ra);
+      finish(tile, buf, a, product(rb));
+    }
+    fetch(tile, 1, rb);
+    const v4f a = product(ra);
+    finish(tile, buf, a, product(rb));
+  } else {
+    for (; tile + 2 < end; tile += 2) {
+      fetch(tile + 1, 0, rb);
+      finish(tile, 0, product(ra), none);
+      fetch(tile + 2, 0, ra);
+      finish(tile + 1, 1, product(rb), none);
+    }
+    if (tile + 1 < end) {
+      fetch(tile + 1, 0, rb);
+      finish(tile, 0, product(ra), none);
+      finish(tile + 1, 1, product(rb), none);
+    } else {
+      finish(tile, 0, product(ra), none);
+    }
+  }
+}
+
+template <int DT, int FMT, int GROUP, bool S32, int RW>
+hipError_t launch_few(const ExpertW4Args& a, hipStream_t stream) {
+  const int tiles = (a.N + 15) / 16;
+  const int64_t row_tiles = most_row_tiles<16>(a.offsets, a.R, a.E);
+  int per = 8;
+  while (per > 1 && row_tiles * ((tiles + per - 1) / per) < 512) per /= 2;
+  const dim3 grid = grid_of((row_tiles * ((tiles + per - 1) / per) + 7) / 8 * 8);
+  if (a.wide != a.N)
+    expert_w4_few_kernel<DT, FMT, GROUP, S32, RW, true>
+        <<<grid, 64 * kWaves, 0, stream>>>(a, per);
+  else
+    expert_w4_few_kernel<DT, FMT, GROUP, S32, RW, false>
+        <<<grid, 64 * kWaves, 0, stream>>>(a, per);
+  return hipGetLastError();
+}
+
+template <int DT, int FMT, int GROUP, bool S32>
 hipError_t launch_rows(const ExpertW4Args& a, hipStream_t stream) {
+  constexpr bool MX = FMT == kW4Mxfp4;
   constexpr int MOST = DT == kF32 ? 2 : 4;
   const bool few = a.R <= 16 * (int64_t)a.E;
+  if constexpr (DT != kF32) {
+    if (few && a.K % kRun == 0) {
+      const int runs = a.K / kRun;
+      if (runs <= 2 * kWaves) return launch_few<DT, FMT, GROUP, S32, 2>(a, stream);
+      if (runs <= 4 * kWaves) return launch_few<DT, FMT, GROUP, S32, 4>(a, stream);
+      if (runs <= 7 * kWaves) return launch_few<DT, FMT, GROUP, S32, 7>(a, stream);
+    }
+  }
   if (few) return launch_tile<DT, MX, GROUP, S32, 1, 2>(a, stream);
   return launch_tile<DT, MX, GROUP, S32, MOST, 2>(a, stream);
 }
@@ -313,19 +524,24 @@ hipError_t launch_rows(const ExpertW4Args& a, hipStream_t stream) {
 
 template <int DT>
 hipError_t launch_expert_w4_dt(const ExpertW4Args& a, bool s32, hipStream_t stream) {
-  if (a.format == kW4Mxfp4) return launch_rows<DT, true, 32, false>(a, stream);
-  auto group = [&](auto wide_scales) {
+  if (a.format == kW4Mxfp4) return launch_rows<DT, kW4Mxfp4, 32, false>(a, stream);
+  auto group = [&](auto format, auto wide_scales) {
+    constexpr int FMT = decltype(format)::value;
     constexpr bool S32 = decltype(wide_scales)::value;
     switch (a.group) {
-      case 32: return launch_rows<DT, false, 32, S32>(a, stream);
-      case 64: return launch_rows<DT, false, 64, S32>(a, stream);
-      default: return launch_rows<DT, false, 128, S32>(a, stream);
+      case 32: return launch_rows<DT, FMT, 32, S32>(a, stream);
+      case 64: return launch_rows<DT, FMT, 64, S32>(a, stream);
+      default: return launch_rows<DT, FMT, 128, S32>(a, stream);
     }
   };
-  if constexpr (DT != kF32) {
-    if (!s32) return group(std::false_type());
-  }
-  return group(std::true_type());
+  auto scales = [&](auto format) {
+    if constexpr (DT != kF32) {
+      if (!s32) return group(format, std::false_type());
+    }
+    return group(format, std::true_type());
+  };
+  if (a.format == kW4Int4Zero) return scales(std::integral_constant<int, kW4Int4Zero>());
+  return scales(std::integral_constant<int, kW4Int4>());
 }
 
 template hipError_t launch_expert_w4_dt<MOE_W4_DTYPE>(const ExpertW4Args&, bool, hipStream_t);
