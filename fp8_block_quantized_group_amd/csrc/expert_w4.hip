@@ -9,8 +9,8 @@
 // are 32 columns of one weight row: four MFMAs of 32 columns, whose B operand
 // they are (a lane's accumulators then belong to one weight row and take one
 // scale per group), the rows of x the A operand, straight from memory.  The
-// codes of a group have to meet in one MFMA: with groups of 128 they do as they
-// lie, groups of 64 and 32 swap registers between the lane quarters first.
+// codes of a group have to meet in one MFMA: the lane quarters exchange registers
+// first.
 //
 // Codes become 16-bit floats without a conversion each: or-ed into the
 // mantissa of 128 (bf16) or 1024 (fp16) they are 128 + q and 1024 + q, two at a
@@ -26,6 +26,7 @@
 #include "expert_act.h"
 #include "expert_rows.h"
 #include "kernels.h"
+#include "lds_copy.h"
 #include "row_vec.h"
 
 #ifndef MOE_W4_DTYPE
@@ -60,29 +61,20 @@ __device__ __forceinline__ float e8m0(uint32_t e) {
   return e == 255u ? __builtin_nanf("") : __builtin_ldexpf(1.0f, (int)e - 127);
 }
 
-// The codes' dwords so that MFMA j takes one group only (GROUP 32, 64), and
-// the first of the 8 columns that lane quarter g has in it.
-template <int GROUP>
+// A lane quarter g holds 32 consecutive codes, columns 32g on: after this, dword
+// j holds columns 32j + 8g on in every quarter, so that MFMA j takes 32
+// consecutive columns, which are of one group, and x's operand for it is 64
+// consecutive bytes of a row.  (With groups of 128 any four dwords would do, but
+// the lanes of x would then lie 64 bytes apart: 37 rows x 14336 by 4096, groups
+// of 64 with half the exchange, 46 us against BATCHUS.)
 __device__ __forceinline__ void gather_groups(u32x4_t& w) {
-  if constexpr (GROUP < 128) {
-    auto swap32 = [](uint32_t a, uint32_t b) {
-      return __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    };
-    const auto p = swap32(w[0], w[2]), q = swap32(w[1], w[3]);
-    w = u32x4_t{p[0], q[0], p[1], q[1]};
-  }
-  if constexpr (GROUP < 64) {
-    const auto p = __builtin_amdgcn_permlane16_swap(w[0], w[1], false, false);
-    const auto q = __builtin_amdgcn_permlane16_swap(w[2], w[3], false, false);
-    w = u32x4_t{p[0], p[1], q[0], q[1]};
-  }
+  const auto p = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+  const auto q = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+  const auto r = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false);
+  const auto s = __builtin_amdgcn_permlane16_swap(p[1], q[1], false, false);
+  w = u32x4_t{r[0], r[1], s[0], s[1]};
 }
-template <int GROUP>
-__device__ __forceinline__ int column_of(int j, int g) {
-  if (GROUP == 128) return 32 * g + 8 * j;
-  if (GROUP == 64) return 32 * ((j & 2) | (g & 1)) + 8 * ((j & 1) | (g & 2));
-  return 32 * j + 8 * g;
-}
+__device__ __forceinline__ int column_of(int j, int g) { return 32 * j + 8 * g; }
 
 // 8 codes as the B operand of one MFMA.  z: the zero point, in the form that
 // the type wants (fp16: 1024 + z twice; fp32 rows: z).
@@ -137,6 +129,50 @@ __device__ __forceinline__ void split3(float x, float (&p)[3]) {
   const float rest = fine ? x - p[0] : 0.0f;
   p[1] = __uint_as_float(__float_as_uint(rest) & 0xFFFF0000u);
   p[2] = rest - p[1];
+}
+
+// x's 8 columns of one MFMA as its A operand: as they are (e2m1 codes come in
+// order), in the order of the codes' pairs, or, of fp32, in three parts.
+template <int DT, bool MX, int LOADS, int PARTS>
+__device__ __forceinline__ void x_operand(const u32x4_t (&x)[LOADS], u32x4_t (&a)[PARTS]) {
+  if constexpr (DT == kF32) {
+    float f[8], q[8][3];
+    RowVec<kF32>::unpack(x[0], f);
+    RowVec<kF32>::unpack(x[1], f + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split3(f[i], q[i]);
+#pragma unroll
+    for (int h = 0; h < 3; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[h][i] = pack_bf16x2(q[2 * i][h], q[2 * i + 1][h]);
+  } else {
+    a[0] = MX ? x[0] : paired(x[0]);
+  }
+}
+
+// The waves' sums of a tile added up, activated and stored.  Of wave w, weight
+// tile n and row tile m, lane l's four values belong to weight row 16n + l % 16
+// and rows 16m + 4 (l / 16) + i.
+template <int DT, int MT, int NT, int W>
+__device__ __forceinline__ void store_tile(const ExpertW4Args& p, const float* flat,
+                                           int64_t row0, int rows, int n0, int outc,
+                                           bool gated) {
+  constexpr int WAVE = NT * MT * 256;
+  for (int o = threadIdx.x; o < 16 * MT * outc; o += 64 * W) {
+    const int r = o / outc, c = o % outc;
+    if (r >= rows || n0 + c >= p.N) continue;
+    auto total = [&](int n, int c16) {
+      const int at = (n * MT + r / 16) * 256 + ((r % 16 / 4) * 16 + c16) * 4 + r % 4;
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) v += flat[w * WAVE + at];
+      return v;
+    };
+    const float a = total(c / 16, c % 16);
+    const float u = gated ? total(NT / 2 + c / 16, c % 16) : 0.0f;
+    const float f = p.act == kActNone ? a : apply_act(p.act, a, u, p.limit);
+    RowVec<DT>::store_one(p.out, (row0 + r) * p.N + n0 + c, f);
+  }
 }
 
 template <int DT, bool MX, int GROUP, bool S32, int MT, int NT>
@@ -212,7 +248,7 @@ __global__ __launch_bounds__(64 * kWaves) void expert_w4_kernel(const ExpertW4Ar
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int k = k0 + column_of<GROUP>(j, g);
+        const int k = k0 + column_of(j, g);
 #pragma unroll
         for (int h = 0; h < XR; ++h) {
           const u32x4_t v = *reinterpret_cast<const u32x4_any*>(
@@ -221,7 +257,7 @@ __global__ __launch_bounds__(64 * kWaves) void expert_w4_kernel(const ExpertW4Ar
         }
       }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) gather_groups<GROUP>(w[n]);
+    for (int n = 0; n < NT; ++n) gather_groups(w[n]);
 
     v4f sum[NT][MT], ssum[MT];
 #pragma unroll
@@ -231,19 +267,7 @@ __global__ __launch_bounds__(64 * kWaves) void expert_w4_kernel(const ExpertW4Ar
       u32x4_t xa[MT][PARTS];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        if constexpr (DT == kF32) {
-          float f[8], q[8][3];
-          RowVec<kF32>::unpack(x[m][j][0], f);
-          RowVec<kF32>::unpack(x[m][j][1], f + 4);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) split3(f[i], q[i]);
-#pragma unroll
-          for (int h = 0; h < 3; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) xa[m][h][i] = pack_bf16x2(q[2 * i][h], q[2 * i + 1][h]);
-        } else {
-          xa[m][0] = MX ? x[m][j][0] : paired(x[m][j][0]);
-        }
+        x_operand<DT, MX>(x[m][j], xa[m]);
         if (SUMS) ssum[m] = mma<DT>(xa[m][0], ones, first ? none : ssum[m]);
       }
 #pragma unroll
@@ -270,29 +294,12 @@ __global__ __launch_bounds__(64 * kWaves) void expert_w4_kernel(const ExpertW4Ar
     }
   }
 
-  // acc[n][m][i] of lane l: weight row 16n + l % 16, row 16m + 4 (l / 16) + i
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int m = 0; m < MT; ++m) red[wave][n * MT + m][lane] = acc[n][m];
   __syncthreads();
-  const float* flat = reinterpret_cast<const float*>(red);
-  constexpr int WAVE = NT * MT * 256;
-  for (int o = threadIdx.x; o < BM * outc; o += 64 * kWaves) {
-    const int r = o / outc, c = o % outc;
-    if (r >= rows || n0 + c >= p.N) continue;
-    auto total = [&](int n, int c16) {
-      const int at = (n * MT + r / 16) * 256 + ((r % 16 / 4) * 16 + c16) * 4 + r % 4;
-      float v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) v += flat[w * WAVE + at];
-      return v;
-    };
-    const float a = total(c / 16, c % 16);
-    const float u = gated ? total(NT / 2 + c / 16, c % 16) : 0.0f;
-    const float f = p.act == kActNone ? a : apply_act(p.act, a, u, p.limit);
-    RowVec<DT>::store_one(p.out, (row0 + r) * p.N + n0 + c, f);
-  }
+  store_tile<DT, MT, NT, kWaves>(p, reinterpret_cast<const float*>(red), row0, rows, n0, outc, gated);
 }
 
 template <int DT, bool MX, int GROUP, bool S32, int MT, int NT>
@@ -305,58 +312,156 @@ hipError_t launch_tile(const ExpertW4Args& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// ---- few rows per expert -------------------------------------------------------
-// Up to 16 rows of x stay in registers, a wave's RW runs of 128 columns each,
-// while the block walks over tiles of weight rows: x is read once per block, and
-// the next tile's codes and scales are on their way while this one is worked on.
+// ---- streamed ------------------------------------------------------------------
+// An MFMA operand's neighbouring lanes hold different rows, and loads of theirs are
+// not joined: 64 accesses of 16 bytes for an instruction (measured: with codes,
+// scales and x loaded so, the address unit was busy all the time, 280 us for 128
+// experts of 2 x 2048 x 4096, 46 for 37 rows x 14336 by 4096).  So everything
+// that is streamed goes to LDS, in a wave's own ring of stages, by loads whose
+// neighbouring lanes are neighbours in memory, and is read from there as operands.
+// No barrier is needed for the ring: a wave reads what it loaded itself.
 
-// The raw codes, scales and zero points of one weight row's run.
+constexpr uint32_t kOutOfRange = 0xF0000000u;    // past every buffer: reads as zeros
+
+// A stage's part for 16 weight rows and one run: 1 KB of codes, 64 bytes of a row
+// after the other, its 16-byte chunk c at c ^ key_codes(row), so that the 16 rows
+// of a fragment read hit distinct bank groups in passes of 8 lanes (32 banks) and
+// of 16 (64 banks); then each row's DW words of scales; then a word of zero points.
+__device__ __forceinline__ int key_codes(int r) {
+  return ((r >> 1) & 2) | (((r >> 1) ^ (r >> 3)) & 1);
+}
+
 template <int FMT, int GROUP, int SB>
-struct RawRun {
+struct Strip {
+  static constexpr bool MX = FMT == kW4Mxfp4, ZERO = FMT == kW4Int4Zero;
   static constexpr int GR = kRun / GROUP;
-  static constexpr int SW = GR * SB >= 4 ? GR * SB / 4 : 1;    // words of scales
-  u32x4_t w;
-  uint32_t s[SW], z;
+  static constexpr int DW = GR * SB >= 4 ? GR * SB / 4 : 1;    // a run's scales may be
+  static constexpr int SCALES = 1024, ZEROS = SCALES + 64 * DW;   // half of a word
+  static constexpr int BYTES = ZEROS + (ZERO ? 64 : 0);
+  static constexpr int LOADS = 2 + ZERO;
 
-  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales,
-                                       const uint8_t* zeros) {
-    w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(codes));
-    typedef uint32_t __attribute__((aligned(1))) word;
-    typedef uint16_t __attribute__((aligned(1))) half;
-    if constexpr (GR * SB == 2) {
-      s[0] = *reinterpret_cast<const half*>(scales);
-    } else {
-#pragma unroll
-      for (int i = 0; i < SW; ++i) s[i] = reinterpret_cast<const word*>(scales)[i];
+  // Where the expert's data is, and this lane's offsets in it (of weight row 0).
+  v4i codes, scales, zeros;
+  uint32_t at_codes, at_scales, at_zeros;
+  int pitch, spitch, zpitch, lane;
+
+  __device__ __forceinline__ Strip() {}
+  __device__ __forceinline__ Strip(const ExpertW4Args& p, int e) {
+    lane = threadIdx.x & 63;
+    const int64_t rows = (int64_t)e * p.wide, groups = p.K / GROUP;
+    pitch = p.K / 2;
+    spitch = (int)groups * SB;
+    zpitch = (int)groups;
+    codes = buffer_rsrc(p.codes + rows * pitch, kOutOfRange);
+    scales = buffer_rsrc(p.scales + rows * spitch, kOutOfRange);
+    zeros = buffer_rsrc(ZERO ? p.zeros + rows * zpitch : p.codes, kOutOfRange);
+    at_codes = (uint32_t)(lane >> 2) * pitch + (((lane & 3) ^ key_codes(lane >> 2)) << 4);
+    at_scales = (uint32_t)(lane / DW) * spitch + (lane % DW) * 4;
+    at_zeros = (uint32_t)lane * zpitch;
+  }
+  // weight rows from `row` (those past `last` read as zeros), run c
+  __device__ __forceinline__ void fetch(uint32_t lds, int row, int last, int c) const {
+    dma16(codes, lds, row + (lane >> 2) < last
+                          ? at_codes + (uint32_t)row * pitch + c * (kRun / 2) : kOutOfRange);
+    if (lane < 16 * DW) {
+      const uint32_t at = at_scales + (uint32_t)row * spitch + (c * GR * SB & ~3);
+      dma4(scales, lds + SCALES, row + lane / DW < last ? at : kOutOfRange);
     }
-    if constexpr (FMT == kW4Int4Zero)
-      z = GR == 1   ? *zeros
-          : GR == 2 ? *reinterpret_cast<const half*>(zeros)
-                    : *reinterpret_cast<const word*>(zeros);
-    else
-      z = 0x08080808u;
+    if (ZERO && lane < 16) {
+      const uint32_t at = at_zeros + (uint32_t)row * zpitch + (c * GR & ~3);
+      dma4(zeros, lds + ZEROS, row + lane < last ? at : kOutOfRange);
+    }
+  }
+  // what of it is this lane's: weight row lane % 16
+  u32x4_t w;
+  uint32_t s[DW], z;
+  __device__ __forceinline__ void read(const uint8_t* lds, int c) {
+    const int i = lane & 15, g = lane >> 4;
+    w = *reinterpret_cast<const u32x4_t*>(lds + i * 64 + ((g ^ key_codes(i)) << 4));
+#pragma unroll
+    for (int d = 0; d < DW; ++d)
+      s[d] = *reinterpret_cast<const uint32_t*>(lds + SCALES + (i * DW + d) * 4);
+    if (GR * SB == 2) s[0] >>= 16 * (c & 1);
+    if (ZERO) {
+      z = *reinterpret_cast<const uint32_t*>(lds + ZEROS + i * 4);
+      if (GR == 1) z >>= 8 * (c & 3);
+      if (GR == 2) z >>= 16 * (c & 1);
+    }
   }
   template <int DT>
   __device__ __forceinline__ float scale(int b) const {
-    if constexpr (FMT == kW4Mxfp4) return e8m0((s[0] >> (8 * b)) & 255u);
+    if constexpr (MX) return e8m0((s[0] >> (8 * b)) & 255u);
     else if constexpr (SB == 4) return __uint_as_float(s[b]);
     else if constexpr (DT == kBf16) return __uint_as_float((s[b / 2] >> (16 * (b & 1))) << 16);
     else return (float)__builtin_bit_cast(_Float16, (uint16_t)(s[b / 2] >> (16 * (b & 1))));
   }
-  __device__ __forceinline__ uint32_t zero(int b) const { return (z >> (8 * b)) & 255u; }
+  __device__ __forceinline__ uint32_t zero(int b) const {
+    return ZERO ? (z >> (8 * b)) & 255u : 8u;
+  }
 };
 
-// waves of a SIMD: registers for four where they hold everything (two blocks per CU)
-constexpr int few_waves(int fmt, int rw) { return rw <= 2 || (rw == 4 && fmt == kW4Mxfp4) ? 4 : 2; }
+// One run's MFMAs of NT strips with MT tiles of 16 rows.  operand(m, q, a): x's
+// operand; the sums of x are made here too where the codes carry an offset.
+template <int DT, int FMT, int GROUP, int SB, int NT, int MT, int PARTS, class X>
+__device__ __forceinline__ void run_product(Strip<FMT, GROUP, SB> (&r)[NT], X&& operand,
+                                            v4f (&acc)[NT][MT]) {
+  constexpr bool MX = FMT == kW4Mxfp4, SUMS = DT == kBf16 && !MX;
+  constexpr int GR = kRun / GROUP;
+  const v4f none = {0.0f, 0.0f, 0.0f, 0.0f};
+  const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll
+  for (int n = 0; n < NT; ++n) gather_groups(r[n].w);
+  v4f sum[NT][MT], ssum[MT];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int b = q * GR / 4;
+    const bool begin = q % (4 / GR) == 0, last = (q + 1) % (4 / GR) == 0;
+    u32x4_t xa[MT][PARTS];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      operand(m, q, xa[m]);
+      if (SUMS) ssum[m] = mma<DT>(xa[m][0], ones, begin ? none : ssum[m]);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t z = r[n].zero(b);
+      const u32x4_t v =
+          codes_as_values<DT, MX>(r[n].w[q], 0x64006400u + z * 0x00010001u, (float)z);
+      const float s = r[n].template scale<DT>(b), zf = -128.0f - (float)z;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        v4f d = begin ? none : sum[n][m];
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h) d = mma<DT>(xa[m][h], v, d);
+        sum[n][m] = d;
+        if (last) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float f = SUMS ? fmaf(zf, ssum[m][i], d[i]) : d[i];
+            acc[n][m][i] = fmaf(s, f, acc[n][m][i]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Up to 16 rows: x stays in registers, a wave's RW runs of it, while the block
+// walks over tiles of 16 weight rows (gated: 16 of the gate's and 16 of the up's).
+constexpr int kFewLds = 79 * 1024;               // two blocks per CU
 
 template <int DT, int FMT, int GROUP, bool S32, int RW, bool GATED>
-__global__ __launch_bounds__(64 * kWaves, few_waves(FMT, RW)) void expert_w4_few_kernel(const ExpertW4Args p,
-                                                                    int per_block) {
+__global__ __launch_bounds__(64 * kWaves, RW <= 4 ? 4 : 2) void expert_w4_few_kernel(
+    const ExpertW4Args p, int per_block) {
   constexpr bool MX = FMT == kW4Mxfp4;
-  constexpr int GR = kRun / GROUP, SB = MX ? 1 : S32 ? 4 : 2;
-  constexpr bool SUMS = DT == kBf16 && !MX;
-  constexpr int NT = GATED ? 2 : 1;
-  typedef RawRun<FMT, GROUP, SB> Raw;
+  constexpr int SB = MX ? 1 : S32 ? 4 : 2, NT = GATED ? 2 : 1;
+  typedef Strip<FMT, GROUP, SB> S;
+  constexpr int RED = 2 * kWaves * NT * 1024;
+  constexpr int FIT = (kFewLds - RED) / (kWaves * S::BYTES);
+  constexpr int D = FIT > 8 ? 8 : FIT;           // stages of a wave's ring
+  static_assert(D >= 4 && D * S::LOADS < 60, "ring");
+  static_assert(D * S::BYTES >= 4096, "a run of x passes through the ring");
+  __shared__ __align__(1024) uint8_t ring[kWaves][D * S::BYTES];
   __shared__ __align__(16) v4f red[2][kWaves][NT][64];
 
   const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
@@ -367,72 +472,93 @@ __global__ __launch_bounds__(64 * kWaves, few_waves(FMT, RW)) void expert_w4_few
   if (!t.live) return;
   const int rows = min(16, t.n - t.m * 16);
   const int64_t row0 = (int64_t)t.r0 + t.m * 16;
-  const int K = p.K, groups = K / GROUP, runs = K / kRun;
+  const int K = p.K, runs = K / kRun;
+  const int c0 = wave * RW, mine = min(max(runs - c0, 0), RW);   // this wave's runs
+  uint8_t* my = ring[wave];
+  const uint32_t my_lds = lds_addr(my);
 
+  // x: 4 rows of a run per load, 16 lanes a row, then through LDS to operands
   u32x4_t xa[RW][4];
-  const uint8_t* xp = p.x + (row0 + min(i16, rows - 1)) * K * 2;
+  {
+    const auto rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(p.x + row0 * K * 2), 0, kOutOfRange, kRsrcWord3);
 #pragma unroll
-  for (int j = 0; j < RW; ++j) {
-    const int c = wave * RW + j;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      xa[j][q] = *reinterpret_cast<const u32x4_any*>(
-          xp + (int64_t)((c < runs ? c : 0) * kRun + column_of<GROUP>(q, g)) * 2);
-  }
-  const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-  const v4f none = {0.0f, 0.0f, 0.0f, 0.0f};
-
-  // 16 weight rows, of the gate's half or the up one's; runs that are not there
-  // load the first one's, against zeros of x
-  auto fetch = [&](int tile, int half, Raw (&r)[RW]) {
-    const int64_t at = (int64_t)t.e * p.wide + half * p.N + min(tile * 16 + i16, p.N - 1);
-    const uint8_t* codes = p.codes + at * (K / 2) + 16 * g;
-    const int64_t sp = at * groups;
-#pragma unroll
-    for (int j = 0; j < RW; ++j) {
-      const int c = wave * RW + j, k = c < runs ? c : 0;
-      const int64_t s = sp + k * GR;
-      r[j].load(codes + k * (kRun / 2), p.scales + s * SB, p.zeros + s);
-    }
-  };
-  auto product = [&](Raw (&r)[RW]) {
-    v4f acc = none;
-#pragma unroll
-    for (int j = 0; j < RW; ++j) {
-      gather_groups<GROUP>(r[j].w);
-      v4f sum, ssum;
-      // The sums of x are the same for every tile, and kept: but 7 runs leave no
-      // registers for them.
-      u32x4_t one = ones;
-      if (RW > 4) asm volatile("" : "+v"(one));
+    for (int j = 0; j < RW; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int b = q * GR / 4;
-        const bool begin = q % (4 / GR) == 0, last = (q + 1) % (4 / GR) == 0;
-        const uint32_t z = r[j].zero(b);
-        if (SUMS) ssum = mma<DT>(xa[j][q], one, begin ? none : ssum);
-        const u32x4_t v =
-            codes_as_values<DT, MX>(r[j].w[q], 0x64006400u + z * 0x00010001u, 0.0f);
-        sum = mma<DT>(xa[j][q], v, begin ? none : sum);
-        if (last) {
-          const float s = r[j].template scale<DT>(b), zf = -128.0f - (float)z;
+        const int r = 4 * q + g;
+        const uint32_t at = (uint32_t)r * K * 2 + (c0 + j) * (kRun * 2) + i16 * 16;
+        xa[j][q] = __builtin_bit_cast(
+            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                         rs, r < rows && j < mine ? at : kOutOfRange, 0, 0));
+      }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float f = SUMS ? fmaf(zf, ssum[i], sum[i]) : sum[i];
-            acc[i] = fmaf(s, f, acc[i]);
-          }
-        }
+    for (int j = 0; j < RW; ++j) {
+      wave_lds_order();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = 4 * q + g;
+        *reinterpret_cast<u32x4_t*>(my + r * 256 + ((i16 ^ r) << 4)) = xa[j][q];
+      }
+      wave_lds_order();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(
+            my + i16 * 256 + (((4 * q + g) ^ i16) << 4));
+        xa[j][q] = MX ? v : paired(v);
       }
     }
-    return acc;
+    wait_lds();
+  }
+
+  const int first = t.nt * per_block, end = min(first + per_block, tiles);
+  S strip[1] = {S(p, t.e)};
+  // The ring is filled in the order it is read: tiles, halves, runs; behind the last
+  // tile with zeros from nowhere, so that as many loads are in flight as ever.
+  int f_tile = first, f_half = 0, f_j = 0, f_slot = 0;
+  auto fetch = [&]() {
+    strip[0].fetch(my_lds + f_slot * S::BYTES, f_half * p.N + f_tile * 16,
+                   f_tile < end ? (f_half + 1) * p.N : 0, c0 + f_j);
+    f_slot = f_slot + 1 == D ? 0 : f_slot + 1;
+    if (++f_j < mine) return;
+    f_j = 0;
+    if (GATED && f_half == 0) {
+      f_half = 1;
+      return;
+    }
+    f_half = 0;
+    ++f_tile;
   };
-  // The waves' sums of a tile.  Two buffers in turn: what is written was read two
-  // tiles ago.  The barrier is for LDS alone, the next loads stay in flight.
-  auto finish = [&](int tile, int buf, v4f a, v4f u) {
-    red[buf][wave][0][lane] = a;
-    if constexpr (GATED) red[buf][wave][NT - 1][lane] = u;
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (threadIdx.x >= 256) return;
+  if (mine > 0) {
+#pragma unroll 1
+    for (int d = 0; d < D; ++d) fetch();
+  }
+  int slot = 0;
+  auto product = [&]() {
+    v4f acc[1][1] = {{v4f{0.0f, 0.0f, 0.0f, 0.0f}}};
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+      if (j < mine) {
+        wait_loads<(D - 1) * S::LOADS>();        // all but the D - 1 stages after this one
+        strip[0].read(my + slot * S::BYTES, c0 + j);
+        wait_lds();
+        fetch();
+        slot = slot + 1 == D ? 0 : slot + 1;
+        run_product<DT, FMT, GROUP, SB, 1, 1, 1>(
+            strip, [&](int, int q, u32x4_t (&a)[1]) { a[0] = xa[j][q]; }, acc);
+      }
+    }
+    return acc[0][0];
+  };
+  int buf = 0;
+#pragma unroll 1
+  for (int tile = first; tile < end; ++tile, buf ^= 1) {
+    // the waves' sums meet in one of two buffers in turn: what is written was read
+    // two tiles ago
+    red[buf][wave][0][lane] = product();
+    if constexpr (GATED) red[buf][wave][NT - 1][lane] = product();
+    lds_barrier();
+    if (threadIdx.x >= 256) continue;
     const float* flat = reinterpret_cast<const float*>(red[buf]);
     const int r16 = threadIdx.x >> 4, c = threadIdx.x & 15;
     const int at = ((r16 / 4) * 16 + c) * 4 + r16 % 4;
@@ -446,45 +572,104 @@ __global__ __launch_bounds__(64 * kWaves, few_waves(FMT, RW)) void expert_w4_few
       if (p.act != kActNone) f = apply_act(p.act, f, h, p.limit);
       RowVec<DT>::store_one(p.out, (row0 + r16) * p.N + tile * 16 + c, f);
     }
-  };
+  }
+  wait_loads<0>();                               // nothing lands in LDS behind the block's end
+}
 
-  Raw ra[RW], rb[RW];
-  int tile = t.nt * per_block;
-  const int end = min(tile + per_block, tiles);
-  fetch(tile, 0, ra);
+// More rows, or more columns than registers hold: x goes through the ring too, 16
+// MT rows of a run beside the codes; a wave takes every W-th run.
+template <int DT, int FMT, int GROUP, bool S32, int MT, bool GATED, int NT, int W, int D>
+__global__ __launch_bounds__(64 * W) void expert_w4_runs_kernel(const ExpertW4Args p) {
+  constexpr bool MX = FMT == kW4Mxfp4;
+  constexpr int SB = MX ? 1 : S32 ? 4 : 2, ES = dtype_size(DT);
+  constexpr int BM = 16 * MT, OUTC = GATED ? NT * 8 : NT * 16;
+  constexpr int XROW = kRun * ES, CH = XROW / 16, PER = 64 / CH;   // x: rows of a load
+  constexpr int PARTS = DT == kF32 ? 3 : 1, XL = DT == kF32 ? 2 : 1;
+  typedef Strip<FMT, GROUP, SB> S;
+  constexpr int STAGE = NT * S::BYTES + BM * XROW, LOADS = NT * S::LOADS + BM / PER;
+  static_assert(W * D * STAGE <= 160 * 1024 && W * NT * MT * 1024 <= W * D * STAGE, "LDS");
+  static_assert(D * LOADS < 60, "loads in flight");
+  __shared__ __align__(1024) uint8_t ring[W * D * STAGE];
+
+  const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const RowTile t = find_row_tile<BM>(p.offsets, p.R, p.E, (p.N + OUTC - 1) / OUTC,
+                                      block_index());
+  if (!t.live) return;
+  const int n0 = t.nt * OUTC, rows = min(BM, t.n - t.m * BM);
+  const int64_t row0 = (int64_t)t.r0 + t.m * BM;
+  const int K = p.K, runs = K / kRun;
+  uint8_t* my = ring + wave * D * STAGE;
+  const uint32_t my_lds = lds_addr(my);
+
+  const v4i rx = buffer_rsrc(p.x + row0 * K * ES, kOutOfRange);
+  uint32_t x_off[BM / PER];
 #pragma unroll
-  for (int j = 0; j < RW; ++j)
+  for (int i = 0; i < BM / PER; ++i) {
+    const int r = i * PER + lane / CH;
+    x_off[i] = r < rows ? (uint32_t)r * K * ES + (((lane % CH) ^ (r & 15)) << 4) : kOutOfRange;
+  }
+  S strip[NT];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (wave * RW + j >= runs) xa[j][q] = u32x4_t{0u, 0u, 0u, 0u};
-      if (!MX) xa[j][q] = paired(xa[j][q]);
+  for (int n = 0; n < NT; ++n) strip[n] = S(p, t.e);
+  auto fetch = [&](int c, int slot) {
+    const uint32_t to = my_lds + slot * STAGE;
+    const bool live = c < runs;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = GATED ? n * p.N + n0 : n0 + 16 * n;
+      strip[n].fetch(to + n * S::BYTES, row, live ? GATED ? (n + 1) * p.N : p.N : 0, c);
     }
-  if constexpr (GATED) {
-    int buf = 0;
-    for (; tile + 1 < end; ++tile, buf ^= 1) {
-      fetch(tile, 1, rb);
-      const v4f a = product(ra);
-      fetch(tile + 1, 0, ra);
-      finish(tile, buf, a, product(rb));
-    }
-    fetch(tile, 1, rb);
-    const v4f a = product(ra);
-    finish(tile, buf, a, product(rb));
-  } else {
-    for (; tile + 2 < end; tile += 2) {
-      fetch(tile + 1, 0, rb);
-      finish(tile, 0, product(ra), none);
-      fetch(tile + 2, 0, ra);
-      finish(tile + 1, 1, product(rb), none);
-    }
-    if (tile + 1 < end) {
-      fetch(tile + 1, 0, rb);
-      finish(tile, 0, product(ra), none);
-      finish(tile + 1, 1, product(rb), none);
-    } else {
-      finish(tile, 0, product(ra), none);
+#pragma unroll
+    for (int i = 0; i < BM / PER; ++i)
+      dma16(rx, to + NT * S::BYTES + i * 1024,
+            live && x_off[i] != kOutOfRange ? x_off[i] + c * XROW : kOutOfRange);
+  };
+  v4f acc[NT][MT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[n][m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // Every step issues a stage, behind the last run one of zeros from nowhere: how
+  // many loads are in flight is then always the same.
+  if (wave < runs) {
+#pragma unroll 1
+    for (int d = 0; d < D - 1; ++d) fetch(wave + d * W, d);
+    int slot = 0, next = D - 1;
+#pragma unroll 1
+    for (int c = wave; c < runs; c += W) {
+      fetch(c + (D - 1) * W, next);
+      wait_loads<(D - 1) * LOADS>();
+      const uint8_t* at = my + slot * STAGE;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) strip[n].read(at + n * S::BYTES, c);
+      const uint8_t* x = at + NT * S::BYTES;
+      run_product<DT, FMT, GROUP, SB, NT, MT, PARTS>(
+          strip,
+          [&](int m, int q, u32x4_t (&a)[PARTS]) {
+            u32x4_t v[XL];
+#pragma unroll
+            for (int h = 0; h < XL; ++h)
+              v[h] = *reinterpret_cast<const u32x4_t*>(
+                  x + (16 * m + i16) * XROW + ((((4 * q + g) * XL + h) ^ i16) << 4));
+            x_operand<DT, MX>(v, a);
+          },
+          acc);
+      wait_lds();                                // before a load into what was read
+      slot = slot + 1 == D ? 0 : slot + 1;
+      next = next + 1 == D ? 0 : next + 1;
     }
   }
+  wait_loads<0>();
+  __syncthreads();
+  v4f* red = reinterpret_cast<v4f*>(ring);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) red[(wave * NT * MT + n * MT + m) * 64 + lane] = acc[n][m];
+  __syncthreads();
+  store_tile<DT, MT, NT, W>(p, reinterpret_cast<const float*>(ring), row0, rows, n0, OUTC, GATED);
 }
 
 template <int DT, int FMT, int GROUP, bool S32, int RW>
@@ -503,21 +688,46 @@ hipError_t launch_few(const ExpertW4Args& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int DT, int FMT, int GROUP, bool S32, int MT, int W, int D>
+hipError_t launch_runs(const ExpertW4Args& a, hipStream_t stream) {
+  const int64_t row_tiles = most_row_tiles<16 * MT>(a.offsets, a.R, a.E);
+  const dim3 grid = grid_of((row_tiles * ((a.N + 15) / 16) + 7) / 8 * 8);
+  if (a.wide != a.N)
+    expert_w4_runs_kernel<DT, FMT, GROUP, S32, MT, true, 2, W, D>
+        <<<grid, 64 * W, 0, stream>>>(a);
+  else
+    expert_w4_runs_kernel<DT, FMT, GROUP, S32, MT, false, 1, W, D>
+        <<<grid, 64 * W, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+// Rows of 16-byte chunks and scales in whole words, as the streamed kernels load
+// them.
+template <int SB>
+bool streams(const ExpertW4Args& a) {
+  const int groups = a.K / a.group;
+  const uintptr_t wide = (uintptr_t)a.x | (uintptr_t)a.codes;
+  return a.K % kRun == 0 && wide % 16 == 0 && (uintptr_t)a.scales % 4 == 0 &&
+         groups * SB % 4 == 0 &&
+         (a.format != kW4Int4Zero || ((uintptr_t)a.zeros % 4 == 0 && groups % 4 == 0));
+}
+
 template <int DT, int FMT, int GROUP, bool S32>
 hipError_t launch_rows(const ExpertW4Args& a, hipStream_t stream) {
-  constexpr bool MX = FMT == kW4Mxfp4;
-  constexpr int MOST = DT == kF32 ? 2 : 4;
+  constexpr int SB = FMT == kW4Mxfp4 ? 1 : S32 ? 4 : 2;
+  if (!streams<SB>(a)) return launch_tile<DT, FMT == kW4Mxfp4, GROUP, S32, 1, 2>(a, stream);
   const bool few = a.R <= 16 * (int64_t)a.E;
   if constexpr (DT != kF32) {
-    if (few && a.K % kRun == 0) {
-      const int runs = a.K / kRun;
-      if (runs <= 2 * kWaves) return launch_few<DT, FMT, GROUP, S32, 2>(a, stream);
-      if (runs <= 4 * kWaves) return launch_few<DT, FMT, GROUP, S32, 4>(a, stream);
-      if (runs <= 7 * kWaves) return launch_few<DT, FMT, GROUP, S32, 7>(a, stream);
-    }
+    const int runs = a.K / kRun;
+    if (few && runs <= 2 * kWaves) return launch_few<DT, FMT, GROUP, S32, 2>(a, stream);
+    if (few && runs <= 4 * kWaves) return launch_few<DT, FMT, GROUP, S32, 4>(a, stream);
+    if (few && runs <= 7 * kWaves) return launch_few<DT, FMT, GROUP, S32, 7>(a, stream);
+    if (few) return launch_runs<DT, FMT, GROUP, S32, 1, 8, 3>(a, stream);
+    return launch_runs<DT, FMT, GROUP, S32, 4, 4, 2>(a, stream);
+  } else {
+    if (few) return launch_runs<DT, FMT, GROUP, S32, 1, 4, 3>(a, stream);
+    return launch_runs<DT, FMT, GROUP, S32, 2, 4, 2>(a, stream);
   }
-  if (few) return launch_tile<DT, MX, GROUP, S32, 1, 2>(a, stream);
-  return launch_tile<DT, MX, GROUP, S32, MOST, 2>(a, stream);
 }
 
 }  // namespace

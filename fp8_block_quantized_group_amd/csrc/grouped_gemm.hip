@@ -196,12 +196,6 @@ __device__ __forceinline__ void dma16_w(v4i rsrc, uint32_t lds, uint32_t voffset
                  ::"s"(lds), "v"(voffset), "s"(rsrc) : "memory", "m0");
 #endif
 }
-__device__ __forceinline__ void dma4(v4i rsrc, uint32_t lds, uint32_t voffset) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-               ::"s"(lds), "v"(voffset), "s"(rsrc) : "memory", "m0");
-#endif
-}
 #pragma clang diagnostic pop
 
 // bf16 activation rows (256 bytes per k-step): the row is stored as two

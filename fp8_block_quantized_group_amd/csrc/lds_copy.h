@@ -45,6 +45,33 @@ __device__ __forceinline__ void dma16(v4i rsrc, uint32_t lds, uint32_t voffset) 
                ::"s"(lds), "v"(voffset), "s"(rsrc) : "memory", "m0");
 #endif
 }
+// ... lane l's 4 bytes at lds + 4*l
+__device__ __forceinline__ void dma4(v4i rsrc, uint32_t lds, uint32_t voffset) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               ::"s"(lds), "v"(voffset), "s"(rsrc) : "memory", "m0");
+#endif
+}
+// At most N of this wave's loads are in flight; its own LDS reads have completed.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(N) : "memory");
+#endif
+}
+// This wave's LDS accesses have completed, for a load into what they read.
+__device__ __forceinline__ void wait_lds() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#endif
+}
+// A barrier for LDS alone: loads stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#endif
+}
 #pragma clang diagnostic pop
 
 // f(integral_constant<int, v>) for a wave-uniform v in [0, N].
