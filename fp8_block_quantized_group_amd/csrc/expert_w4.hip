@@ -323,30 +323,38 @@ hipError_t launch_tile(const ExpertW4Args& a, hipStream_t stream) {
 
 constexpr uint32_t kOutOfRange = 0xF0000000u;    // past every buffer: reads as zeros
 
-// A stage's part for 16 weight rows and one run: 1 KB of codes, 64 bytes of a row
-// after the other, its 16-byte chunk c at c ^ key_codes(row), so that the 16 rows
-// of a fragment read hit distinct bank groups in passes of 8 lanes (32 banks) and
-// of 16 (64 banks); then each row's DW words of scales; then a word of zero points.
+// A stage's part for 16 weight rows and H runs: a row's 64 H bytes of codes one
+// after the other, its 16-byte chunk c at c ^ key (the 16 rows of a fragment read
+// then hit distinct bank groups in passes of 8 lanes, 32 banks, and of 16, 64
+// banks); then each row's DW words of scales and, with them, ZW of zero points.
+template <int H>
 __device__ __forceinline__ int key_codes(int r) {
-  return ((r >> 1) & 2) | (((r >> 1) ^ (r >> 3)) & 1);
+  if (H == 1) return ((r >> 1) & 2) | (((r >> 1) ^ (r >> 3)) & 1);
+  return (r & 6) | ((r ^ (r >> 3)) & 1);
 }
 
-template <int FMT, int GROUP, int SB>
+template <int FMT, int GROUP, int SB, int H>
 struct Strip {
   static constexpr bool MX = FMT == kW4Mxfp4, ZERO = FMT == kW4Int4Zero;
-  static constexpr int GR = kRun / GROUP;
-  static constexpr int DW = GR * SB >= 4 ? GR * SB / 4 : 1;    // a run's scales may be
-  static constexpr int SCALES = 1024, ZEROS = SCALES + 64 * DW;   // half of a word
-  static constexpr int BYTES = ZEROS + (ZERO ? 64 : 0);
-  static constexpr int LOADS = 2 + ZERO;
+  static constexpr int GR = kRun / GROUP, CH = 4 * H, CODES = H;   // loads of codes
+  // a stage's scales and zero points in bytes of a row; less than a word: its part
+  static constexpr int SBY = H * GR * SB, ZBY = H * GR;
+  static constexpr int DW = SBY >= 4 ? SBY / 4 : 1, ZW = ZERO ? (ZBY >= 4 ? ZBY / 4 : 1) : 0;
+  static constexpr int SL = (16 * DW + 63) / 64, ZL = ZERO ? 1 : 0;
+  static constexpr int SCALES = 1024 * H, ZEROS = SCALES + 64 * DW;
+  static constexpr int BYTES = ZEROS + 64 * ZW;
+  static constexpr int LOADS = CODES + SL + ZL;
+  static_assert(16 * ZW <= 64, "one load");
 
   // Where the expert's data is, and this lane's offsets in it (of weight row 0).
   v4i codes, scales, zeros;
   uint32_t at_codes, at_scales, at_zeros;
   int pitch, spitch, zpitch, lane;
+  bool stream;                   // no other block reads these weights
 
   __device__ __forceinline__ Strip() {}
-  __device__ __forceinline__ Strip(const ExpertW4Args& p, int e) {
+  __device__ __forceinline__ Strip(const ExpertW4Args& p, int e, bool alone) {
+    stream = alone;
     lane = threadIdx.x & 63;
     const int64_t rows = (int64_t)e * p.wide, groups = p.K / GROUP;
     pitch = p.K / 2;
@@ -355,37 +363,58 @@ struct Strip {
     codes = buffer_rsrc(p.codes + rows * pitch, kOutOfRange);
     scales = buffer_rsrc(p.scales + rows * spitch, kOutOfRange);
     zeros = buffer_rsrc(ZERO ? p.zeros + rows * zpitch : p.codes, kOutOfRange);
-    at_codes = (uint32_t)(lane >> 2) * pitch + (((lane & 3) ^ key_codes(lane >> 2)) << 4);
+    const int r = lane / CH;
+    at_codes = (uint32_t)r * pitch;
     at_scales = (uint32_t)(lane / DW) * spitch + (lane % DW) * 4;
-    at_zeros = (uint32_t)lane * zpitch;
+    at_zeros = ZERO ? (uint32_t)(lane / (ZW + !ZERO)) * zpitch + (lane % (ZW + !ZERO)) * 4 : 0;
   }
-  // weight rows from `row` (those past `last` read as zeros), run c
+  // weight rows from `row` (those from `last` on read as zeros), stage c of H runs
   __device__ __forceinline__ void fetch(uint32_t lds, int row, int last, int c) const {
-    dma16(codes, lds, row + (lane >> 2) < last
-                          ? at_codes + (uint32_t)row * pitch + c * (kRun / 2) : kOutOfRange);
-    if (lane < 16 * DW) {
-      const uint32_t at = at_scales + (uint32_t)row * spitch + (c * GR * SB & ~3);
-      dma4(scales, lds + SCALES, row + lane / DW < last ? at : kOutOfRange);
+#pragma unroll
+    for (int i = 0; i < CODES; ++i) {
+      const int r = i * (64 / CH) + lane / CH;
+      const int chunk = (lane % CH) ^ key_codes<H>(r);
+      const bool in = row + r < last && (H == 1 || c * CH + chunk < pitch / 16);
+      const uint32_t from = at_codes + (uint32_t)(row + i * (64 / CH)) * pitch +
+                            (c * CH + chunk) * 16;
+      if (stream) dma16_nt(codes, lds + i * 1024, in ? from : kOutOfRange);
+      else dma16(codes, lds + i * 1024, in ? from : kOutOfRange);
     }
-    if (ZERO && lane < 16) {
-      const uint32_t at = at_zeros + (uint32_t)row * zpitch + (c * GR & ~3);
-      dma4(zeros, lds + ZEROS, row + lane < last ? at : kOutOfRange);
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      const int l = i * 64 + lane;
+      if (SL == 1 && l >= 16 * DW) continue;
+      const int word = (c * SBY & ~3) + (l % DW) * 4;
+      const uint32_t at =
+          at_scales + (uint32_t)(row + i * (64 / DW)) * spitch + (c * SBY & ~3);
+      dma4(scales, lds + SCALES + i * 256,
+           row + l / DW < last && word < spitch ? at : kOutOfRange);
+    }
+    if constexpr (ZERO) {
+      if (lane < 16 * ZW) {
+        const int word = (c * ZBY & ~3) + (lane % ZW) * 4;
+        const uint32_t at = at_zeros + (uint32_t)row * zpitch + (c * ZBY & ~3);
+        dma4(zeros, lds + ZEROS, row + lane / ZW < last && word < zpitch ? at : kOutOfRange);
+      }
     }
   }
-  // what of it is this lane's: weight row lane % 16
+  // what of run h of it is this lane's: weight row lane % 16
+  static constexpr int RW = GR * SB >= 4 ? GR * SB / 4 : 1;    // a run's words of scales
   u32x4_t w;
-  uint32_t s[DW], z;
-  __device__ __forceinline__ void read(const uint8_t* lds, int c) {
+  uint32_t s[RW], z;
+  __device__ __forceinline__ void read(const uint8_t* lds, int c, int h) {
     const int i = lane & 15, g = lane >> 4;
-    w = *reinterpret_cast<const u32x4_t*>(lds + i * 64 + ((g ^ key_codes(i)) << 4));
+    w = *reinterpret_cast<const u32x4_t*>(lds + i * (64 * H) +
+                                          (((4 * h + g) ^ key_codes<H>(i)) << 4));
+    // a run's scales or zero points may be half or a quarter of a word
+    const int sb = (c * SBY & 3) + h * GR * SB, zb = (c * ZBY & 3) + h * GR;
 #pragma unroll
-    for (int d = 0; d < DW; ++d)
-      s[d] = *reinterpret_cast<const uint32_t*>(lds + SCALES + (i * DW + d) * 4);
-    if (GR * SB == 2) s[0] >>= 16 * (c & 1);
-    if (ZERO) {
-      z = *reinterpret_cast<const uint32_t*>(lds + ZEROS + i * 4);
-      if (GR == 1) z >>= 8 * (c & 3);
-      if (GR == 2) z >>= 16 * (c & 1);
+    for (int d = 0; d < RW; ++d)
+      s[d] = *reinterpret_cast<const uint32_t*>(lds + SCALES + i * DW * 4 + (sb & ~3) + d * 4);
+    if (GR * SB < 4) s[0] >>= 8 * (sb & 3);
+    if constexpr (ZERO) {
+      z = *reinterpret_cast<const uint32_t*>(lds + ZEROS + i * ZW * 4 + (zb & ~3));
+      if (GR < 4) z >>= 8 * (zb & 3);
     }
   }
   template <int DT>
@@ -401,14 +430,17 @@ struct Strip {
 };
 
 // One run's MFMAs of NT strips with MT tiles of 16 rows.  operand(m, q, a): x's
-// operand; the sums of x are made here too where the codes carry an offset.
-template <int DT, int FMT, int GROUP, int SB, int NT, int MT, int PARTS, class X>
-__device__ __forceinline__ void run_product(Strip<FMT, GROUP, SB> (&r)[NT], X&& operand,
+// operand; the sums of x are made here too where the codes carry an offset.  KEEP:
+// the compiler may find them the same for every tile and hold on to them.
+template <int DT, int PARTS, bool KEEP, int FMT, int GROUP, int SB, int NT, int MT, int H,
+          class X>
+__device__ __forceinline__ void run_product(Strip<FMT, GROUP, SB, H> (&r)[NT], X&& operand,
                                             v4f (&acc)[NT][MT]) {
   constexpr bool MX = FMT == kW4Mxfp4, SUMS = DT == kBf16 && !MX;
   constexpr int GR = kRun / GROUP;
   const v4f none = {0.0f, 0.0f, 0.0f, 0.0f};
-  const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+  u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+  if (!KEEP) asm volatile("" : "+v"(ones));
 #pragma unroll
   for (int n = 0; n < NT; ++n) gather_groups(r[n].w);
   v4f sum[NT][MT], ssum[MT];
@@ -448,21 +480,22 @@ __device__ __forceinline__ void run_product(Strip<FMT, GROUP, SB> (&r)[NT], X&& 
 
 // Up to 16 rows: x stays in registers, a wave's RW runs of it, while the block
 // walks over tiles of 16 weight rows (gated: 16 of the gate's and 16 of the up's).
-constexpr int kFewLds = 79 * 1024;               // two blocks per CU
 
-template <int DT, int FMT, int GROUP, bool S32, int RW, bool GATED>
-__global__ __launch_bounds__(64 * kWaves, RW <= 4 ? 4 : 2) void expert_w4_few_kernel(
+// Stages are pairs of runs, whole lines of 128 bytes of codes.
+template <int DT, int FMT, int GROUP, bool S32, int W, int RW, bool GATED>
+__global__ __launch_bounds__(64 * W, 4) void expert_w4_few_kernel(
     const ExpertW4Args p, int per_block) {
   constexpr bool MX = FMT == kW4Mxfp4;
   constexpr int SB = MX ? 1 : S32 ? 4 : 2, NT = GATED ? 2 : 1;
-  typedef Strip<FMT, GROUP, SB> S;
-  constexpr int RED = 2 * kWaves * NT * 1024;
-  constexpr int FIT = (kFewLds - RED) / (kWaves * S::BYTES);
+  typedef Strip<FMT, GROUP, SB, 2> S;
+  constexpr int RED = W * NT * 1024;
+  constexpr int FIT = (158 * 1024 / (16 / W) - RED) / (W * S::BYTES);
   constexpr int D = FIT > 8 ? 8 : FIT;           // stages of a wave's ring
-  static_assert(D >= 4 && D * S::LOADS < 60, "ring");
+  constexpr bool kKeep = RW * S::GR <= 8;        // the sums of x: four registers a group
+  static_assert(D >= 2 && D * S::LOADS < 60, "ring");
   static_assert(D * S::BYTES >= 4096, "a run of x passes through the ring");
-  __shared__ __align__(1024) uint8_t ring[kWaves][D * S::BYTES];
-  __shared__ __align__(16) v4f red[2][kWaves][NT][64];
+  __shared__ __align__(1024) uint8_t ring[W][D * S::BYTES];
+  __shared__ __align__(16) v4f red[W][NT][64];
 
   const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -473,7 +506,8 @@ __global__ __launch_bounds__(64 * kWaves, RW <= 4 ? 4 : 2) void expert_w4_few_ke
   const int rows = min(16, t.n - t.m * 16);
   const int64_t row0 = (int64_t)t.r0 + t.m * 16;
   const int K = p.K, runs = K / kRun;
-  const int c0 = wave * RW, mine = min(max(runs - c0, 0), RW);   // this wave's runs
+  const int c0 = wave * RW, mine = min(max(runs - c0, 0), RW);   // this wave's runs,
+  const int pairs = (mine + 1) / 2;                              // and stages
   uint8_t* my = ring[wave];
   const uint32_t my_lds = lds_addr(my);
 
@@ -512,15 +546,15 @@ __global__ __launch_bounds__(64 * kWaves, RW <= 4 ? 4 : 2) void expert_w4_few_ke
   }
 
   const int first = t.nt * per_block, end = min(first + per_block, tiles);
-  S strip[1] = {S(p, t.e)};
+  S strip[1] = {S(p, t.e, t.n <= 16)};
   // The ring is filled in the order it is read: tiles, halves, runs; behind the last
   // tile with zeros from nowhere, so that as many loads are in flight as ever.
   int f_tile = first, f_half = 0, f_j = 0, f_slot = 0;
   auto fetch = [&]() {
     strip[0].fetch(my_lds + f_slot * S::BYTES, f_half * p.N + f_tile * 16,
-                   f_tile < end ? (f_half + 1) * p.N : 0, c0 + f_j);
+                   f_tile < end ? (f_half + 1) * p.N : 0, c0 / 2 + f_j);
     f_slot = f_slot + 1 == D ? 0 : f_slot + 1;
-    if (++f_j < mine) return;
+    if (++f_j < pairs) return;
     f_j = 0;
     if (GATED && f_half == 0) {
       f_half = 1;
@@ -537,34 +571,42 @@ __global__ __launch_bounds__(64 * kWaves, RW <= 4 ? 4 : 2) void expert_w4_few_ke
   auto product = [&]() {
     v4f acc[1][1] = {{v4f{0.0f, 0.0f, 0.0f, 0.0f}}};
 #pragma unroll
-    for (int j = 0; j < RW; ++j) {
-      if (j < mine) {
+    for (int j = 0; j < RW / 2; ++j) {
+      if (j < pairs) {
         wait_loads<(D - 1) * S::LOADS>();        // all but the D - 1 stages after this one
-        strip[0].read(my + slot * S::BYTES, c0 + j);
+        S second = strip[0];
+        strip[0].read(my + slot * S::BYTES, c0 / 2 + j, 0);
+        second.read(my + slot * S::BYTES, c0 / 2 + j, 1);
         wait_lds();
         fetch();
         slot = slot + 1 == D ? 0 : slot + 1;
-        run_product<DT, FMT, GROUP, SB, 1, 1, 1>(
-            strip, [&](int, int q, u32x4_t (&a)[1]) { a[0] = xa[j][q]; }, acc);
+        run_product<DT, 1, kKeep>(
+            strip, [&](int, int q, u32x4_t (&a)[1]) { a[0] = xa[2 * j][q]; }, acc);
+        strip[0].w = second.w;
+        strip[0].z = second.z;
+#pragma unroll
+        for (int d = 0; d < S::RW; ++d) strip[0].s[d] = second.s[d];
+        run_product<DT, 1, kKeep>(
+            strip, [&](int, int q, u32x4_t (&a)[1]) { a[0] = xa[2 * j + 1][q]; }, acc);
       }
     }
     return acc[0][0];
   };
-  int buf = 0;
 #pragma unroll 1
-  for (int tile = first; tile < end; ++tile, buf ^= 1) {
-    // the waves' sums meet in one of two buffers in turn: what is written was read
-    // two tiles ago
-    red[buf][wave][0][lane] = product();
-    if constexpr (GATED) red[buf][wave][NT - 1][lane] = product();
+  for (int tile = first; tile < end; ++tile) {
+    // the waves' sums meet in LDS, where the last tile's have been read by now
+    const v4f a = product(), u = GATED ? product() : v4f{};
+    lds_barrier();
+    red[wave][0][lane] = a;
+    if constexpr (GATED) red[wave][NT - 1][lane] = u;
     lds_barrier();
     if (threadIdx.x >= 256) continue;
-    const float* flat = reinterpret_cast<const float*>(red[buf]);
+    const float* flat = reinterpret_cast<const float*>(red);
     const int r16 = threadIdx.x >> 4, c = threadIdx.x & 15;
     const int at = ((r16 / 4) * 16 + c) * 4 + r16 % 4;
     float f = 0.0f, h = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < W; ++w) {
       f += flat[w * NT * 256 + at];
       if (GATED) h += flat[w * NT * 256 + 256 + at];
     }
@@ -578,16 +620,17 @@ __global__ __launch_bounds__(64 * kWaves, RW <= 4 ? 4 : 2) void expert_w4_few_ke
 
 // More rows, or more columns than registers hold: x goes through the ring too, 16
 // MT rows of a run beside the codes; a wave takes every W-th run.
-template <int DT, int FMT, int GROUP, bool S32, int MT, bool GATED, int NT, int W, int D>
+template <int DT, int FMT, int GROUP, bool S32, int MT, bool GATED, int NT, int W>
 __global__ __launch_bounds__(64 * W) void expert_w4_runs_kernel(const ExpertW4Args p) {
   constexpr bool MX = FMT == kW4Mxfp4;
   constexpr int SB = MX ? 1 : S32 ? 4 : 2, ES = dtype_size(DT);
   constexpr int BM = 16 * MT, OUTC = GATED ? NT * 8 : NT * 16;
   constexpr int XROW = kRun * ES, CH = XROW / 16, PER = 64 / CH;   // x: rows of a load
   constexpr int PARTS = DT == kF32 ? 3 : 1, XL = DT == kF32 ? 2 : 1;
-  typedef Strip<FMT, GROUP, SB> S;
+  typedef Strip<FMT, GROUP, SB, 1> S;
   constexpr int STAGE = NT * S::BYTES + BM * XROW, LOADS = NT * S::LOADS + BM / PER;
-  static_assert(W * D * STAGE <= 160 * 1024 && W * NT * MT * 1024 <= W * D * STAGE, "LDS");
+  constexpr int FIT = 160 * 1024 / (W * STAGE), D = FIT > 3 ? 3 : FIT;   // stages of a ring
+  static_assert(D >= 2 && NT * MT * 1024 <= D * STAGE, "LDS");
   static_assert(D * LOADS < 60, "loads in flight");
   __shared__ __align__(1024) uint8_t ring[W * D * STAGE];
 
@@ -611,7 +654,7 @@ __global__ __launch_bounds__(64 * W) void expert_w4_runs_kernel(const ExpertW4Ar
   }
   S strip[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) strip[n] = S(p, t.e);
+  for (int n = 0; n < NT; ++n) strip[n] = S(p, t.e, false);
   auto fetch = [&](int c, int slot) {
     const uint32_t to = my_lds + slot * STAGE;
     const bool live = c < runs;
@@ -643,9 +686,9 @@ __global__ __launch_bounds__(64 * W) void expert_w4_runs_kernel(const ExpertW4Ar
       wait_loads<(D - 1) * LOADS>();
       const uint8_t* at = my + slot * STAGE;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) strip[n].read(at + n * S::BYTES, c);
+      for (int n = 0; n < NT; ++n) strip[n].read(at + n * S::BYTES, c, 0);
       const uint8_t* x = at + NT * S::BYTES;
-      run_product<DT, FMT, GROUP, SB, NT, MT, PARTS>(
+      run_product<DT, PARTS, true>(
           strip,
           [&](int m, int q, u32x4_t (&a)[PARTS]) {
             u32x4_t v[XL];
@@ -672,32 +715,28 @@ __global__ __launch_bounds__(64 * W) void expert_w4_runs_kernel(const ExpertW4Ar
   store_tile<DT, MT, NT, W>(p, reinterpret_cast<const float*>(ring), row0, rows, n0, OUTC, GATED);
 }
 
-template <int DT, int FMT, int GROUP, bool S32, int RW>
+template <int DT, int FMT, int GROUP, bool S32, int W, int RW>
 hipError_t launch_few(const ExpertW4Args& a, hipStream_t stream) {
   const int tiles = (a.N + 15) / 16;
   const int64_t row_tiles = most_row_tiles<16>(a.offsets, a.R, a.E);
-  int per = 8;
+  int per = 16;
   while (per > 1 && row_tiles * ((tiles + per - 1) / per) < 512) per /= 2;
   const dim3 grid = grid_of((row_tiles * ((tiles + per - 1) / per) + 7) / 8 * 8);
   if (a.wide != a.N)
-    expert_w4_few_kernel<DT, FMT, GROUP, S32, RW, true>
-        <<<grid, 64 * kWaves, 0, stream>>>(a, per);
+    expert_w4_few_kernel<DT, FMT, GROUP, S32, W, RW, true><<<grid, 64 * W, 0, stream>>>(a, per);
   else
-    expert_w4_few_kernel<DT, FMT, GROUP, S32, RW, false>
-        <<<grid, 64 * kWaves, 0, stream>>>(a, per);
+    expert_w4_few_kernel<DT, FMT, GROUP, S32, W, RW, false><<<grid, 64 * W, 0, stream>>>(a, per);
   return hipGetLastError();
 }
 
-template <int DT, int FMT, int GROUP, bool S32, int MT, int W, int D>
+template <int DT, int FMT, int GROUP, bool S32, int MT, int W>
 hipError_t launch_runs(const ExpertW4Args& a, hipStream_t stream) {
   const int64_t row_tiles = most_row_tiles<16 * MT>(a.offsets, a.R, a.E);
   const dim3 grid = grid_of((row_tiles * ((a.N + 15) / 16) + 7) / 8 * 8);
   if (a.wide != a.N)
-    expert_w4_runs_kernel<DT, FMT, GROUP, S32, MT, true, 2, W, D>
-        <<<grid, 64 * W, 0, stream>>>(a);
+    expert_w4_runs_kernel<DT, FMT, GROUP, S32, MT, true, 2, W><<<grid, 64 * W, 0, stream>>>(a);
   else
-    expert_w4_runs_kernel<DT, FMT, GROUP, S32, MT, false, 1, W, D>
-        <<<grid, 64 * W, 0, stream>>>(a);
+    expert_w4_runs_kernel<DT, FMT, GROUP, S32, MT, false, 1, W><<<grid, 64 * W, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -712,21 +751,32 @@ bool streams(const ExpertW4Args& a) {
          (a.format != kW4Int4Zero || ((uintptr_t)a.zeros % 4 == 0 && groups % 4 == 0));
 }
 
+// Up to 16 rows per expert on average: x in registers, by columns 8 x 2, 8 x 4 or 16
+// x 4 runs (bf16, 512 rows of 128 experts, 2 x 2048 columns, MXFP4, us: 2048 columns
+// 108, 124 with 8 x 4; 4096: 202, 213 with 16 x 2; 7168: 387, 438 with 8 x 8, and
+// 660 streamed).  Past 4096 columns a few tiles are done sooner streamed (one row x
+// 7168 by 4096: 7.1, 9.5 in registers; by 16384: 24.3 and 24.8), past 8192 all are.
+// More rows are streamed in tiles of 16 MT: up to 4 (fp32: 2).
 template <int DT, int FMT, int GROUP, bool S32>
 hipError_t launch_rows(const ExpertW4Args& a, hipStream_t stream) {
   constexpr int SB = FMT == kW4Mxfp4 ? 1 : S32 ? 4 : 2;
   if (!streams<SB>(a)) return launch_tile<DT, FMT == kW4Mxfp4, GROUP, S32, 1, 2>(a, stream);
-  const bool few = a.R <= 16 * (int64_t)a.E;
+  const int64_t per = ((int64_t)a.R + a.E - 1) / a.E;          // rows of an expert
   if constexpr (DT != kF32) {
     const int runs = a.K / kRun;
-    if (few && runs <= 2 * kWaves) return launch_few<DT, FMT, GROUP, S32, 2>(a, stream);
-    if (few && runs <= 4 * kWaves) return launch_few<DT, FMT, GROUP, S32, 4>(a, stream);
-    if (few && runs <= 7 * kWaves) return launch_few<DT, FMT, GROUP, S32, 7>(a, stream);
-    if (few) return launch_runs<DT, FMT, GROUP, S32, 1, 8, 3>(a, stream);
-    return launch_runs<DT, FMT, GROUP, S32, 4, 4, 2>(a, stream);
+    const int64_t tiles = most_row_tiles<16>(a.offsets, a.R, a.E) * ((a.N + 15) / 16);
+    if (per <= 16) {
+      if (runs <= 16) return launch_few<DT, FMT, GROUP, S32, 8, 2>(a, stream);
+      if (runs <= 32) return launch_few<DT, FMT, GROUP, S32, 8, 4>(a, stream);
+      if (runs <= 64 && tiles > 1024) return launch_few<DT, FMT, GROUP, S32, 16, 4>(a, stream);
+      return launch_runs<DT, FMT, GROUP, S32, 1, 8>(a, stream);
+    }
+    if (per <= 32) return launch_runs<DT, FMT, GROUP, S32, 2, 4>(a, stream);
+    if (per <= 48) return launch_runs<DT, FMT, GROUP, S32, 3, 4>(a, stream);
+    return launch_runs<DT, FMT, GROUP, S32, 4, 4>(a, stream);
   } else {
-    if (few) return launch_runs<DT, FMT, GROUP, S32, 1, 4, 3>(a, stream);
-    return launch_runs<DT, FMT, GROUP, S32, 2, 4, 2>(a, stream);
+    if (per <= 16) return launch_runs<DT, FMT, GROUP, S32, 1, 4>(a, stream);
+    return launch_runs<DT, FMT, GROUP, S32, 2, 4>(a, stream);
   }
 }
 

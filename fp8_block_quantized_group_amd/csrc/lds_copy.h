@@ -45,6 +45,13 @@ __device__ __forceinline__ void dma16(v4i rsrc, uint32_t lds, uint32_t voffset) 
                ::"s"(lds), "v"(voffset), "s"(rsrc) : "memory", "m0");
 #endif
 }
+// The same with the non-temporal hint, for data that no other block reads.
+__device__ __forceinline__ void dma16_nt(v4i rsrc, uint32_t lds, uint32_t voffset) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+               ::"s"(lds), "v"(voffset), "s"(rsrc) : "memory", "m0");
+#endif
+}
 // ... lane l's 4 bytes at lds + 4*l
 __device__ __forceinline__ void dma4(v4i rsrc, uint32_t lds, uint32_t voffset) {
 #if defined(__HIP_DEVICE_COMPILE__)
