@@ -733,10 +733,12 @@ template <int DT, int FMT, int GROUP, bool S32, int MT, int W>
 hipError_t launch_runs(const ExpertW4Args& a, hipStream_t stream) {
   const int64_t row_tiles = most_row_tiles<16 * MT>(a.offsets, a.R, a.E);
   const dim3 grid = grid_of((row_tiles * ((a.N + 15) / 16) + 7) / 8 * 8);
+  // eight waves where two stages of each fit
+  constexpr int W1 = MT == 2 && DT != kF32 ? 8 : W;
   if (a.wide != a.N)
     expert_w4_runs_kernel<DT, FMT, GROUP, S32, MT, true, 2, W><<<grid, 64 * W, 0, stream>>>(a);
   else
-    expert_w4_runs_kernel<DT, FMT, GROUP, S32, MT, false, 1, W><<<grid, 64 * W, 0, stream>>>(a);
+    expert_w4_runs_kernel<DT, FMT, GROUP, S32, MT, false, 1, W1><<<grid, 64 * W1, 0, stream>>>(a);
   return hipGetLastError();
 }
 
