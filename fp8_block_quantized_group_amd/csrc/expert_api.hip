@@ -71,7 +71,8 @@ moe_status_t check_linear(const moe_expert_linear_t* p) {
   if (wide * p->in_features * (int64_t)elem(p->dtype) >= (int64_t)0xF0000000u)
     return fail(MOE_ERR_UNSUPPORTED, "one expert's weights must be under 3.75 GiB");
   // and the weights' gradient is tiled expert by expert
-  if ((wide + 63) / 64 * ((p->in_features + 63) / 64) * p->num_experts >= (int64_t)1 << 31)
+  if (((wide + 63) / 64 * ((p->in_features + 63) / 64) + 7) * p->num_experts >=
+      (int64_t)1 << 31)
     return fail(MOE_ERR_UNSUPPORTED, "the experts' weights are more than 2^31 tiles");
   return MOE_OK;
 }

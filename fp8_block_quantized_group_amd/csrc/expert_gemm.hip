@@ -18,6 +18,7 @@
 // the result (W in grad_x, both in grad_W) lies there as it comes and is read
 // transposed by ds_read_b64_tr_b16 (fp32: word by word).  Every product of the
 // 16-bit types is exact and sums are fp32; fp32 goes through the fp32 MFMA.
+#include <stdlib.h>
 #include <type_traits>
 
 #include "expert_act.h"
@@ -52,9 +53,11 @@ struct Tile {
 };
 
 // 16-byte chunk c of LDS row r of an operand that runs along the reduction is
-// at chunk c ^ key_row(r): a fragment read's 16 rows hit distinct 16-byte bank
-// groups in each pass of 8 lanes (32 banks) and of 16 (64 banks).
-__device__ __forceinline__ int key_row(int r) { return (r & 6) | ((r ^ (r >> 3)) & 1); }
+// at chunk c ^ (r & 7).  A ds_read_b128 passes 16 lanes at a time, of the first
+// half lanes 0-3, 12-15, 20-23 and 24-27, then the others: rows 0-3 and 12-15 at
+// one chunk with rows 4-11 at the next, which land in 16 different bank groups.
+// (With the key of passes of 8 consecutive lanes every read took twice its time.)
+__device__ __forceinline__ int key_row(int r) { return r & 7; }
 // The same for one that runs along the result: row r is a step of the
 // reduction.  A transposed read's 16 lanes take 32 bytes of 4 rows, its four
 // groups rows 8 apart; fp32 reads 64 bytes of rows 4 apart.
@@ -181,11 +184,14 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
   int64_t a_step, b_step;       // bytes per BK of the reduction
   if constexpr (P == kGradW) {
     const int mts = (p.wide + BM - 1) / BM;
-    const int64_t per = (int64_t)mts * nts;
-    const int64_t t = tile_of_block(block_index(), per * p.E);
-    if (t < 0) return;
-    e = (int)(t / per);
-    const TileAt at = tile_at(t - e * per, mts, nts);
+    // Experts differ in work: each is shared by the XCDs, an eighth of its tiles in
+    // a run (a run of experts per XCD instead: WBALANCE).
+    const int64_t per = (int64_t)mts * nts, run = (per + 7) / 8;
+    const int64_t at8 = block_index() >> 3;
+    e = (int)(at8 / run);
+    const int64_t t = (int64_t)(block_index() & 7) * run + (at8 - e * run);
+    if (t >= per) return;
+    const TileAt at = tile_at(t, mts, nts);
     const ExpertRange r = expert_range(p.offsets, p.R, e);
     L = r.n;
     n0 = at.n * OUTC;
@@ -418,12 +424,12 @@ hipError_t launch_shape(const ExpertGemmArgs& a, bool direct, hipStream_t stream
   constexpr int OUTC = GATED ? S::BN / 2 : S::BN;
   const int ncols = P == kOut ? a.N : a.K;
   const int64_t nts = (ncols + OUTC - 1) / OUTC;
-  const int64_t mts = P == kGradW ? (int64_t)((a.wide + S::BM - 1) / S::BM) * a.E
+  const int64_t mts = P == kGradW ? (a.wide + S::BM - 1) / S::BM
                                   : most_row_tiles<S::BM>(a.offsets, a.R, a.E);
-  const dim3 grid = grid_of((mts * nts + 7) / 8 * 8);
+  const dim3 grid = grid_of((mts * nts + 7) / 8 * 8 * (P == kGradW ? a.E : 1));
   if (direct)
     expert_gemm_kernel<DT, P, S, true, GATED><<<grid, S::THREADS, 0, stream>>>(a);
-  else
+  else if constexpr (S::BM <= 128)
     expert_gemm_kernel<DT, P, S, false, GATED><<<grid, S::THREADS, 0, stream>>>(a);
   return hipGetLastError();
 }
@@ -433,6 +439,11 @@ hipError_t launch_gemm(const ExpertGemmArgs& a, bool direct, hipStream_t stream)
   if constexpr (P != kGradW) {
     if (a.R <= 32 * (int64_t)a.E)
       return launch_shape<DT, P, Tile<64, 128, 1, 4, 2>, GATED>(a, direct, stream);
+  }
+  if constexpr (DT != kF32) {
+    static const int v = getenv("EGV") ? atoi(getenv("EGV")) : 1;
+    if (v == 1 && direct) return launch_shape<DT, P, Tile<256, 256, 2, 4, 1>, GATED>(a, direct, stream);
+    if (v == 2 && direct) return launch_shape<DT, P, Tile<256, 256, 2, 2, 1>, GATED>(a, direct, stream);
   }
   return launch_shape<DT, P, Tile<128, 128, 2, 2, 2>, GATED>(a, direct, stream);
 }

@@ -324,13 +324,14 @@ hipError_t launch_tile(const ExpertW4Args& a, hipStream_t stream) {
 constexpr uint32_t kOutOfRange = 0xF0000000u;    // past every buffer: reads as zeros
 
 // A stage's part for 16 weight rows and H runs: a row's 64 H bytes of codes one
-// after the other, its 16-byte chunk c at c ^ key (the 16 rows of a fragment read
-// then hit distinct bank groups in passes of 8 lanes, 32 banks, and of 16, 64
-// banks); then each row's DW words of scales and, with them, ZW of zero points.
+// after the other, its 16-byte chunk c at c ^ key; then each row's DW words of
+// scales and, with them, ZW of zero points.  A ds_read_b128 passes 16 lanes at a
+// time, rows 0-3 and 12-15 at one chunk with rows 4-11 at the next: the keys put
+// them into 16 different bank groups.
 template <int H>
 __device__ __forceinline__ int key_codes(int r) {
-  if (H == 1) return ((r >> 1) & 2) | (((r >> 1) ^ (r >> 3)) & 1);
-  return (r & 6) | ((r ^ (r >> 3)) & 1);
+  if (H == 1) return (((r >> 1) ^ (r >> 2)) & 2) | (r >> 3);
+  return r & 7;
 }
 
 template <int FMT, int GROUP, int SB, int H>
