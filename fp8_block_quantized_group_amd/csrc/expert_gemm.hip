@@ -310,29 +310,36 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
     for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
   // One barrier per step: behind it this step's tiles are in LDS and the other
-  // pair, read in the step before, is free.
-  if (steps > 0) fetch(0);
-  for (int t = 0; t < steps; ++t) {
-    settle(t);
-    wait_then_barrier<0>();
-    if (t + 1 < steps) fetch(t + 1);
-    const uint8_t* ta = lds + (t & 1) * S::STAGE;
-    const uint8_t* tb = ta + BM * kRowB;
+  // pair, read in the step before, is free.  The wave rows take 16 rows in turn, so
+  // that a tile of few rows is few MFMAs for both: LIVE of the TM.
+  auto loop = [&](auto live) {
+    constexpr int LIVE = decltype(live)::value;
+    for (int t = 0; t < steps; ++t) {
+      settle(t);
+      wait_then_barrier<0>();
+      if (t + 1 < steps) fetch(t + 1);
+      const uint8_t* ta = lds + (t & 1) * S::STAGE;
+      const uint8_t* tb = ta + BM * kRowB;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      u32x4_t fa[TM], fb[TN];
+      for (int s = 0; s < 2; ++s) {
+        u32x4_t fa[LIVE], fb[TN];
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
-        fb[j] = fragment<DT, BR, BN>(tb, wn * WNC + 16 * j, s, lane);
+        for (int j = 0; j < TN; ++j)
+          fb[j] = fragment<DT, BR, BN>(tb, wn * WNC + 16 * j, s, lane);
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
-        fa[i] = fragment<DT, AR, BM>(ta, (wm * TM + i) * 16, s, lane);
+        for (int i = 0; i < LIVE; ++i)
+          fa[i] = fragment<DT, AR, BM>(ta, (i * S::WM + wm) * 16, s, lane);
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < LIVE; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[j], fa[i], acc[i][j]);
+          for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[j], fa[i], acc[i][j]);
+      }
     }
-  }
+  };
+  if (steps > 0) fetch(0);
+  if (TM >= 8 && mrows <= BM / 4) loop(std::integral_constant<int, (TM >= 8 ? TM / 4 : TM)>());
+  else if (TM >= 4 && mrows <= BM / 2) loop(std::integral_constant<int, (TM >= 4 ? TM / 2 : TM)>());
+  else loop(std::integral_constant<int, TM>());
 
   // 16 rows at a time through the wave's own LDS, so that a lane stores 8
   // consecutive columns and the activation's code is there once.
@@ -348,7 +355,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
         RowVec<DT>::template store<false>(row, col + c, limit, RowVec<DT>::pack(f + c));
   };
   for (int i = 0; i < TM; ++i) {
-    const int first = (wm * TM + i) * 16;
+    const int first = (i * S::WM + wm) * 16;
     if (first >= mrows) break;
     wave_lds_order();
     with_constant<TM - 1>(i, [&](auto at) {
