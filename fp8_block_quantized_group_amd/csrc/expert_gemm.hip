@@ -18,7 +18,6 @@
 // the result (W in grad_x, both in grad_W) lies there as it comes and is read
 // transposed by ds_read_b64_tr_b16 (fp32: word by word).  Every product of the
 // 16-bit types is exact and sums are fp32; fp32 goes through the fp32 MFMA.
-#include <stdlib.h>
 #include <type_traits>
 
 #include "expert_act.h"
@@ -39,12 +38,13 @@ typedef __attribute__((address_space(3))) v4s lds_v4s;
 
 constexpr uint32_t kOutOfRange = 0xF0000000u;   // past every buffer: reads as zeros
 constexpr int kRowB = 128;                      // bytes of the reduction per step
+constexpr int kCus = 256;                       // of the card
 
 enum Product { kOut, kGradX, kGradW };
 
-template <int BM_, int BN_, int WM_, int WN_, int PER_CU>
+template <int BM_, int BN_, int WM_, int WN_, int PER_CU_>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, PER_CU = PER_CU_;
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
   static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;   // 16 x 16 tiles of a wave
   static constexpr int WAVES_PER_EU = PER_CU * NW / 4 > 0 ? PER_CU * NW / 4 : 1;
@@ -163,7 +163,22 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
   constexpr int WNC = TN * 16, OUTC = GATED ? BN / 2 : BN;     // result columns of a block
   constexpr int PITCH = WNC + 4;                               // floats of an epilogue row
   constexpr int EPI = S::NW * 16 * PITCH * 4;
-  constexpr int LDS = 2 * S::STAGE > EPI ? 2 * S::STAGE : EPI;
+  // Stages of the ring with LIVE of the TM tiles of rows.  What a tile of few rows
+  // leaves free of LDS holds more of them, two to four: its few MFMAs do not cover
+  // the loads' latency.  Operands in registers on their way (not DIRECT) take two.
+  constexpr bool TRIM = DIRECT && !AR;
+  constexpr int HALF = TM >= 4 ? TM / 2 : TM, QUARTER = TM >= 8 ? TM / 4 : HALF;
+  constexpr auto slot_bytes = [](int live) {
+    return ((TRIM ? BM * live / TM : BM) + BN) * kRowB;
+  };
+  constexpr auto depth = [=](int live) {
+    const int fit = 160 * 1024 / S::PER_CU / slot_bytes(live);
+    return !DIRECT || fit < 2 ? 2 : fit > 4 ? 4 : fit;
+  };
+  constexpr auto most = [](int x, int y) { return x > y ? x : y; };
+  constexpr int LDS = most(most(EPI, depth(TM) * slot_bytes(TM)),
+                           most(depth(HALF) * slot_bytes(HALF),
+                                depth(QUARTER) * slot_bytes(QUARTER)));
   static_assert(LDS <= 160 * 1024, "LDS of a CU");
   __shared__ __align__(1024) uint8_t lds[LDS];
   typedef Slots<DT, AR, BM, S::THREADS> SA;
@@ -249,25 +264,29 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
   u32x4_t a_reg[DIRECT ? 1 : SA::COUNT], b_reg[DIRECT ? 1 : SB::COUNT];
   const uint32_t lds0 = lds_addr(lds);
 
-  // the step's tiles on their way: into LDS, or into registers
-  auto fetch = [&](int t) {
+  // step t's tiles on their way: into LDS (behind the last step zeros from nowhere, so
+  // that as many loads are in flight as ever), or into registers
+  auto fetch = [&](auto live, int t, int slot) {
+    constexpr int LIVE = decltype(live)::value;
+    constexpr int AROWS = TRIM ? BM * LIVE / TM : BM, AC = AROWS * SA::COUNT / BM;
     const uint8_t* at = a + t * a_step;
     const uint8_t* bt = b + t * b_step;
     const int left = L - t * BK;
     if constexpr (DIRECT) {
       const v4i ra = buffer_rsrc(at, kOutOfRange), rb = buffer_rsrc(bt, kOutOfRange);
-      const uint32_t to = lds0 + (t & 1) * S::STAGE + wave * 1024;
+      const uint32_t to = lds0 + slot * slot_bytes(LIVE) + wave * 1024;
 #pragma unroll
-      for (int i = 0; i < SA::COUNT; ++i) {
+      for (int i = 0; i < AC; ++i) {
         const int k = AR ? SA::row(i) : SA::chunk(i) * CE;
         dma16(ra, to + i * S::THREADS * 16, k < left ? a_off[i] : kOutOfRange);
       }
 #pragma unroll
       for (int i = 0; i < SB::COUNT; ++i) {
         const int k = BR ? SB::row(i) : SB::chunk(i) * CE;
-        dma16(rb, to + BM * kRowB + i * S::THREADS * 16, k < left ? b_off[i] : kOutOfRange);
+        dma16(rb, to + AROWS * kRowB + i * S::THREADS * 16, k < left ? b_off[i] : kOutOfRange);
       }
     } else {
+      if (left <= 0) return;
       // rows that are not there load the first one's, which is, and are dropped
 #pragma unroll
       for (int i = 0; i < SA::COUNT; ++i) {
@@ -309,17 +328,26 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // One barrier per step: behind it this step's tiles are in LDS and the other
-  // pair, read in the step before, is free.  The wave rows take 16 rows in turn, so
-  // that a tile of few rows is few MFMAs for both: LIVE of the TM.
+  // One barrier per step: behind it this step's tiles are in LDS and the slot read in
+  // the step before is free.  The wave rows take 16 rows in turn, so that a tile of
+  // few rows is few MFMAs for both: LIVE of the TM.
   auto loop = [&](auto live) {
-    constexpr int LIVE = decltype(live)::value;
+    constexpr int LIVE = decltype(live)::value, D = depth(LIVE);
+    constexpr int AROWS = TRIM ? BM * LIVE / TM : BM;
+    constexpr int LOADS = AROWS * SA::COUNT / BM + SB::COUNT;
+    if (steps > 0) {
+#pragma unroll
+      for (int d = 0; d < D - 1; ++d) fetch(live, d, d);
+    }
+    int slot = 0, next = D - 1;
     for (int t = 0; t < steps; ++t) {
       settle(t);
-      wait_then_barrier<0>();
-      if (t + 1 < steps) fetch(t + 1);
-      const uint8_t* ta = lds + (t & 1) * S::STAGE;
-      const uint8_t* tb = ta + BM * kRowB;
+      wait_then_barrier<DIRECT ? (D - 2) * LOADS : 0>();
+      fetch(live, t + D - 1, next);
+      const uint8_t* ta = lds + slot * slot_bytes(LIVE);
+      const uint8_t* tb = ta + AROWS * kRowB;
+      slot = slot + 1 == D ? 0 : slot + 1;
+      next = next + 1 == D ? 0 : next + 1;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         u32x4_t fa[LIVE], fb[TN];
@@ -335,10 +363,10 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
           for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[j], fa[i], acc[i][j]);
       }
     }
+    if (DIRECT) wait_loads<0>();              // the zeros behind the last step
   };
-  if (steps > 0) fetch(0);
-  if (TM >= 8 && mrows <= BM / 4) loop(std::integral_constant<int, (TM >= 8 ? TM / 4 : TM)>());
-  else if (TM >= 4 && mrows <= BM / 2) loop(std::integral_constant<int, (TM >= 4 ? TM / 2 : TM)>());
+  if (QUARTER < HALF && mrows <= BM / 4) loop(std::integral_constant<int, QUARTER>());
+  else if (HALF < TM && mrows <= BM / 2) loop(std::integral_constant<int, HALF>());
   else loop(std::integral_constant<int, TM>());
 
   // 16 rows at a time through the wave's own LDS, so that a lane stores 8
@@ -426,14 +454,23 @@ __global__ __launch_bounds__(kActThreads) void act_grad_kernel(const ExpertActGr
   if (gated) RV::template store<false>(d + (int64_t)p.N * RV::kSize, col, p.N, RV::pack(u));
 }
 
+typedef Tile<64, 128, 1, 4, 2> Tile64;
+typedef Tile<128, 128, 2, 2, 2> Tile128;
+typedef Tile<256, 256, 2, 4, 1> Tile256;
+
+// Tiles of the result, at most (the rows of an expert are on the device).
+template <class S, Product P, bool GATED>
+int64_t most_tiles(const ExpertGemmArgs& a) {
+  constexpr int OUTC = GATED ? S::BN / 2 : S::BN;
+  const int64_t nts = ((P == kOut ? a.N : a.K) + OUTC - 1) / OUTC;
+  return nts * (P == kGradW ? (int64_t)((a.wide + S::BM - 1) / S::BM) * a.E
+                            : most_row_tiles<S::BM>(a.offsets, a.R, a.E));
+}
+
 template <int DT, Product P, class S, bool GATED>
 hipError_t launch_shape(const ExpertGemmArgs& a, bool direct, hipStream_t stream) {
-  constexpr int OUTC = GATED ? S::BN / 2 : S::BN;
-  const int ncols = P == kOut ? a.N : a.K;
-  const int64_t nts = (ncols + OUTC - 1) / OUTC;
-  const int64_t mts = P == kGradW ? (a.wide + S::BM - 1) / S::BM
-                                  : most_row_tiles<S::BM>(a.offsets, a.R, a.E);
-  const dim3 grid = grid_of((mts * nts + 7) / 8 * 8 * (P == kGradW ? a.E : 1));
+  const int64_t tiles = most_tiles<S, P, GATED>(a), per = P == kGradW ? tiles / a.E : tiles;
+  const dim3 grid = grid_of((per + 7) / 8 * 8 * (P == kGradW ? a.E : 1));
   if (direct)
     expert_gemm_kernel<DT, P, S, true, GATED><<<grid, S::THREADS, 0, stream>>>(a);
   else if constexpr (S::BM <= 128)
@@ -441,18 +478,23 @@ hipError_t launch_shape(const ExpertGemmArgs& a, bool direct, hipStream_t stream
   return hipGetLastError();
 }
 
+// 256 x 256 with a tile for every CU and, of rows, 64 of an expert on average; 64 rows
+// where that makes no more than two tiles per CU; 128 x 128 else.  bf16, out, us in
+// 64 / 128 / 256: 512 x 7168 by 2 x 2048 51 / 76 / 168; 16 experts of 62 rows, 4096 by
+// 2 x 2048 146 / 125 / 148, of 125 178 / 187 / 137; 60 of 133, 2048 by 2 x 1408 239 /
+// 231 / 200; 32 of 512, 4096 by 2 x 2048 - / 731 / 703, of 1024, 7168 - / 2283 / 1963.
 template <int DT, Product P, bool GATED>
 hipError_t launch_gemm(const ExpertGemmArgs& a, bool direct, hipStream_t stream) {
-  if constexpr (P != kGradW) {
-    if (a.R <= 32 * (int64_t)a.E)
-      return launch_shape<DT, P, Tile<64, 128, 1, 4, 2>, GATED>(a, direct, stream);
-  }
   if constexpr (DT != kF32) {
-    static const int v = getenv("EGV") ? atoi(getenv("EGV")) : 1;
-    if (v == 1 && direct) return launch_shape<DT, P, Tile<256, 256, 2, 4, 1>, GATED>(a, direct, stream);
-    if (v == 2 && direct) return launch_shape<DT, P, Tile<256, 256, 2, 2, 1>, GATED>(a, direct, stream);
+    if (direct && most_tiles<Tile256, P, GATED>(a) >= kCus &&
+        (P == kGradW || a.R >= 64 * (int64_t)a.E))
+      return launch_shape<DT, P, Tile256, GATED>(a, direct, stream);
   }
-  return launch_shape<DT, P, Tile<128, 128, 2, 2, 2>, GATED>(a, direct, stream);
+  if constexpr (P != kGradW) {
+    if (most_tiles<Tile64, P, GATED>(a) <= 2 * kCus)
+      return launch_shape<DT, P, Tile64, GATED>(a, direct, stream);
+  }
+  return launch_shape<DT, P, Tile128, GATED>(a, direct, stream);
 }
 
 template <class F>
@@ -464,6 +506,18 @@ hipError_t with_dtype(int dtype, F&& f) {
   }
 }
 
+// Whether launch_expert_few is the faster one: up to 8 rows of an expert on average
+// where the reduction is long enough for its eight waves, or up to 128 of tiles that
+// would leave CUs idle.  us, few / tiles: 256 rows of 64 experts, 4096 by 2 x 1024 179 /
+// 198, 2048 by 4096 212 / 196; 16 of 8, 4096 by 2 x 2048 44 / 69; 100 x 7168 by 2 x 2048
+// 25 / 47, 256 48 / 48; 64 of 256, 2048 by 2 x 512 56 / 47.
+bool few_rows(const ExpertGemmArgs& a) {
+  const int64_t per = ((int64_t)a.R + a.E - 1) / a.E;
+  const int64_t tiles = act_width(a.act) == 2 ? most_tiles<Tile64, kOut, true>(a)
+                                              : most_tiles<Tile64, kOut, false>(a);
+  return (per <= 8 && a.K >= 4096) || (tiles <= kCus && tiles * per <= 8192);
+}
+
 bool aligned16(const void* p, int64_t pitch) { return (((uintptr_t)p | pitch) & 15) == 0; }
 
 }  // namespace
@@ -471,6 +525,8 @@ bool aligned16(const void* p, int64_t pitch) { return (((uintptr_t)p | pitch) & 
 hipError_t launch_expert_out(const ExpertGemmArgs& a, int dtype, hipStream_t stream) {
   const int64_t pitch = (int64_t)a.K * dtype_size(dtype);
   const bool direct = aligned16(a.a, pitch) && aligned16(a.b, pitch);
+  if (direct && dtype != kF32 && few_rows(a))
+    return launch_expert_few(a, dtype, stream);
   return with_dtype(dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     return act_width(a.act) == 2 ? launch_gemm<DT, kOut, true>(a, direct, stream)

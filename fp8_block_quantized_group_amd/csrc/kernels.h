@@ -320,6 +320,8 @@ struct ExpertGemmArgs {
   float limit;
 };
 hipError_t launch_expert_out(const ExpertGemmArgs& a, int dtype, hipStream_t stream);
+// the same for 16-bit rows whose chunks are aligned, few of them per expert
+hipError_t launch_expert_few(const ExpertGemmArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_expert_grad_x(const ExpertGemmArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_expert_grad_w(const ExpertGemmArgs& a, int dtype, hipStream_t stream);
 
