@@ -275,3 +275,177 @@ def test_large_tiles_and_repeats():
         assert torch.equal(a, check_forward(t, last, torch.bfloat16, "silu"))
         assert all(torch.equal(u, v) for u, v in
                    zip(b, check_backward(t, last, torch.bfloat16, "silu")))
+
+
+# ---- the kernels that sizes choose --------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("act", ["none", "silu", "gelu_no_mul"])
+@pytest.mark.parametrize("R,E,K,N,behind", [
+    (1, 1, 4096, 24, 0), (5, 1, 4104, 33, 0), (16, 1, 136, 700, 0), (17, 1, 1000, 40, 0),
+    (70, 1, 264, 50, 0), (128, 1, 72, 24, 0), (12, 6, 4160, 21, 2), (3, 40, 4096, 16, 1),
+    (60, 2, 520, 64, 3), (9, 300, 4096, 8, 0)])
+def test_few_rows_forward(R, E, K, N, behind, act, dtype):
+    t, last = make(R + K, R, E, K, N, dtype, act, behind=behind)
+    check_forward(t, last, dtype, act)
+    check_forward(t, last, dtype, act, keep=False)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+def test_whole_cards_of_large_tiles(dtype):
+    """More than 256 tiles of 256 x 256, ragged on every side: out, grad_x (many
+    columns of the weights) and grad_weight (many experts)."""
+    t, last = make(41, 9000, 3, 72, 2000, dtype, "none", behind=5)
+    check_forward(t, last, dtype, "none")
+    t, last = make(42, 9000, 3, 2072, 40, dtype, "silu", behind=5)
+    check_backward(t, last, dtype, "silu")
+    t, last = make(43, 600, 64, 520, 264, dtype, "silu", behind=5)
+    check_backward(t, last, dtype, "silu")
+
+
+@pytest.mark.parametrize("rows", [1, 40, 65, 129, 200, 256, 257])
+def test_large_tiles_of_few_rows(rows):
+    """Tiles with a quarter, half and all of their rows."""
+    E, N = 40, 2048
+    off = np.minimum(np.arange(E + 1) * 77, 2990)
+    off = np.concatenate([off[:20], off[20:] - off[20] + off[19] + rows])
+    t, last = make(rows, 40 * 77 + 400, E, 64, N, torch.bfloat16, "none",
+                   offsets=off.tolist())
+    check_forward(t, last, torch.bfloat16, "none")
+
+
+@pytest.mark.parametrize("K,N,E,R", [(1, 32768, 2, 9), (32768, 1, 2, 9), (8, 3, 1024, 1),
+                                     (32768, 24, 1, 3)])
+def test_the_ends_of_the_sizes(K, N, E, R):
+    for dtype in (torch.bfloat16, torch.float32):
+        t, last = make(K + N, R, E, K, N, dtype, "none")
+        check_forward(t, last, dtype, "none")
+        check_backward(t, last, dtype, "none")
+
+
+def test_weights_past_four_gib():
+    """All experts' weights are more than 32-bit offsets reach; each alone is not."""
+    E, K, N = 40, 8192, 8192                                   # 5.4 GB of bf16
+    w = torch.zeros((E, N, K), dtype=torch.bfloat16, device="cuda")
+    w[E - 1, N - 1, K - 1] = 3.0
+    x = torch.zeros((80, K), dtype=torch.bfloat16, device="cuda")
+    x[:, K - 1] = torch.arange(80, device="cuda").to(torch.bfloat16)
+    off = (torch.arange(E + 1, device="cuda") * 2).to(torch.int32)
+    p = moe.ExpertLinear(80, K, N, E)
+    out = torch.empty((80, N), dtype=torch.bfloat16, device="cuda")
+    moe.expert_linear(p, x, w, out, expert_offsets=off)
+    want = torch.zeros_like(out)
+    want[78:, N - 1] = 3.0 * x[78:, K - 1]
+    assert torch.equal(out, want)
+    gx = torch.empty_like(x)
+    gw = torch.empty_like(w)
+    moe.expert_linear_backward(p, x, w, out, gx, gw, expert_offsets=off)
+    assert torch.equal(gx[:78], torch.zeros_like(gx[:78]))
+    assert torch.equal(gx[78:, K - 1], 3.0 * out[78:, N - 1])
+    total = (out[78:, N - 1].double() * x[78:, K - 1].double()).sum().to(torch.bfloat16)
+    assert gw[E - 1, N - 1, K - 1] == total and int((gw != 0).sum()) == 1
+
+
+# ---- as they are used together ------------------------------------------------------
+
+def test_a_training_step_around_the_experts():
+    """Router, sorted rows, both linear layers, the weighted combine and every
+    gradient, in fp32, against torch's differentiation in 64 bits.
+
+    Each step is off by a few sums' roundings of its terms; six of them in a chain,
+    of at most 96 terms: 6 * 2 * (96 + 8) * 2^-24 of the gradient's norm, times 8
+    for what cancels: terms of random signs are sqrt(96) / 2 to sqrt(96) times their
+    sum, taken as norms, and errors of random signs add up the same way."""
+    T, H, F, E, k = 50, 96, 64, 6, 2
+    g = torch.Generator().manual_seed(5)
+    x, w1, w2, gy = (torch.randn(s, generator=g) for s in
+                     ((T, H), (E, 2 * F, H), (E, H, F), (T, H)))
+    w1, w2 = w1 * H ** -0.5, w2 * F ** -0.5
+    logits = torch.randn((T, E), generator=g)
+    f32 = torch.float32
+    r = moe.Router(T, E, k)
+    ids = torch.empty((T, k), dtype=torch.int32, device="cuda")
+    wt = torch.empty((T, k), dtype=f32, device="cuda")
+    moe.router_topk(r, logits.cuda(), ids, wt)
+    rows = moe.ExpertRows(T, H, E, k, dtype=f32)
+    s = moe.alloc_permute_outputs(rows)
+    moe.permute(rows, x.cuda(), ids, **s)
+    up = moe.ExpertLinear(T * k, H, F, E, dtype=f32, activation="silu")
+    down = moe.ExpertLinear(T * k, F, H, E, dtype=f32)
+    e = lambda *shape: torch.empty(shape, device="cuda")                # noqa: E731
+    h, pre, yr, y = e(T * k, F), e(T * k, 2 * F), e(T * k, H), e(T, H)
+    W1, W2, off = w1.cuda(), w2.cuda(), s["expert_offsets"]
+    moe.expert_linear(up, s["rows"], W1, h, expert_offsets=off, pre_act=pre)
+    moe.expert_linear(down, h, W2, yr, expert_offsets=off)
+    moe.unpermute(rows, yr, s["slot_row"], wt, y)
+    gr, gw, gh, gx_rows, gx = e(T * k, H), e(T, k), e(T * k, F), e(T * k, H), e(T, H)
+    g1, g2, glog = e(*w1.shape), e(*w2.shape), e(T, E)
+    moe.unpermute_backward(rows, gy.cuda(), yr, s["slot_row"], wt, gr, gw)
+    moe.expert_linear_backward(down, h, W2, gr, gh, g2, expert_offsets=off)
+    moe.expert_linear_backward(up, s["rows"], W1, gh, gx_rows, g1, expert_offsets=off,
+                               pre_act=pre)
+    moe.permute_backward(rows, gx_rows, s["slot_row"], gx)
+    moe.router_topk_backward(r, logits.cuda(), ids, gw, glog)
+
+    d = {n: v.double().requires_grad_() for n, v in
+         dict(x=x, w1=w1, w2=w2, logits=logits).items()}
+    p = torch.softmax(d["logits"], 1).gather(1, ids.cpu().long())
+    p = p / p.sum(1, keepdim=True)
+    at = ids.cpu().long()
+    both = torch.einsum("th,tkfh->tkf", d["x"], d["w1"][at])
+    hd = torch.nn.functional.silu(both[..., :F]) * both[..., F:]
+    yd = (p[:, :, None] * torch.einsum("tkf,tkhf->tkh", hd, d["w2"][at])).sum(1)
+    (yd * gy.double()).sum().backward()
+    yd = yd.detach()
+    bound = 6 * 2 * (96 + 8) * X.U * 8
+    assert float((y.cpu().double() - yd).norm()) <= bound * float(yd.norm())
+    for name, got in (("x", gx), ("w1", g1), ("w2", g2), ("logits", glog)):
+        want = d[name].grad
+        assert float((got.cpu().double() - want).norm()) <= bound * float(want.norm()), name
+
+
+def test_a_decode_step_with_4_bit_experts():
+    """Sorted rows through both 4-bit layers and back, as one captured graph, bit for
+    bit the calls one by one; the same weights as the layer's MXFP4 ones."""
+    T, H, F, E, k = 9, 256, 128, 8, 2
+    rng = np.random.default_rng(2)
+    byte = lambda *s: torch.from_numpy(rng.integers(0, 256, s, dtype=np.uint8)).cuda()  # noqa: E731,E501
+    exps = lambda *s: torch.from_numpy(rng.integers(117, 122, s, dtype=np.uint8)).cuda()  # noqa: E731,E501
+    x = rand(rng, (T, H), torch.bfloat16).cuda()
+    ids = torch.from_numpy(np.argsort(rng.random((T, E)), 1)[:, :k].astype(np.int32)).cuda()
+    wt = torch.from_numpy(rng.random((T, k)).astype(np.float32)).cuda()
+    rows = moe.ExpertRows(T, H, E, k)
+    s = moe.alloc_permute_outputs(rows)
+    up = moe.ExpertLinearW4(T * k, H, F, E, activation="silu", format="mxfp4", group_size=32)
+    down = moe.ExpertLinearW4(T * k, F, H, E, format="int4", group_size=64)
+    c1, s1 = byte(E, 2 * F, H // 2), exps(E, 2 * F, H // 32)
+    c2 = byte(E, H, F // 2)
+    s2 = rand(rng, (E, H, F // 64), torch.bfloat16, 0.02).cuda()
+    h = torch.empty((T * k, F), dtype=torch.bfloat16, device="cuda")
+    yr = torch.empty((T * k, H), dtype=torch.bfloat16, device="cuda")
+    y = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        moe.permute(rows, x, ids, **s)
+        moe.expert_linear_w4(up, s["rows"], c1, s1, h, expert_offsets=s["expert_offsets"])
+        moe.expert_linear_w4(down, h, c2, s2, yr, expert_offsets=s["expert_offsets"])
+        moe.unpermute(rows, yr, s["slot_row"], wt, y)
+
+    step()
+    v1 = X.dequant_w4(c1.cpu().numpy(), s1.cpu().numpy(), "mxfp4")
+    v2 = X.dequant_w4(c2.cpu().numpy(), f64(s2), "int4")
+    off = s["expert_offsets"].cpu().numpy()
+    close(h, *X.linear_w4(f64(s["rows"]), *v1, off, "silu"), "h")
+    close(yr, *X.linear_w4(f64(h), *v2, off), "y rows")
+    want = y.clone()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        step()
+    for turn in range(3):
+        for v in (h, yr, y, s["rows"]):
+            v.fill_(float(turn))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)

@@ -179,3 +179,45 @@ def test_replayed_graph():
         got = out.clone()
         call()
         assert torch.equal(got, out)
+
+
+@pytest.mark.parametrize("form,group", FORMS)
+@pytest.mark.parametrize("R,E,K,N", [
+    (4, 3, 1024, 40), (4, 3, 3968, 40), (4, 3, 4224, 24), (4, 2, 8192, 24), (4, 2, 8320, 24),
+    (3, 2, 4224, 16500), (20, 1, 1024, 24), (40, 1, 1024, 24), (64, 1, 1152, 24),
+    (100, 1, 512, 20)])
+def test_kernels_that_sizes_choose(R, E, K, N, form, group):
+    """x in registers with 8 x 2, 8 x 4 and 16 x 4 runs (the last of many tiles), and
+    streamed, in row tiles of 16 to 64; wholes and parts of the waves' runs."""
+    for act in ("none", "silu"):
+        if N > 10000 and (form != "int4" or group == 32):
+            act = "none"
+        check(*make(R + K, R, E, K, N if act == "none" or N < 10000 else 8300, torch.bfloat16,
+                    form, group, act=act, behind=1 if E > 1 else 0))
+
+
+def test_other_stream_and_two_threads():
+    import threading
+    made = [make(30 + i, 40, 4, 512, 64, torch.float16, "int4_zero", 64, act="silu")
+            for i in range(2)]
+    want = [check(*m) for m in made]
+    got, fail = [None, None], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    got[i] = run(made[i][0], made[i][2])
+                torch.cuda.current_stream().synchronize()
+        except BaseException as e:         # noqa: BLE001 -- handed to the test
+            fail.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not fail, fail
+    for i in range(2):
+        last = made[i][1]
+        assert torch.equal(got[i][:last], want[i][:last])
