@@ -10,7 +10,9 @@
 // (or 32) of each side by side, so that a wave holds both when it stores.
 //
 // One kernel, three forms: a block makes BM x BN of the result in registers
-// from LDS tiles of 128 bytes of the reduction, two of them in turn.  The MFMA's
+// from LDS tiles of 128 bytes of the reduction, a ring of two to four of them (two
+// where the operands' rows are not multiples of 16 bytes: they pass through registers,
+// loaded a step ahead).  The MFMA's
 // A operand is the side of the result's columns and its B operand that of its
 // rows, so a lane holds four consecutive columns of one row.  An operand whose
 // memory runs along the reduction (x and W in out, d in grad_x) lies in LDS as
@@ -18,6 +20,12 @@
 // the result (W in grad_x, both in grad_W) lies there as it comes and is read
 // transposed by ds_read_b64_tr_b16 (fp32: word by word).  Every product of the
 // 16-bit types is exact and sums are fp32; fp32 goes through the fp32 MFMA.
+//
+// A batch's product is bound by the MFMAs under the card's power: 32768 rows of 32
+// experts, 7168 by 2 x 2048, bf16 with silu and the pre-activations kept, 1.9 ms (0.96
+// PFLOP/s; a library's dense product of that size 1.3 ms), the MFMAs busy 55 % of the
+// time at 2.0 GHz.  Register double buffers, wave pairs in turns and more waves in
+// smaller tiles gave nothing.  Products of few rows are bound by the weights' bytes.
 #include <type_traits>
 
 #include "expert_act.h"
@@ -200,7 +208,8 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
   if constexpr (P == kGradW) {
     const int mts = (p.wide + BM - 1) / BM;
     // Experts differ in work: each is shared by the XCDs, an eighth of its tiles in
-    // a run (a run of experts per XCD instead: WBALANCE).
+    // a run (a run of experts per XCD instead: 32
+    // experts of 1024 rows on average, 2 x 2048 by 7168, 2.8 against 2.1 ms).
     const int64_t per = (int64_t)mts * nts, run = (per + 7) / 8;
     const int64_t at8 = block_index() >> 3;
     e = (int)(at8 / run);
@@ -473,21 +482,24 @@ hipError_t launch_shape(const ExpertGemmArgs& a, bool direct, hipStream_t stream
   const dim3 grid = grid_of((per + 7) / 8 * 8 * (P == kGradW ? a.E : 1));
   if (direct)
     expert_gemm_kernel<DT, P, S, true, GATED><<<grid, S::THREADS, 0, stream>>>(a);
-  else if constexpr (S::BM <= 128)
+  else
     expert_gemm_kernel<DT, P, S, false, GATED><<<grid, S::THREADS, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-// 256 x 256 with a tile for every CU and, of rows, 64 of an expert on average; 64 rows
-// where that makes no more than two tiles per CU; 128 x 128 else.  bf16, out, us in
+// 256 x 256 with a tile for every CU and, of rows, 64 of an expert on average (512 where
+// operands pass through registers, which do not load less for a tile of few rows); 64
+// rows where that makes no more than two tiles per CU; 128 x 128 else.  bf16, out, us in
 // 64 / 128 / 256: 512 x 7168 by 2 x 2048 51 / 76 / 168; 16 experts of 62 rows, 4096 by
 // 2 x 2048 146 / 125 / 148, of 125 178 / 187 / 137; 60 of 133, 2048 by 2 x 1408 239 /
-// 231 / 200; 32 of 512, 4096 by 2 x 2048 - / 731 / 703, of 1024, 7168 - / 2283 / 1963.
+// 231 / 200; 32 of 512, 4096 by 2 x 2048 - / 731 / 703, of 1024, 7168 - / 2283 / 1963.  Unaligned, in
+// 128 / 256: 60 experts of 136 rows, 1001 by 2047 136 / 163, their weights' gradient 146
+// / 131; 16 of 512, 2049 by 2047 196 / 183; 8 of 4096, 4097 by 2047 1160 / 1026.
 template <int DT, Product P, bool GATED>
 hipError_t launch_gemm(const ExpertGemmArgs& a, bool direct, hipStream_t stream) {
   if constexpr (DT != kF32) {
-    if (direct && most_tiles<Tile256, P, GATED>(a) >= kCus &&
-        (P == kGradW || a.R >= 64 * (int64_t)a.E))
+    if (most_tiles<Tile256, P, GATED>(a) >= kCus &&
+        (P == kGradW || a.R >= (direct ? 64 : 512) * (int64_t)a.E))
       return launch_shape<DT, P, Tile256, GATED>(a, direct, stream);
   }
   if constexpr (P != kGradW) {
