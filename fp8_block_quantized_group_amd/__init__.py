@@ -861,7 +861,7 @@ def expert_linear_workspace_size(p: ExpertLinear) -> int:
 
 
 def alloc_expert_linear_workspace(p: ExpertLinear, device="cuda") -> Optional[torch.Tensor]:
-    """Scratch of expert_linear_backward; None without an activation."""
+    """Scratch of expert_linear_backward; None where it needs none."""
     n = expert_linear_workspace_size(p)
     return torch.empty(n, dtype=torch.uint8, device=device) if n > 0 else None
 

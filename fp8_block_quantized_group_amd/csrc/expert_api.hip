@@ -77,12 +77,6 @@ moe_status_t check_linear(const moe_expert_linear_t* p) {
   return MOE_OK;
 }
 
-size_t linear_ws_bytes(const moe_expert_linear_t* p) {
-  if (p->activation == MOE_ACT_NONE) return 0;
-  return moe::round_up((size_t)p->num_rows * wide_of(p->out_features, p->activation) *
-                       elem(p->dtype));
-}
-
 moe::ExpertGemmArgs gemm_args(const moe_expert_linear_t* p, const int32_t* offsets) {
   moe::ExpertGemmArgs a{};
   a.offsets = offsets;
@@ -93,7 +87,27 @@ moe::ExpertGemmArgs gemm_args(const moe_expert_linear_t* p, const int32_t* offse
   a.E = p->num_experts;
   a.act = p->activation;
   a.limit = limit_of(p->activation, p->act_limit);
+  a.split = 1;
   return a;
+}
+
+// The backward's workspace: d, then the parts' sums of a split gradient.
+size_t linear_d_bytes(const moe_expert_linear_t* p) {
+  if (p->activation == MOE_ACT_NONE) return 0;
+  return moe::round_up((size_t)p->num_rows * wide_of(p->out_features, p->activation) *
+                       elem(p->dtype));
+}
+size_t linear_ws_bytes(const moe_expert_linear_t* p) {
+  const moe::ExpertGemmArgs a = gemm_args(p, nullptr);
+  const size_t sx = moe::expert_split(a, p->dtype, false), sw = moe::expert_split(a, p->dtype, true);
+  const size_t x = sx > 1 ? sx * a.R * a.K * 4 : 0;
+  const size_t w = sw > 1 ? sw * a.E * a.wide * a.K * 4 : 0;
+  return linear_d_bytes(p) + moe::round_up(std::max(x, w));
+}
+void split_gradient(moe::ExpertGemmArgs& a, int dtype, bool grad_w, void* parts) {
+  a.split = moe::expert_split(a, dtype, grad_w);
+  a.part = (float*)parts;
+  a.part_size = (grad_w ? (int64_t)a.E * a.wide : a.R) * a.K;
 }
 
 moe_status_t check_w4(const moe_expert_linear_w4_t* p) {
@@ -163,12 +177,14 @@ moe_status_t moe_expert_linear_backward(const moe_expert_linear_t* p, const void
     if (grad_x != nullptr) CHECK(check_ptr(weight, "weight", es));
     if (act) {
       CHECK(check_ptr(pre_act, "pre_act", es));
-      CHECK(check_ptr(ws, "ws", 16));
-      if (ws_bytes < linear_ws_bytes(p))
-        return fail(MOE_ERR_WORKSPACE, "expert linear workspace too small: %zu < %zu bytes",
-                    ws_bytes, linear_ws_bytes(p));
     } else if (pre_act != nullptr) {
       return fail(MOE_ERR_INVALID_ARG, "pre_act given without an activation");
+    }
+    if (const size_t need = linear_ws_bytes(p)) {
+      CHECK(check_ptr(ws, "ws", 16));
+      if (ws_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "expert linear workspace too small: %zu < %zu bytes",
+                    ws_bytes, need);
     }
   }
   const hipStream_t s = (hipStream_t)stream;
@@ -190,13 +206,16 @@ moe_status_t moe_expert_linear_backward(const moe_expert_linear_t* p, const void
                         "moe_expert_linear_backward"));
     a.a = (const uint8_t*)ws;
   }
+  void* parts = ws == nullptr ? nullptr : (uint8_t*)ws + linear_d_bytes(p);
   if (grad_x != nullptr && p->num_rows > 0) {
+    split_gradient(a, p->dtype, false, parts);
     a.b = (const uint8_t*)weight;
     a.out = (uint8_t*)grad_x;
     CHECK(launch_status(moe::launch_expert_grad_x(a, p->dtype, s),
                         "moe_expert_linear_backward"));
   }
   if (grad_weight != nullptr) {
+    split_gradient(a, p->dtype, true, parts);
     if (p->num_rows == 0) a.offsets = nullptr;      // R = 0: every expert's range is empty
     a.b = (const uint8_t*)x;
     a.out = (uint8_t*)grad_weight;

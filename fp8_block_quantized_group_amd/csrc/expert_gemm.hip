@@ -26,6 +26,7 @@
 // PFLOP/s; a library's dense product of that size 1.3 ms), the MFMAs busy 55 % of the
 // time at 2.0 GHz.  Register double buffers, wave pairs in turns and more waves in
 // smaller tiles gave nothing.  Products of few rows are bound by the weights' bytes.
+#include <algorithm>
 #include <type_traits>
 
 #include "expert_act.h"
@@ -249,7 +250,15 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
     const int w = j / WNC, q = j % WNC, c = w * (WNC / 2) + q % (WNC / 2);
     return n0 + c < p.N ? (q < WNC / 2 ? c : p.N + c) : -1;
   };
-  const int steps = (L + BK - 1) / BK;
+  int steps = (L + BK - 1) / BK;
+  if (P != kOut && p.split > 1) {              // this block's part of the reduction
+    const int s = blockIdx.z, t0 = (int)((int64_t)steps * s / p.split);
+    const int t1 = (int)((int64_t)steps * (s + 1) / p.split);
+    a += t0 * a_step;
+    b += t0 * b_step;
+    L = min(L, t1 * BK) - t0 * BK;
+    steps = t1 - t0;
+  }
 
   uint32_t a_off[SA::COUNT], b_off[SB::COUNT];    // DIRECT: from the step's first element
   if constexpr (DIRECT) {
@@ -337,6 +346,29 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
+  // fp32: the products' sums are added up every 8 steps (256 terms), so that a long
+  // reduction's error grows with the root of its 256ths: 8192 terms, 2e-6 of the
+  // result in one chain.  The 16-bit types' rounding hides a chain's 2^-24 per term.
+  constexpr bool BLOCKED = DT == kF32;
+  v4f total[BLOCKED ? TM : 1][BLOCKED ? TN : 1];
+  if constexpr (BLOCKED) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) total[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  auto add_up = [&](auto live) {
+    if constexpr (BLOCKED) {
+#pragma unroll
+      for (int i = 0; i < decltype(live)::value; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          total[i][j] += acc[i][j];
+          acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+    }
+  };
+
   // One barrier per step: behind it this step's tiles are in LDS and the slot read in
   // the step before is free.  The wave rows take 16 rows in turn, so that a tile of
   // few rows is few MFMAs for both: LIVE of the TM.
@@ -371,7 +403,9 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
 #pragma unroll
           for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[j], fa[i], acc[i][j]);
       }
+      if (BLOCKED && (t & 7) == 7) add_up(live);
     }
+    add_up(live);
     if (DIRECT) wait_loads<0>();              // the zeros behind the last step
   };
   if (QUARTER < HALF && mrows <= BM / 4) loop(std::integral_constant<int, QUARTER>());
@@ -399,7 +433,8 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
 #pragma unroll
       for (int j = 0; j < TN; ++j)
         *reinterpret_cast<v4f*>(mine + (lane & 15) * PITCH + 16 * j + (lane >> 4) * 4) =
-            acc[decltype(at)::value][j];
+            BLOCKED ? total[BLOCKED ? decltype(at)::value : 0][BLOCKED ? j : 0]
+                    : acc[decltype(at)::value][j];
     });
     wave_lds_order();
     constexpr int LANES = WNC / (GATED ? 2 : 1) / 8;      // that share a row
@@ -421,6 +456,17 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
       if (P == kOut && p.act != kActNone) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) g[c] = apply_act(p.act, g[c], u[c], p.limit);
+      }
+      if (P != kOut && p.split > 1) {          // a part's sums, unrounded
+        float* part = p.part + (int64_t)blockIdx.z * p.part_size +
+                      (P == kGradW ? (int64_t)e * p.wide : 0) * ncols +
+                      (row0 + first + r) * ncols;
+#pragma unroll
+        for (int c = 0; c < 8; c += 4)
+          if (col + c < ncols)
+            RowVec<kF32>::template store<false>(reinterpret_cast<uint8_t*>(part), col + c, ncols,
+                                                RowVec<kF32>::pack(g + c));
+        continue;
       }
       store8(out + (first + r) * out_pitch, col, ncols, g);
     }
@@ -463,6 +509,18 @@ __global__ __launch_bounds__(kActThreads) void act_grad_kernel(const ExpertActGr
   if (gated) RV::template store<false>(d + (int64_t)p.N * RV::kSize, col, p.N, RV::pack(u));
 }
 
+// The parts' sums in their order, rounded once; rows: those that are there.
+template <int DT>
+__global__ __launch_bounds__(kActThreads) void add_parts_kernel(const ExpertGemmArgs p,
+                                                                bool by_rows) {
+  const int64_t at = (int64_t)block_index() * kActThreads + threadIdx.x;
+  const int rows = p.offsets == nullptr ? p.R : min(max(p.offsets[p.E], 0), p.R);
+  if (at >= (by_rows ? (int64_t)rows * p.K : p.part_size)) return;
+  float f = 0.0f;
+  for (int s = 0; s < p.split; ++s) f += p.part[s * p.part_size + at];
+  RowVec<DT>::store_one(p.out, at, f);
+}
+
 typedef Tile<64, 128, 1, 4, 2> Tile64;
 typedef Tile<128, 128, 2, 2, 2> Tile128;
 typedef Tile<256, 256, 2, 4, 1> Tile256;
@@ -479,7 +537,8 @@ int64_t most_tiles(const ExpertGemmArgs& a) {
 template <int DT, Product P, class S, bool GATED>
 hipError_t launch_shape(const ExpertGemmArgs& a, bool direct, hipStream_t stream) {
   const int64_t tiles = most_tiles<S, P, GATED>(a), per = P == kGradW ? tiles / a.E : tiles;
-  const dim3 grid = grid_of((per + 7) / 8 * 8 * (P == kGradW ? a.E : 1));
+  dim3 grid = grid_of((per + 7) / 8 * 8 * (P == kGradW ? a.E : 1));
+  if (P != kOut) grid.z = a.split;
   if (direct)
     expert_gemm_kernel<DT, P, S, true, GATED><<<grid, S::THREADS, 0, stream>>>(a);
   else
@@ -497,6 +556,15 @@ hipError_t launch_shape(const ExpertGemmArgs& a, bool direct, hipStream_t stream
 // / 131; 16 of 512, 2049 by 2047 196 / 183; 8 of 4096, 4097 by 2047 1160 / 1026.
 template <int DT, Product P, bool GATED>
 hipError_t launch_gemm(const ExpertGemmArgs& a, bool direct, hipStream_t stream) {
+  if constexpr (P != kOut) {
+    if (a.split > 1) {
+      const hipError_t err = launch_shape<DT, P, Tile128, GATED>(a, direct, stream);
+      if (err != hipSuccess) return err;
+      add_parts_kernel<DT><<<grid_of((a.part_size + kActThreads - 1) / kActThreads), kActThreads,
+                             0, stream>>>(a, P == kGradX);
+      return hipGetLastError();
+    }
+  }
   if constexpr (DT != kF32) {
     if (most_tiles<Tile256, P, GATED>(a) >= kCus &&
         (P == kGradW || a.R >= (direct ? 64 : 512) * (int64_t)a.E))
@@ -533,6 +601,22 @@ bool few_rows(const ExpertGemmArgs& a) {
 bool aligned16(const void* p, int64_t pitch) { return (((uintptr_t)p | pitch) & 15) == 0; }
 
 }  // namespace
+
+// A gradient whose tiles of 128 x 128 leave half of the CUs or more without one is split
+// along its reduction (grad_x: the weights' rows; grad_weight: an expert's rows, of
+// which the host knows the average), 8 steps or more to a part, at most two tiles per CU:
+// under 512 parts of tiles of 64 KB.
+// SPLITFIG
+int expert_split(const ExpertGemmArgs& a, int dtype, bool grad_w) {
+  const auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  const int bk = kRowB / dtype_size(dtype);
+  const int64_t nts = up(a.K, 128);
+  const int64_t tiles = grad_w ? nts * up(a.wide, 128) * a.E
+                               : nts * (a.R / 128 + std::min(a.R, a.E));
+  const int64_t steps = up(grad_w ? up(a.R, a.E) : a.wide, bk);
+  if (tiles == 0 || tiles > kCus / 2) return 1;
+  return (int)std::max<int64_t>(1, std::min(2 * kCus / tiles, steps / 8));
+}
 
 hipError_t launch_expert_out(const ExpertGemmArgs& a, int dtype, hipStream_t stream) {
   const int64_t pitch = (int64_t)a.K * dtype_size(dtype);

@@ -318,7 +318,11 @@ struct ExpertGemmArgs {
   int R, K, N, wide, E;        // wide: columns before the activation, N or 2N
   int act;                     // moe_act_t or kActNone; out only
   float limit;
+  int split;                   // gradients: parts of the reduction (expert_split)
+  float* part;                 // [split, part_size] where there are several
+  int64_t part_size;           // of the result
 };
+int expert_split(const ExpertGemmArgs& a, int dtype, bool grad_w);
 hipError_t launch_expert_out(const ExpertGemmArgs& a, int dtype, hipStream_t stream);
 // the same for 16-bit rows whose chunks are aligned, few of them per expert
 hipError_t launch_expert_few(const ExpertGemmArgs& a, int dtype, hipStream_t stream);

@@ -721,8 +721,10 @@ moe_status_t moe_expert_linear(const moe_expert_linear_t* p, const void* x,
                                const int32_t* expert_offsets, const void* weight, void* out,
                                void* pre_act, void* stream);
 
-/* Device scratch bytes of moe_expert_linear_backward (host only; 0 without an
- * activation): the pre-activations' gradient, [R, wide] in dtype. */
+/* Device scratch bytes of moe_expert_linear_backward (host only; may be 0): with an
+ * activation the pre-activations' gradient, [R, wide] in dtype; for results too small
+ * to fill the card the fp32 sums of parts of the reduction, up to 32 MiB, which are
+ * added up in their order. */
 moe_status_t moe_expert_linear_workspace_size(const moe_expert_linear_t* p, size_t* bytes);
 
 /* With d = grad_out F'(pre_act), rounded to dtype (grad_out itself without an

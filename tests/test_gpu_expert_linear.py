@@ -449,3 +449,67 @@ def test_a_decode_step_with_4_bit_experts():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+# ---- gradients whose reduction is split -----------------------------------------------
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("R,E,K,N,behind", [
+    (2100, 1, 136, 200, 0), (1999, 1, 77, 131, 0), (3000, 2, 264, 72, 3), (5, 1, 72, 2400, 0),
+    (70, 3, 40, 1500, 1), (33, 1, 129, 2047, 0), (4000, 3, 8, 8, 7)])
+def test_split_gradients(R, E, K, N, behind, dtype, act):
+    p = moe.ExpertLinear(R, K, N, E, dtype=dtype, activation=act)
+    d = 0 if act == "none" else R * p.wide * dtype.itemsize
+    assert moe.expert_linear_workspace_size(p) > d + 512            # there are parts
+    t, last = make(R + K, R, E, K, N, dtype, act, behind=behind)
+    check_backward(t, last, dtype, act)
+
+
+def test_split_gradients_of_one_expert_with_all_rows():
+    off = [0, 0, 0, 2990, 2990]
+    t, last = make(8, 3000, 4, 136, 100, torch.bfloat16, "silu", offsets=off)
+    check_backward(t, last, torch.bfloat16, "silu")
+
+
+def test_split_gradients_replayed():
+    """One captured graph, its workspace dirty before every replay, with other rows per
+    expert in each."""
+    R, K, N, E = 3000, 264, 72, 2
+    p = moe.ExpertLinear(R, K, N, E, activation="silu")
+    rng = np.random.default_rng(4)
+    dev = lambda *s: rand(rng, s, torch.bfloat16).cuda()               # noqa: E731
+    x, w, g, pre = dev(R, K), dev(E, 2 * N, K), dev(R, N), dev(R, 2 * N)
+    off = torch.tensor([0, 100, R], dtype=torch.int32, device="cuda")
+    gx, gw = torch.empty_like(x), torch.empty_like(w)
+    ws = moe.alloc_expert_linear_workspace(p)
+    call = lambda a, b, s: moe.expert_linear_backward(                  # noqa: E731
+        p, x, w, g, a, b, expert_offsets=off, pre_act=pre, ws=s)
+    call(gx, gw, ws)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        call(gx, gw, ws)
+    for first in (0, 1700, 3000):
+        off[1] = first
+        for v in (gx, gw):
+            v.fill_(7.0)
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        ax, aw = torch.empty_like(x), torch.empty_like(w)
+        call(ax, aw, "auto")
+        assert torch.equal(gx, ax) and torch.equal(gw, aw)
+
+
+def test_long_sums_of_fp32():
+    """32768 terms: parts of 256 are summed first, so the error is that of 256 + 128
+    additions in a chain at most, not of 32768."""
+    g = torch.Generator().manual_seed(3)
+    x, w = torch.rand((40, 32768), generator=g), torch.rand((1, 24, 32768), generator=g)
+    p = moe.ExpertLinear(40, 32768, 24, 1, dtype=torch.float32)
+    out = torch.empty((40, 24), device="cuda")
+    moe.expert_linear(p, x.cuda(), w.cuda(), out)
+    want = x.double() @ w[0].double().T
+    assert float(((out.cpu().double() - want) / want).abs().max()) <= (256 + 128) * X.U

@@ -288,3 +288,28 @@ def test_block_refuses_staged_rows_it_cannot_use():
     p, layer, inp = layer_of("bf16", "fp8_block128")
     with pytest.raises(ValueError, match="bf16"):
         moe.MoeBlock(layer, block.router, block.router_weight, block.norm, staged=True)
+
+
+@pytest.mark.parametrize("act,weight", PAIRS)
+def test_layer_on_staged_slabs(act, weight):
+    """The batched layout: slabs of staged rows, counts from the dispatch."""
+    p, layer, inp = layer_of(act, weight, "batched", T=250, max_tokens=160, pad_frac=0.0)
+    n = inp["expert_num_tokens"]
+    bufs = moe.alloc_stage_outputs(p)
+    moe.stage(p, inp["hidden"], inp["topk_ids"], inp["topk_weights"], bufs, expert_num_tokens=n)
+    want = layer(inp["hidden"], inp["topk_ids"], inp["topk_weights"], expert_num_tokens=n)
+    out = layer.quantized(bufs["x_q"], bufs["x_sf"], inp["topk_ids"], inp["topk_weights"],
+                          expert_num_tokens=n)
+    assert torch.equal(out, want)
+
+
+def test_layer_on_staged_rows_of_two_lists_with_padding():
+    """More than 128 rows of an expert, a quarter of the tokens padding."""
+    p, layer, inp = layer_of("ue8m0", "fp8_block128", T=2500)
+    pad = (torch.arange(2500, device="cuda") % 4 == 1).to(torch.uint8)
+    bufs = moe.alloc_stage_outputs(p)
+    moe.stage(p, inp["hidden"], inp["topk_ids"], inp["topk_weights"], bufs, is_padding=pad)
+    want = layer(inp["hidden"], inp["topk_ids"], inp["topk_weights"], is_padding=pad)
+    out = layer.quantized(bufs["x_q"], bufs["x_sf"], inp["topk_ids"], inp["topk_weights"],
+                          is_padding=pad)
+    assert torch.equal(out, want)
