@@ -227,7 +227,7 @@ def test_staged_rows_arguments(lib):
 
 def test_linear_workspace_of_split_gradients(lib):
     """No activation, but few results of long sums: their parts need a workspace."""
-    p = moe.ExpertLinear(2100, 136, 200, 1)
+    p = moe.ExpertLinear(6300, 136, 200, 1)
     n = moe.expert_linear_workspace_size(p)
     assert 0 < n <= 32 << 20
     bwd = lib.moe_expert_linear_backward
@@ -235,7 +235,7 @@ def test_linear_workspace_of_split_gradients(lib):
     refused(lib, bwd(p._ref, *args, None, n, None), -1, "ws is NULL")
     refused(lib, bwd(p._ref, *args, ODD, n, None), -1, "ws")
     refused(lib, bwd(p._ref, *args, V, n - 1, None), -3, "workspace")
-    for R in (1, 100, 2000, 32768, 1 << 20):
+    for R in (1, 100, 6000, 32768, 1 << 20):
         for K, N, E in ((64, 64, 1), (4096, 4096, 1), (32768, 64, 1), (64, 32768, 3),
                         (7168, 2048, 32), (8, 8, 1024)):
             p = moe.ExpertLinear(R, K, N, E)

@@ -456,8 +456,8 @@ def test_a_decode_step_with_4_bit_experts():
 @pytest.mark.parametrize("act", ["none", "silu"])
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("R,E,K,N,behind", [
-    (2100, 1, 136, 200, 0), (1999, 1, 77, 131, 0), (3000, 2, 264, 72, 3), (5, 1, 72, 2400, 0),
-    (70, 3, 40, 1500, 1), (33, 1, 129, 2047, 0), (4000, 3, 8, 8, 7)])
+    (6300, 1, 136, 200, 0), (6999, 1, 77, 131, 0), (9000, 2, 264, 72, 3), (5, 1, 72, 4400, 0),
+    (70, 3, 40, 3500, 1), (33, 1, 129, 4047, 0), (9500, 3, 8, 8, 7)])
 def test_split_gradients(R, E, K, N, behind, dtype, act):
     p = moe.ExpertLinear(R, K, N, E, dtype=dtype, activation=act)
     d = 0 if act == "none" else R * p.wide * dtype.itemsize
@@ -467,15 +467,15 @@ def test_split_gradients(R, E, K, N, behind, dtype, act):
 
 
 def test_split_gradients_of_one_expert_with_all_rows():
-    off = [0, 0, 0, 2990, 2990]
-    t, last = make(8, 3000, 4, 136, 100, torch.bfloat16, "silu", offsets=off)
+    off = [0, 0, 0, 12990, 12990]
+    t, last = make(8, 13000, 4, 136, 100, torch.bfloat16, "silu", offsets=off)
     check_backward(t, last, torch.bfloat16, "silu")
 
 
 def test_split_gradients_replayed():
     """One captured graph, its workspace dirty before every replay, with other rows per
     expert in each."""
-    R, K, N, E = 3000, 264, 72, 2
+    R, K, N, E = 6500, 264, 72, 2
     p = moe.ExpertLinear(R, K, N, E, activation="silu")
     rng = np.random.default_rng(4)
     dev = lambda *s: rand(rng, s, torch.bfloat16).cuda()               # noqa: E731
@@ -491,7 +491,7 @@ def test_split_gradients_replayed():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=st):
         call(gx, gw, ws)
-    for first in (0, 1700, 3000):
+    for first in (0, 1700, 6500):
         off[1] = first
         for v in (gx, gw):
             v.fill_(7.0)
