@@ -57,7 +57,6 @@ struct Tile {
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
   static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;   // 16 x 16 tiles of a wave
   static constexpr int WAVES_PER_EU = PER_CU * NW / 4 > 0 ? PER_CU * NW / 4 : 1;
-  static constexpr int STAGE = (BM + BN) * kRowB;
   static_assert(TN % 2 == 0, "gate and up in one wave");
 };
 
@@ -175,7 +174,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
   // Stages of the ring with LIVE of the TM tiles of rows.  What a tile of few rows
   // leaves free of LDS holds more of them, two to four: its few MFMAs do not cover
   // the loads' latency.  Operands in registers on their way (not DIRECT) take two.
-  constexpr bool TRIM = DIRECT && !AR;
+  constexpr bool TRIM = !AR;
   constexpr int HALF = TM >= 4 ? TM / 2 : TM, QUARTER = TM >= 8 ? TM / 4 : HALF;
   constexpr auto slot_bytes = [](int live) {
     return ((TRIM ? BM * live / TM : BM) + BN) * kRowB;
@@ -307,7 +306,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
       if (left <= 0) return;
       // rows that are not there load the first one's, which is, and are dropped
 #pragma unroll
-      for (int i = 0; i < SA::COUNT; ++i) {
+      for (int i = 0; i < AC; ++i) {
         const int r = SA::row(i), c = SA::chunk(i) * CE;
         a_reg[i] = load_chunk<DT>(at + (int64_t)(r < (AR ? left : mrows) ? r : 0) * a_pitch, c,
                                   AR ? mrows : left);
@@ -320,12 +319,14 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
       }
     }
   };
-  auto settle = [&](int t) {
+  auto settle = [&](auto live, int t) {
     if constexpr (!DIRECT) {
+      constexpr int LIVE = decltype(live)::value;
+      constexpr int AROWS = TRIM ? BM * LIVE / TM : BM, AC = AROWS * SA::COUNT / BM;
       const int left = L - t * BK;
-      uint8_t* to = lds + (t & 1) * S::STAGE + threadIdx.x * 16;
+      uint8_t* to = lds + (t & 1) * slot_bytes(LIVE) + threadIdx.x * 16;
 #pragma unroll
-      for (int i = 0; i < SA::COUNT; ++i) {
+      for (int i = 0; i < AC; ++i) {
         const int r = SA::row(i), c = SA::chunk(i) * CE;
         settle_chunk<DT>(a_reg[i], c, AR ? mrows : left, r < (AR ? left : mrows));
         *reinterpret_cast<u32x4_t*>(to + i * S::THREADS * 16) = a_reg[i];
@@ -335,7 +336,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
         const int r = SB::row(i), c = SB::chunk(i) * CE;
         settle_chunk<DT>(b_reg[i], c, BR ? ncols - n0 : left,
                          BR ? r < left : weight_row(r) >= 0);
-        *reinterpret_cast<u32x4_t*>(to + BM * kRowB + i * S::THREADS * 16) = b_reg[i];
+        *reinterpret_cast<u32x4_t*>(to + AROWS * kRowB + i * S::THREADS * 16) = b_reg[i];
       }
     }
   };
@@ -382,7 +383,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
     }
     int slot = 0, next = D - 1;
     for (int t = 0; t < steps; ++t) {
-      settle(t);
+      settle(live, t);
       wait_then_barrier<DIRECT ? (D - 2) * LOADS : 0>();
       fetch(live, t + D - 1, next);
       const uint8_t* ta = lds + slot * slot_bytes(LIVE);
@@ -546,14 +547,15 @@ hipError_t launch_shape(const ExpertGemmArgs& a, bool direct, hipStream_t stream
   return hipGetLastError();
 }
 
-// 256 x 256 with a tile for every CU and, of rows, 64 of an expert on average (512 where
-// operands pass through registers, which do not load less for a tile of few rows); 64
-// rows where that makes no more than two tiles per CU; 128 x 128 else.  bf16, out, us in
-// 64 / 128 / 256: 512 x 7168 by 2 x 2048 51 / 76 / 168; 16 experts of 62 rows, 4096 by
-// 2 x 2048 146 / 125 / 148, of 125 178 / 187 / 137; 60 of 133, 2048 by 2 x 1408 239 /
-// 231 / 200; 32 of 512, 4096 by 2 x 2048 - / 731 / 703, of 1024, 7168 - / 2283 / 1963.  Unaligned, in
-// 128 / 256: 60 experts of 136 rows, 1001 by 2047 136 / 163, their weights' gradient 146
-// / 131; 16 of 512, 2049 by 2047 196 / 183; 8 of 4096, 4097 by 2047 1160 / 1026.
+// 256 x 256 with a tile for every CU and, of rows, 64 of an expert on average (1024 where
+// operands pass through registers: half a tile of the larger ones is then dear); 64 rows
+// where that makes no more than two tiles per CU; 128 x 128 else.  bf16, out, us in 64 /
+// 128 / 256: 512 x 7168 by 2 x 2048 51 / 76 / 168; 16 experts of 62 rows, 4096 by 2 x
+// 2048 146 / 125 / 148, of 125 178 / 187 / 137; 60 of 133, 2048 by 2 x 1408 239 / 231 /
+// 200; 32 of 512, 4096 by 2 x 2048 - / 731 / 703, of 1024, 7168 - / 2283 / 1963.
+// Unaligned, in 128 / 256: 60 experts of 136 rows, 1001 by 2047 133 / 166, their weights'
+// gradient 146 / 132; 2049 by 2047, 32 of 256 rows 238 / 224, 16 of 512 183 / 196, of 1024
+// 303 / 294; 8 of 4096, 4097 by 2047 1160 / 1023.
 template <int DT, Product P, bool GATED>
 hipError_t launch_gemm(const ExpertGemmArgs& a, bool direct, hipStream_t stream) {
   if constexpr (P != kOut) {
@@ -567,7 +569,7 @@ hipError_t launch_gemm(const ExpertGemmArgs& a, bool direct, hipStream_t stream)
   }
   if constexpr (DT != kF32) {
     if (most_tiles<Tile256, P, GATED>(a) >= kCus &&
-        (P == kGradW || a.R >= (direct ? 64 : 512) * (int64_t)a.E))
+        (P == kGradW || a.R >= (direct ? 64 : 1024) * (int64_t)a.E))
       return launch_shape<DT, P, Tile256, GATED>(a, direct, stream);
   }
   if constexpr (P != kGradW) {

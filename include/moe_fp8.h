@@ -772,7 +772,9 @@ typedef struct {
  * alone, zeros uint8 of the scales' shape (any value counts as it is).  The
  * weights are used as the exact products of scale and code; sums are fp32.
  * Made for decode batches: every 64 rows of an expert (32 of fp32) read its
- * weights once.  A row with an infinity or a NaN gives infinities or NaN. */
+ * weights once.  A row with an infinity or a NaN gives infinities or NaN, and
+ * so may a bf16 row where a group's sum of 384 |x| passes fp32's range (codes
+ * are multiplied as 128 + q and the zero is taken off the sum). */
 moe_status_t moe_expert_linear_w4(const moe_expert_linear_w4_t* p, const void* x,
                                   const int32_t* expert_offsets, const void* codes,
                                   const void* scales, const void* zeros, void* out,

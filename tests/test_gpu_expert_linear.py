@@ -303,6 +303,16 @@ def test_whole_cards_of_large_tiles(dtype):
     check_backward(t, last, dtype, "silu")
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+def test_whole_cards_of_large_unaligned_tiles(dtype):
+    t, last = make(44, 4500, 2, 77, 4001, dtype, "none", behind=5)
+    check_forward(t, last, dtype, "none")
+    t, last = make(45, 4500, 2, 4001, 27, dtype, "silu", behind=5)
+    check_backward(t, last, dtype, "silu")
+    t, last = make(46, 600, 64, 519, 263, dtype, "silu", behind=5)
+    check_backward(t, last, dtype, "silu")
+
+
 @pytest.mark.parametrize("rows", [1, 40, 65, 129, 200, 256, 257])
 def test_large_tiles_of_few_rows(rows):
     """Tiles with a quarter, half and all of their rows."""
