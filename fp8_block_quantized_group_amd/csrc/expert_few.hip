@@ -176,7 +176,7 @@ hipError_t launch_strips(const ExpertGemmArgs& a, hipStream_t stream) {
   const int64_t tiles =
       most_row_tiles<16 * MT>(a.offsets, a.R, a.E) * ((a.N + OUTC - 1) / OUTC);
   expert_few_kernel<DT, GATED, MT, NT>
-      <<<grid_of((tiles + 7) / 8 * 8), 64 * kWaves, 0, stream>>>(a);
+      <<<grid_of(blocks_of_tiles(tiles)), 64 * kWaves, 0, stream>>>(a);
   return hipGetLastError();
 }
 

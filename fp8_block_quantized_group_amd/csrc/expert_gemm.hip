@@ -207,15 +207,10 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
   int64_t a_step, b_step;       // bytes per BK of the reduction
   if constexpr (P == kGradW) {
     const int mts = (p.wide + BM - 1) / BM;
-    // Experts differ in work: each is shared by the XCDs, an eighth of its tiles in
-    // a run (a run of experts per XCD instead: 32
-    // experts of 1024 rows on average, 2 x 2048 by 7168, 2.8 against 2.1 ms).
-    const int64_t per = (int64_t)mts * nts, run = (per + 7) / 8;
-    const int64_t at8 = block_index() >> 3;
-    e = (int)(at8 / run);
-    const int64_t t = (int64_t)(block_index() & 7) * run + (at8 - e * run);
-    if (t >= per) return;
-    const TileAt at = tile_at(t, mts, nts);
+    const ExpertTile w = expert_tile_of_block(block_index(), (int64_t)mts * nts, p.E);
+    if (w.e < 0) return;
+    e = w.e;
+    const TileAt at = tile_at(w.t, mts, nts);
     const ExpertRange r = expert_range(p.offsets, p.R, e);
     L = r.n;
     n0 = at.n * OUTC;
@@ -538,7 +533,7 @@ int64_t most_tiles(const ExpertGemmArgs& a) {
 template <int DT, Product P, class S, bool GATED>
 hipError_t launch_shape(const ExpertGemmArgs& a, bool direct, hipStream_t stream) {
   const int64_t tiles = most_tiles<S, P, GATED>(a), per = P == kGradW ? tiles / a.E : tiles;
-  dim3 grid = grid_of((per + 7) / 8 * 8 * (P == kGradW ? a.E : 1));
+  dim3 grid = grid_of(blocks_of_tiles(per) * (P == kGradW ? a.E : 1));
   if (P != kOut) grid.z = a.split;
   if (direct)
     expert_gemm_kernel<DT, P, S, true, GATED><<<grid, S::THREADS, 0, stream>>>(a);

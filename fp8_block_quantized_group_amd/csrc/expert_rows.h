@@ -2,8 +2,7 @@
 // sorted by expert.
 #pragma once
 
-#include <hip/hip_runtime.h>
-#include <stdint.h>
+#include "grid_map.h"
 
 namespace moe {
 
@@ -16,26 +15,6 @@ __device__ __forceinline__ ExpertRange expert_range(const int32_t* off, int R, i
   if (off == nullptr) return ExpertRange{0, R};
   const int a = min(max(off[e], 0), R), b = min(max(off[e + 1], a), R);
   return ExpertRange{a, b - a};
-}
-
-// Block b's tile of `live` ones.  Consecutive blocks run on the 8 XCDs in turn;
-// each takes a run of consecutive tiles, whose operands its L2 then shares.
-// -1: none.
-__device__ __forceinline__ int64_t tile_of_block(int64_t b, int64_t live) {
-  const int64_t run = (live + 7) / 8, t = (b & 7) * run + (b >> 3);
-  return (b >> 3) < run && t < live ? t : -1;
-}
-
-// Tile t of mts x nts, walked in bands of 8 rows of tiles, down each band first.
-struct TileAt {
-  int m, n;
-};
-constexpr int kBand = 8;
-__device__ __forceinline__ TileAt tile_at(int64_t t, int mts, int nts) {
-  const int64_t per = (int64_t)kBand * nts;
-  const int band = (int)(t / per), rest = (int)(t - band * per);
-  const int h = min(kBand, mts - band * kBand);
-  return TileAt{band * kBand + rest % h, rest / h};
 }
 
 // The rows' tile for this block: the tiles of all experts with rows, in their

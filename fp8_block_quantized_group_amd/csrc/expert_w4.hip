@@ -316,7 +316,7 @@ hipError_t launch_tile(const ExpertW4Args& a, hipStream_t stream) {
   const int64_t tiles =
       most_row_tiles<16 * MT>(a.offsets, a.R, a.E) * ((a.N + outc - 1) / outc);
   expert_w4_kernel<DT, MX, GROUP, S32, MT, NT>
-      <<<grid_of((tiles + 7) / 8 * 8), 64 * kWaves, 0, stream>>>(a);
+      <<<grid_of(blocks_of_tiles(tiles)), 64 * kWaves, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -730,7 +730,7 @@ hipError_t launch_few(const ExpertW4Args& a, hipStream_t stream) {
   const int64_t row_tiles = most_row_tiles<16>(a.offsets, a.R, a.E);
   int per = 16;
   while (per > 1 && row_tiles * ((tiles + per - 1) / per) < 512) per /= 2;
-  const dim3 grid = grid_of((row_tiles * ((tiles + per - 1) / per) + 7) / 8 * 8);
+  const dim3 grid = grid_of(blocks_of_tiles(row_tiles * ((tiles + per - 1) / per)));
   if (a.wide != a.N)
     expert_w4_few_kernel<DT, FMT, GROUP, S32, W, RW, true><<<grid, 64 * W, 0, stream>>>(a, per);
   else
@@ -741,7 +741,7 @@ hipError_t launch_few(const ExpertW4Args& a, hipStream_t stream) {
 template <int DT, int FMT, int GROUP, bool S32, int MT, int W>
 hipError_t launch_runs(const ExpertW4Args& a, hipStream_t stream) {
   const int64_t row_tiles = most_row_tiles<16 * MT>(a.offsets, a.R, a.E);
-  const dim3 grid = grid_of((row_tiles * ((a.N + 15) / 16) + 7) / 8 * 8);
+  const dim3 grid = grid_of(blocks_of_tiles(row_tiles * ((a.N + 15) / 16)));
   // eight waves where two stages of each fit
   constexpr int W1 = MT == 2 && DT != kF32 ? 8 : W;
   if (a.wide != a.N)

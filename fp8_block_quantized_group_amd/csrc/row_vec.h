@@ -12,6 +12,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "grid_map.h"
 
 namespace moe {
 
@@ -187,14 +188,6 @@ struct RowOne {
   }
 };
 
-// Grids in two dimensions: a dimension holds fewer than 2^32 lanes, 2^22
-// blocks of 1024.  A kernel compares its block's index (at most 2^31 blocks,
-// rounded up to rows of the grid) with what there is.
-constexpr int64_t kGridX = 1 << 20;
-inline dim3 grid_of(int64_t blocks) {
-  return dim3((unsigned)(blocks < kGridX ? blocks : kGridX),
-              (unsigned)((blocks + kGridX - 1) / kGridX));
-}
 __device__ __forceinline__ uint32_t block_index() {
   return blockIdx.y * (uint32_t)kGridX + blockIdx.x;
 }
