@@ -39,6 +39,16 @@ __host__ __device__ inline ExpertTile expert_tile_of_block(int64_t b, int64_t pe
   return e < experts && t < per ? ExpertTile{(int)e, t} : ExpertTile{-1, 0};
 }
 
+// Tiles of `tile` rows (at most 256) that n rows take; n + 255 passes 31 bits, not 32.
+__host__ __device__ constexpr int row_tiles(int n, int tile) {
+  return (int)(((unsigned)n + (unsigned)tile - 1) / (unsigned)tile);
+}
+// ... that rows sorted by expert can have at most
+constexpr int64_t most_row_tiles(int tile, bool sorted, int rows, int experts) {
+  return sorted ? (int64_t)(rows / tile) + (experts < rows ? experts : rows)
+                : (int64_t)row_tiles(rows, tile);
+}
+
 // Tile t of mts x nts, walked in bands of 8 rows of tiles, down each band first.
 struct TileAt {
   int m, n;

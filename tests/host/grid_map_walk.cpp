@@ -1,6 +1,7 @@
 // Walks every block of a launch, up to the last one of the rounded-up grid, and counts
 // the tiles that the blocks take.  Arguments: "experts" per E, or "tiles" launched live.
-// Prints one line: "ok", or the first block that goes wrong.
+// Prints one line: "ok", or the first block that goes wrong.  "rows" rows tile prints the
+// tiles of so many rows, of one expert and at most of 1024.
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -10,6 +11,13 @@
 
 int main(int argc, char** argv) {
   if (argc != 4) return 2;
+  if (std::strcmp(argv[1], "rows") == 0) {
+    const int rows = std::atoi(argv[2]), tile = std::atoi(argv[3]);
+    std::printf("%d %lld %lld\n", moe::row_tiles(rows, tile),
+                (long long)moe::most_row_tiles(tile, false, rows, 1),
+                (long long)moe::most_row_tiles(tile, true, rows, 1024));
+    return 0;
+  }
   const bool experts = std::strcmp(argv[1], "experts") == 0;
   const int64_t per = std::atoll(argv[2]), second = std::atoll(argv[3]);
   const int64_t tiles = experts ? per * second : second;

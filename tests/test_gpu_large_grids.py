@@ -101,3 +101,37 @@ def test_norm_that_leaves_staged():
     for rows in (slice(0, tail), slice(T - tail, T)):
         a, b = run(x[rows])
         assert torch.equal(q[rows], a) and torch.equal(sf[rows], b)
+
+
+def test_as_many_rows_as_32_bits_hold():
+    """Rows and a tile less one are more than 31 bits."""
+    R = (1 << 31) - 1
+    x = torch.empty((R, 1), dtype=torch.bfloat16, device="cuda")
+    for a in range(0, R, 1 << 28):
+        x[a:a + (1 << 28)].normal_()
+    w = torch.full((1, 1, 1), 2.0, dtype=torch.bfloat16, device="cuda")
+    out = marked((R + 300, 1), torch.bfloat16)
+    moe.expert_linear(moe.ExpertLinear(R, 1, 1), x, w, out[:R])
+    assert untouched(out[R:])
+    for a in range(0, R, 1 << 28):
+        b = min(R, a + (1 << 28))
+        assert torch.equal(out[a:b], 2.0 * x[a:b])
+
+
+def test_offsets_whose_tiles_pass_32_bits():
+    """512 of 1024 experts with all rows each, 2^32 + 1536 tiles of 128: nothing around
+    the rows is written."""
+    R, E = (1 << 30) + 384, 1024
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[1::2] = R
+    off = off.cuda()
+    x = torch.ones((R, 1), device="cuda")
+    w = torch.ones((E, 1, 1), device="cuda")
+    room = marked((R + 600, 1), torch.float32)
+    p = moe.ExpertLinear(R, 1, 1, E, dtype=torch.float32)
+    moe.expert_linear(p, x, w, room[300:R + 300], expert_offsets=off)
+    torch.cuda.synchronize()
+    assert untouched(room[:300]) and untouched(room[R + 300:])
+    moe.expert_linear_backward(p, None, w, x, room[300:R + 300], expert_offsets=off)
+    torch.cuda.synchronize()
+    assert untouched(room[:300]) and untouched(room[R + 300:])

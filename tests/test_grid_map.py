@@ -19,9 +19,9 @@ def walk(tmp_path_factory):
                     os.path.join(ROCM, "include"),
                     os.path.join(HERE, "host", "grid_map_walk.cpp"), "-o", exe], check=True)
 
-    def run(*args):
+    def run(*args, want="ok\n"):
         r = subprocess.run([exe, *map(str, args)], capture_output=True, text=True, timeout=60)
-        assert r.returncode == 0 and r.stdout == "ok\n", (args, r.stdout, r.stderr)
+        assert r.returncode == 0 and r.stdout == want, (args, r.stdout, r.stderr)
     return run
 
 
@@ -42,3 +42,11 @@ def test_tiles_of_every_expert(walk, per, E):
 def test_tiles_of_sorted_rows(walk, launched, live):
     """live of them on the device, where the host launched for the most there can be."""
     walk("tiles", launched, live)
+
+
+@pytest.mark.parametrize("tile", [16, 64, 256])
+@pytest.mark.parametrize("rows", [1, 15, 16, 17, 256, 257, (1 << 31) - 256, (1 << 31) - 255,
+                                  (1 << 31) - 1])
+def test_tiles_of_rows(walk, rows, tile):
+    one = -(-rows // tile)
+    walk("rows", rows, tile, want=f"{one} {one} {rows // tile + min(rows, 1024)}\n")
