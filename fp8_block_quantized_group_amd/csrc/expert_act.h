@@ -14,14 +14,28 @@ __device__ __forceinline__ float sigmoid_f32(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __expf(-x));
 }
 
+// Activations whose clamps (fminf, fmaxf) would make a number of a NaN.
+__device__ __forceinline__ bool act_clamps(int kind, float limit) {
+  return kind == kActRelu2NoMul || kind == kActSwigluOai || kind == kActSwigluStep ||
+         (kind == kActSilu && limit > 0.0f);
+}
+// apply_act for callers' own rows: NaN in the gate or up column gives NaN, so that a row
+// that went wrong shows.  kind and limit are uniform: a scalar branch where none clamps.
+__device__ __forceinline__ float expert_act(int kind, float g, float u, float limit) {
+  const float f = apply_act(kind, g, u, limit);
+  return act_clamps(kind, limit) && __builtin_isunordered(g, u) ? g + u : f;
+}
+
 struct ActGrad {
   float gate, up;      // of the gate column (or the only one) and of the up column
 };
 
-// The gradient of apply_act at (g, u) for the output's gradient dh, in fp32.
+// The gradient of expert_act at (g, u) for the output's gradient dh, in fp32.
 // With f(x) = x s(x), s a sigmoid of slope a at 0 times 4: f' = s + a f (1 - s).
-// A clamped value passes its gradient up to and at the limit, none past it.
+// A clamped value passes its gradient up to and at the limit, none past it.  NaN gives
+// NaN, at a clamp too.
 __device__ __forceinline__ ActGrad act_grad(int kind, float g, float u, float limit, float dh) {
+  if (act_clamps(kind, limit) && __builtin_isunordered(g, u)) return ActGrad{g + u, g + u};
   switch (kind) {
     case kActNone:
       return ActGrad{dh, 0.0f};

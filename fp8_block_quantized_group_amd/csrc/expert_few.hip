@@ -165,7 +165,7 @@ __global__ __launch_bounds__(64 * kWaves) void expert_few_kernel(const ExpertGem
       RowVec<DT>::store_one(p.pre, row * p.wide + n0 + c, a);
       if (GATED) RowVec<DT>::store_one(p.pre, row * p.wide + p.N + n0 + c, u);
     }
-    const float f = p.act == kActNone ? a : apply_act(p.act, a, u, p.limit);
+    const float f = p.act == kActNone ? a : expert_act(p.act, a, u, p.limit);
     RowVec<DT>::store_one(p.out, row * p.N + n0 + c, f);
   }
 }

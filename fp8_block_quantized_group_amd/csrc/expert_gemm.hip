@@ -451,7 +451,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_EU) void expert_gemm_kerne
       }
       if (P == kOut && p.act != kActNone) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) g[c] = apply_act(p.act, g[c], u[c], p.limit);
+        for (int c = 0; c < 8; ++c) g[c] = expert_act(p.act, g[c], u[c], p.limit);
       }
       if (P != kOut && p.split > 1) {          // a part's sums, unrounded
         float* part = p.part + (int64_t)blockIdx.z * p.part_size +

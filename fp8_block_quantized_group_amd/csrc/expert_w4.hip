@@ -178,7 +178,7 @@ __device__ __forceinline__ void store_tile(const ExpertW4Args& p, const float* f
     };
     const float a = total(c / 16, c % 16);
     const float u = gated ? total(NT / 2 + c / 16, c % 16) : 0.0f;
-    const float f = p.act == kActNone ? a : apply_act(p.act, a, u, p.limit);
+    const float f = p.act == kActNone ? a : expert_act(p.act, a, u, p.limit);
     RowVec<DT>::store_one(p.out, (row0 + r) * p.N + n0 + c, f);
   }
 }
@@ -620,7 +620,7 @@ __global__ __launch_bounds__(64 * W, 4) void expert_w4_few_kernel(
       if (GATED) h += flat[w * NT * 256 + 256 + at];
     }
     if (r16 < rows && tile * 16 + c < p.N) {
-      if (p.act != kActNone) f = apply_act(p.act, f, h, p.limit);
+      if (p.act != kActNone) f = expert_act(p.act, f, h, p.limit);
       RowVec<DT>::store_one(p.out, (row0 + r16) * p.N + tile * 16 + c, f);
     }
   }

@@ -716,7 +716,8 @@ typedef struct {
  * before that rounding).  expert_offsets int32 [E+1], ascending from 0 (what
  * is not, is cut to [0, R]; such calls give wrong rows, never an access out
  * of bounds), or NULL with one expert: it has all rows.  Rows from
- * expert_offsets[E] on stay as they were. */
+ * expert_offsets[E] on stay as they were.  A NaN in a row makes the row's
+ * results NaN, whatever F is; an infinity makes infinities or NaN before F. */
 moe_status_t moe_expert_linear(const moe_expert_linear_t* p, const void* x,
                                const int32_t* expert_offsets, const void* weight, void* out,
                                void* pre_act, void* stream);
@@ -732,7 +733,8 @@ moe_status_t moe_expert_linear_workspace_size(const moe_expert_linear_t* p, size
  *   grad_x[r, :]    = d[r, :] W_e                     [R, in]
  *   grad_weight[e]  = sum over e's rows of d[r, :]^T x[r, :]   [E, wide, in]
  * Either may be NULL.  Experts without rows get a grad_weight of zeros, also
- * with R = 0.  A clamp passes its gradient up to and at the limit.  pre_act
+ * with R = 0.  A clamp passes its gradient up to and at the limit, and a NaN
+ * in pre_act on to the gradients.  pre_act
  * must be NULL exactly when there is no activation; x is needed for
  * grad_weight, weight for grad_x.  ws: device scratch of
  * moe_expert_linear_workspace_size bytes, 16-byte aligned (NULL when that is
@@ -772,9 +774,10 @@ typedef struct {
  * alone, zeros uint8 of the scales' shape (any value counts as it is).  The
  * weights are used as the exact products of scale and code; sums are fp32.
  * Made for decode batches: every 64 rows of an expert (32 of fp32) read its
- * weights once.  A row with an infinity or a NaN gives infinities or NaN, and
- * so may a bf16 row where a group's sum of 384 |x| passes fp32's range (codes
- * are multiplied as 128 + q and the zero is taken off the sum). */
+ * weights once.  A row with a NaN gives NaN, one with an infinity
+ * infinities or NaN before F, and so may a bf16 row where a group's sum of
+ * 384 |x| passes fp32's range (codes are multiplied as 128 + q and the zero is
+ * taken off the sum). */
 moe_status_t moe_expert_linear_w4(const moe_expert_linear_w4_t* p, const void* x,
                                   const int32_t* expert_offsets, const void* codes,
                                   const void* scales, const void* zeros, void* out,

@@ -1,0 +1,102 @@
+"""NaN, infinities and the far ends of the types through the experts' own products: a
+row that went wrong shows, whatever the activation, and the others stay as they were."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_block_quantized_group_amd as moe
+from expert_util import marked, rand
+from oracle import expert_oracle as X
+
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.bfloat16, torch.float16, torch.float32]
+NAN = float("nan")
+ACTS = [("none", 0.0)] + [(a, 0.0) for a in X.GATED + X.SINGLE] + [
+    ("silu", 1.0), ("swigluoai", 0.75), ("swiglustep", 0.5)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    moe.load_library()
+
+
+def check_rows(clean, got, bad):
+    rest = [r for r in range(clean.shape[0]) if r not in bad]
+    assert got[bad].isnan().all()
+    assert torch.equal(got[rest], clean[rest])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("act,limit", ACTS)
+@pytest.mark.parametrize("R,K,N", [(5, 72, 40), (150, 65, 33), (300, 128, 264)])
+def test_linear(R, K, N, act, limit, dtype):
+    rng = np.random.default_rng(R)
+    p = moe.ExpertLinear(R, K, N, dtype=dtype, activation=act, act_limit=limit)
+    x, w = rand(rng, (R, K), dtype).cuda(), rand(rng, (1, p.wide, K), dtype, K ** -0.5).cuda()
+
+    def run():
+        out, pre = marked((R, N), dtype), marked((R, p.wide), dtype)
+        moe.expert_linear(p, x, w, out, pre_act=pre)
+        return out, pre
+
+    clean = run()
+    bad = [1, R - 1]
+    x[bad, [3, K - 1]] = NAN
+    for a, b in zip(clean, run()):
+        check_rows(a, b, bad)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("act,limit", ACTS[1:])
+def test_linear_gradients(act, limit, dtype):
+    """NaN in a gate or an only column, and in an up column, of pre_act; in grad_out.
+    grad_weight: the column's own rows of it (of the up column at a clamp)."""
+    rng, R, K, N = np.random.default_rng(3), 20, 72, 40
+    p = moe.ExpertLinear(R, K, N, dtype=dtype, activation=act, act_limit=limit)
+    x, w = rand(rng, (R, K), dtype).cuda(), rand(rng, (1, p.wide, K), dtype, K ** -0.5).cuda()
+    gout, pre = rand(rng, (R, N), dtype).cuda(), rand(rng, (R, p.wide), dtype, 0.2).cuda()
+
+    def run(gout, pre):
+        gx, gw = marked((R, K), dtype), marked(w.shape, dtype)
+        moe.expert_linear_backward(p, x, w, gout, gx, gw, pre_act=pre)
+        return gx, gw[0]
+
+    clean = run(gout, pre)
+    for col in (7,) if p.wide == N else (7, N + 7):
+        bad = pre.clone()
+        bad[4, col] = NAN
+        gx, gw = run(gout, bad)
+        check_rows(clean[0], gx, [4])
+        rest = [c for c in range(p.wide) if c % N != 7]
+        assert gw[7].isnan().all() and torch.equal(gw[rest], clean[1][rest])
+    bad = gout.clone()
+    bad[4, 7] = NAN
+    check_rows(clean[0], run(bad, pre)[0], [4])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("act,limit", ACTS)
+@pytest.mark.parametrize("R,K,form,group", [(5, 256, "int4", 64), (40, 512, "int4_zero", 128),
+                                            (9, 96, "int4", 32), (20, 256, "mxfp4", 32)])
+def test_4_bit_weights(R, K, form, group, act, limit, dtype):
+    rng, N = np.random.default_rng(R), 40
+    p = moe.ExpertLinearW4(R, K, N, dtype=dtype, activation=act, act_limit=limit, format=form,
+                           group_size=group)
+    codes = torch.from_numpy(rng.integers(0, 256, (1, p.wide, K // 2), dtype=np.uint8)).cuda()
+    groups = (1, p.wide, K // group)
+    scales = (torch.full(groups, 124, dtype=torch.uint8) if form == "mxfp4" else
+              rand(rng, groups, dtype, 0.1)).cuda()
+    zeros = torch.full(groups, 7, dtype=torch.uint8).cuda() if form == "int4_zero" else None
+    x = rand(rng, (R, K), dtype).cuda()
+
+    def run():
+        out = marked((R, N), dtype)
+        moe.expert_linear_w4(p, x, codes, scales, out, zeros=zeros)
+        return out
+
+    clean = run()
+    bad = [1, R - 1]
+    x[bad, [3, K - 1]] = NAN
+    check_rows(clean, run(), bad)
