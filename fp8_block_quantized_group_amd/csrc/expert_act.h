@@ -26,6 +26,12 @@ __device__ __forceinline__ float expert_act(int kind, float g, float u, float li
   return act_clamps(kind, limit) && __builtin_isunordered(g, u) ? g + u : f;
 }
 
+// Past kFar a sigmoid is 0 or 1 in fp32 and its slope 0.  What multiplies that 0 is taken
+// from kFar: an infinity, or a square that passes fp32's range, would make it NaN.
+constexpr float kFar = 256.0f;
+__device__ __forceinline__ float from_below(float g) { return g < -kFar ? -kFar : g; }
+__device__ __forceinline__ float near_zero(float g) { return g > kFar ? kFar : from_below(g); }
+
 struct ActGrad {
   float gate, up;      // of the gate column (or the only one) and of the up column
 };
@@ -41,32 +47,33 @@ __device__ __forceinline__ ActGrad act_grad(int kind, float g, float u, float li
       return ActGrad{dh, 0.0f};
     case kActSwigluOai: {
       const float gc = fminf(g, limit), uc = fminf(fmaxf(u, -limit), limit);
-      const float s = sigmoid_f32(kSwigluOaiAlpha * gc), f = gc * s;
-      const float df = s + kSwigluOaiAlpha * f * (1.0f - s);
+      const float s = sigmoid_f32(kSwigluOaiAlpha * gc), f = from_below(gc) * s;
+      const float df = s + kSwigluOaiAlpha * near_zero(gc) * s * (1.0f - s);
       return ActGrad{g <= limit ? dh * (uc + 1.0f) * df : 0.0f,
                      fabsf(u) <= limit ? dh * f : 0.0f};
     }
     case kActSwigluStep: {
       const float uc = fminf(fmaxf(u, -limit), limit);
-      const float s = sigmoid_f32(g), f = g * s;
-      return ActGrad{f <= limit ? dh * uc * (s + f * (1.0f - s)) : 0.0f,
+      const float s = sigmoid_f32(g), f = from_below(g) * s;
+      return ActGrad{f <= limit ? dh * uc * (s + near_zero(g) * s * (1.0f - s)) : 0.0f,
                      fabsf(u) <= limit ? dh * fminf(f, limit) : 0.0f};
     }
     case kActGelu:
     case kActGeluNoMul: {
-      const float phi = 0.5f * erfcf(-g * 0.70710678118654752f);
-      const float df = phi + g * 0.39894228040143268f * __expf(-0.5f * g * g);
-      return kind == kActGelu ? ActGrad{dh * u * df, dh * g * phi} : ActGrad{dh * df, 0.0f};
+      const float phi = 0.5f * erfcf(-g * 0.70710678118654752f), x = near_zero(g);
+      const float df = phi + x * 0.39894228040143268f * __expf(-0.5f * x * x);
+      return kind == kActGelu ? ActGrad{dh * u * df, dh * from_below(g) * phi}
+                              : ActGrad{dh * df, 0.0f};
     }
     case kActGeluTanh:
     case kActGeluTanhNoMul: {
       // (1 + tanh y) / 2 = sigmoid(2y); d(2y)/dg = 2 sqrt(2/pi) (1 + 3 * 0.044715 g^2)
-      const float g2 = g * g;
-      const float s = sigmoid_f32(1.5957691216057308f * (g + 0.044715f * g2 * g));
-      const float f = g * s;
+      const float x = near_zero(g), x2 = x * x;
+      const float s = sigmoid_f32(1.5957691216057308f * (x + 0.044715f * x2 * x));
       const float df =
-          s + f * (1.0f - s) * (1.5957691216057308f * (1.0f + 0.134145f * g2));
-      return kind == kActGeluTanh ? ActGrad{dh * u * df, dh * f} : ActGrad{dh * df, 0.0f};
+          s + x * s * (1.0f - s) * (1.5957691216057308f * (1.0f + 0.134145f * x2));
+      return kind == kActGeluTanh ? ActGrad{dh * u * df, dh * (from_below(g) * s)}
+                                  : ActGrad{dh * df, 0.0f};
     }
     case kActRelu2NoMul:
       return ActGrad{dh * 2.0f * fmaxf(g, 0.0f), 0.0f};
@@ -74,8 +81,8 @@ __device__ __forceinline__ ActGrad act_grad(int kind, float g, float u, float li
       const bool gated = kind == kActSilu, clamped = gated && limit > 0.0f;
       const float gc = clamped ? fminf(g, limit) : g;
       const float uc = clamped ? fminf(fmaxf(u, -limit), limit) : u;
-      const float s = sigmoid_f32(gc), f = gc * s;
-      const float df = s + f * (1.0f - s);
+      const float s = sigmoid_f32(gc), f = from_below(gc) * s;
+      const float df = s + near_zero(gc) * s * (1.0f - s);
       if (!gated) return ActGrad{dh * df, 0.0f};
       return ActGrad{clamped && g > limit ? 0.0f : dh * uc * df,
                      clamped && fabsf(u) > limit ? 0.0f : dh * f};

@@ -100,3 +100,37 @@ def test_4_bit_weights(R, K, form, group, act, limit, dtype):
     bad = [1, R - 1]
     x[bad, [3, K - 1]] = NAN
     check_rows(clean, run(), bad)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("act,limit", ACTS[1:])
+def test_gradients_of_large_pre_activations(act, limit, dtype):
+    """One row and one column per expert, x = 1: grad_weight is d.  The roundings are the
+    oracle's at 20; from 100 on a sigmoid and its slope are 0 or 1, in 64 bits to 1e-40 and
+    in 32 exactly, so that nothing rounds with the argument.  An infinity has the slopes
+    and, below, the value of the largest numbers."""
+    top = torch.finfo(dtype).max
+    far = [v for v in (20.0, 100.0, 300.0, 1e4, 1e19, 1e20, 1e30) if v < top] + [top]
+    at = [s * v for v in far + [float("inf")] for s in (1, -1)]
+    E, gated = len(at), act in X.GATED
+    dh, up = 0.5, 0.5
+    p = moe.ExpertLinear(E, 1, 1, E, dtype=dtype, activation=act, act_limit=limit)
+    pre = torch.tensor([[g, up][:p.wide] for g in at], dtype=dtype)
+    ones = torch.ones((E, 1), dtype=dtype, device="cuda")
+    gw = marked((E, p.wide, 1), dtype)
+    moe.expert_linear_backward(p, ones, None, ones * dh, None, gw, pre_act=pre.cuda(),
+                               expert_offsets=torch.arange(E + 1, dtype=torch.int32).cuda())
+    got = gw[:, :, 0].cpu().double().numpy()
+    pre = pre.double().numpy()
+    g = np.clip(pre[:, :1], -1e38, 1e38)       # the slopes of infinities
+    f, dg, du = X.activate(act, np.concatenate([g, pre[:, 1:]], 1), limit)
+    if act == "relu2_no_mul":
+        dg = 2.0 * np.maximum(pre, 0.0)
+    want = np.concatenate([dg, du], 1) * dh if gated else dg * dh
+    if gated and limit == 0.0 and act in ("silu", "gelu", "gelu_tanh"):
+        want[:, 1:] = np.where(pre[:, :1] > 0, pre[:, :1] * dh, want[:, 1:])
+    fine = np.isfinite(want)
+    assert np.array_equal(got[~fine], want[~fine])
+    rel = X.act_rel(20.0) + 3.0 * torch.finfo(dtype).eps / 2     # d, the product, 1 + X
+    tiny = float(torch.finfo(dtype).smallest_normal)
+    assert (np.abs(got - want)[fine] <= rel * np.abs(want[fine]) * 1.01 + tiny).all(), (got, want)
