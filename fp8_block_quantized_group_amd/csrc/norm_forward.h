@@ -142,7 +142,8 @@ __device__ __forceinline__ float row_inv_rms(F&& value, int H, float eps, float 
 // crosses the lanes that share it (16 of 8 columns or 32 of 4, MX 4 or 8), each
 // lane stores its codes and the first one the scale.  Rows are whole groups, so
 // lanes past the row's end share none with others.  The quantizer is the
-// staging's own; what it quantizes has not been rounded to 16 bits first.
+// staging's own; what it quantizes has not been rounded to 16 bits first, and NaN
+// leaves as NaN (the converter's clamp makes -448 of it).
 template <int N>
 __device__ __forceinline__ void quantize_vector(const NormArgs& a, const float (&h)[N],
                                                 int64_t row, int col) {
@@ -165,6 +166,14 @@ __device__ __forceinline__ void quantize_vector(const NormArgs& a, const float (
   for (int c = 0; c < N / 4; ++c)
     code[c] = f32x4_to_e4m3x4(h[4 * c] * s.recip, h[4 * c + 1] * s.recip, h[4 * c + 2] * s.recip,
                               h[4 * c + 3] * s.recip);
+  bool nan = false;
+#pragma unroll
+  for (int c = 0; c < N; ++c) nan |= __builtin_isnan(h[c] * s.recip);
+  if (nan) {
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      if (__builtin_isnan(h[c] * s.recip)) code[c / 4] |= 0x7Fu << (8 * (c & 3));
+  }
   if constexpr (N == 8) *reinterpret_cast<uint2*>(q) = make_uint2(code[0], code[1]);
   else *reinterpret_cast<uint32_t*>(q) = code[0];
   const int group = mx ? 32 : 128, in = col % group;

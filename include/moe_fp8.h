@@ -654,6 +654,7 @@ moe_status_t moe_block_norm(const moe_block_norm_t* p, const void* residual, con
  * x_q [T, hidden] and x_sf in the layout of moe_stage (16- and 4-byte
  * aligned), by its quantizer, from the normed values before they are rounded
  * (staging the stored normed rounds twice; its codes may differ by a step).
+ * NaN leaves as a NaN code (moe_stage's quantizer makes -448 of it).
  * normed may be NULL with or without y.  hidden must be a multiple of 128. */
 moe_status_t moe_block_norm_quant(const moe_block_norm_t* p, int32_t act_quant,
                                   const void* residual, const void* y, const void* post_weight,

@@ -134,3 +134,29 @@ def test_gradients_of_large_pre_activations(act, limit, dtype):
     rel = X.act_rel(20.0) + 3.0 * torch.finfo(dtype).eps / 2     # d, the product, 1 + X
     tiny = float(torch.finfo(dtype).smallest_normal)
     assert (np.abs(got - want)[fine] <= rel * np.abs(want[fine]) * 1.01 + tiny).all(), (got, want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("quant", ["ue8m0", "fp32", "mxfp8"])
+@pytest.mark.parametrize("T,H", [(9, 512), (600, 128), (40, 7168), (600, 5120)])
+def test_norm_that_leaves_staged(T, H, quant, dtype):
+    """A row with a NaN has NaN codes alone, one with an infinity where it was; the e4m3
+    NaN is 0x7F with either sign."""
+    x = rand(np.random.default_rng(H), (T, H), dtype)
+    p = moe.BlockNorm(T, H, dtype=dtype)
+
+    def run():
+        o = moe.alloc_quant_outputs(p, quant)
+        o["x_q"].fill_(0x5A)
+        moe.block_norm_quant(p, x.cuda(), quant=quant, **o)
+        return o["x_q"], o["x_sf"]
+
+    q, sf = run()
+    x[1, 7] = NAN
+    x[4, 100] = float("inf")
+    got, gsf = run()
+    rest = [r for r in range(T) if r not in (1, 4)]
+    assert torch.equal(got[rest], q[rest]) and torch.equal(gsf[rest], sf[rest])
+    nan = (got & 0x7F) == 0x7F
+    assert nan[1].all() and nan[4].nonzero().flatten().tolist() == [100]
+    assert not nan[rest].any()
