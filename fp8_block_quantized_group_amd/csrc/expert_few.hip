@@ -9,7 +9,7 @@
 // 64 accesses of 16 bytes are what such a load then takes).  No barrier is needed
 // until the end.  x is the MFMA's A operand, the weights its B operand.
 //
-// 256 rows of 64 experts, 4096 by 2 x 1024, bf16 with silu: 166 us, 6.5 TB/s of weights;
+// 256 rows of 64 experts, 4096 by 2 x 1024, bf16 with silu: 166-172 us, 6.3-6.5 TB/s;
 // one row x 7168 by 2 x 2048 10.9 us, 59 MB at 5.4 TB/s (62 with the tiles of batches).
 #include "expert_act.h"
 #include "expert_rows.h"

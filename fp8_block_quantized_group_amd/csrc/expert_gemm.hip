@@ -21,11 +21,13 @@
 // transposed by ds_read_b64_tr_b16 (fp32: word by word).  Every product of the
 // 16-bit types is exact and sums are fp32; fp32 goes through the fp32 MFMA.
 //
-// A batch's product is bound by the MFMAs under the card's power: 32768 rows of 32
-// experts, 7168 by 2 x 2048, bf16 with silu and the pre-activations kept, 1.9 ms (0.96
-// PFLOP/s; a library's dense product of that size 1.3 ms), the MFMAs busy 55 % of the
-// time at 2.0 GHz.  Register double buffers, wave pairs in turns and more waves in
-// smaller tiles gave nothing.  Products of few rows are bound by the weights' bytes.
+// A batch's product waits for its tiles: 32768 rows of 32 experts, 7168 by 2 x 2048, bf16
+// with silu and the pre-activations kept, 1.9 ms (0.94 PFLOP/s; a library's dense product
+// of that size 1.3 ms), the MFMAs busy 45 % of the cycles at 2.1 GHz, the waves 37 % of
+// theirs at waits and barriers.  The ring holds two stages of 64 KB, so a step's barrier
+// waits for loads that were issued behind the one before.  Register double buffers, wave
+// pairs in turns and more waves in smaller tiles gave nothing.  Products of few rows are
+// bound by the weights' bytes.
 #include <algorithm>
 #include <type_traits>
 

@@ -730,16 +730,16 @@ moe_status_t moe_expert_linear(const moe_expert_linear_t* p, const void* x,
 moe_status_t moe_expert_linear_workspace_size(const moe_expert_linear_t* p, size_t* bytes);
 
 /* With d = grad_out F'(pre_act), rounded to dtype (grad_out itself without an
- * activation; the products take their operands in that type):
+ * activation; the products take their operands in that type: in fp16 a d past
+ * 65504 is an infinity, as a gradient stored in fp16 would be):
  *   grad_x[r, :]    = d[r, :] W_e                     [R, in]
  *   grad_weight[e]  = sum over e's rows of d[r, :]^T x[r, :]   [E, wide, in]
  * Either may be NULL.  Experts without rows get a grad_weight of zeros, also
- * with R = 0.  A clamp passes its gradient up to and at the limit, and a NaN
- * in pre_act on to the gradients.  pre_act
- * must be NULL exactly when there is no activation; x is needed for
- * grad_weight, weight for grad_x.  ws: device scratch of
- * moe_expert_linear_workspace_size bytes, 16-byte aligned (NULL when that is
- * 0); calls sharing one must not overlap. */
+ * with R = 0.  A clamp passes its gradient up to and at the limit; a NaN in
+ * pre_act makes its row's gradients NaN.  pre_act must be NULL exactly when
+ * there is no activation; x is needed for grad_weight, weight for grad_x.
+ * ws: device scratch of moe_expert_linear_workspace_size bytes, 16-byte
+ * aligned (NULL when that is 0); calls sharing one must not overlap. */
 moe_status_t moe_expert_linear_backward(const moe_expert_linear_t* p, const void* x,
                                         const int32_t* expert_offsets, const void* weight,
                                         const void* pre_act, const void* grad_out, void* grad_x,
@@ -774,8 +774,11 @@ typedef struct {
  * [E, wide, in / 2], scales [E, wide, in / group_size] and, MOE_W4_INT4_ZERO
  * alone, zeros uint8 of the scales' shape (any value counts as it is).  The
  * weights are used as the exact products of scale and code; sums are fp32.
- * Made for decode batches: every 64 rows of an expert (32 of fp32) read its
- * weights once.  A row with a NaN gives NaN, one with an infinity
+ * Made for decode batches: an expert's weights are read and converted once for
+ * every tile of its rows, of 16 rows where the experts have up to 16 on average
+ * (num_rows / num_experts), of up to 64 (fp32: 32) where they have more, and
+ * always of 16 where in_features is not a multiple of 128, x or codes are not
+ * 16-byte aligned, or scales, zeros or a row of either not whole 4 bytes.  A row with a NaN gives NaN, one with an infinity
  * infinities or NaN before F, and so may a bf16 row where a group's sum of
  * 384 |x| passes fp32's range (codes are multiplied as 128 + q and the zero is
  * taken off the sum). */
