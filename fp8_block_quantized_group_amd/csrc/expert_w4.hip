@@ -16,8 +16,8 @@
 // stays in registers where it fits and is streamed beside them where it does not
 // (launch_rows has the sizes and their times).  512 rows of 128 experts, 4096
 // by 2 x 2048, MXFP4: 184 us, 1147 MB of codes and scales at 6.2 TB/s.  One row x
-// 7168 by 4096: 6.9 us, of which x's rows of zeros beside the one are four of every six
-// loads.  Past 16 rows of an expert the conversion of the codes, once for every tile of
+// 7168 by 4096: 6.9 us; four of every six loads are of x's 16 rows, of which one is
+// there.  Past 16 rows of an expert the conversion of the codes, once for every tile of
 // up to 64 rows, and x's way through the ring bound it: 37 rows x 14336 by 4096, 33 MB,
 // 27.6 us; 4096 rows x 4096 by 4096 750 us.  fp32 rows, 512 of 128 experts as above, 830
 // us.  Columns or pointers that lines do not fit take the simple kernel, which loads from

@@ -778,10 +778,10 @@ typedef struct {
  * every tile of its rows, of 16 rows where the experts have up to 16 on average
  * (num_rows / num_experts), of up to 64 (fp32: 32) where they have more, and
  * always of 16 where in_features is not a multiple of 128, x or codes are not
- * 16-byte aligned, or scales, zeros or a row of either not whole 4 bytes.  A row with a NaN gives NaN, one with an infinity
- * infinities or NaN before F, and so may a bf16 row where a group's sum of
- * 384 |x| passes fp32's range (codes are multiplied as 128 + q and the zero is
- * taken off the sum). */
+ * 16-byte aligned, or scales, zeros or a row of either not whole 4 bytes.  A
+ * row with a NaN gives NaN, one with an infinity infinities or NaN before F, and
+ * so may a bf16 row where a group's sum of 384 |x| passes fp32's range (codes
+ * are multiplied as 128 + q and the zero is taken off the sum). */
 moe_status_t moe_expert_linear_w4(const moe_expert_linear_w4_t* p, const void* x,
                                   const int32_t* expert_offsets, const void* codes,
                                   const void* scales, const void* zeros, void* out,
